@@ -243,6 +243,80 @@ kda_status kda_gated_rmsnorm(const void *o, const void *gate, const float *weigh
                              kda_stream_t stream);
 
 /*
+ * 8-bit activations. A token's channels leave in blocks of 128 (the last block
+ * may be short), each with one fp32 scale:
+ *
+ *   s = max(max_j |y_j|, 2^-96) / 448,   code_j = e4m3(y_j / s)
+ *
+ * (round to nearest even; 448 is the largest e4m3 value), so that y_j is about
+ * code_j * s. Codes are token-major like y, one byte each; scales are
+ * block-major, scales[b * T + t] for block b of token t, ceil(channels / 128)
+ * rows of T floats, which is the a_scales operand of kda_fp8_linear. A block of
+ * zeros gives zero codes. A NaN among the y_j gives a NaN code and leaves the
+ * rest of its block alone (a NaN in a norm's input reaches the norm's whole row);
+ * an infinite y_j makes its block's scale infinite.
+ */
+
+/*
+ * Residual addition, RMSNorm and 8-bit output in one pass, in front of a
+ * layer's projections ([G] section 6, the normalisation before each block;
+ * the form is the plain RMSNorm of kda_gated_rmsnorm without its gate):
+ *
+ *   h = x + residual            (h = x when residual is NULL)
+ *   y = h / sqrt(mean_j h_j^2 + eps) * weight,  stored as codes and scales
+ *
+ * A row whose mean square plus eps is exactly zero gives zeros. The norm takes
+ * the fp32 sum itself, not its rounding to res_dtype; |h| must stay below
+ * about 1e19, where the sum of squares passes fp32.
+ *   x [T,N] dtype; residual [T,N] res_dtype or NULL; weight [N] fp32
+ *   sum_out [T,N] res_dtype or NULL: receives h; it may be residual, or x
+ *     where dtype = res_dtype
+ *   y [T,N] e4m3 codes; scales [ceil(N/128),T] fp32; neither may alias
+ *     another argument
+ * Requires T >= 0 (0 is a no-op), N a multiple of 16 in 16..32768, eps >= 0.
+ */
+kda_status kda_add_rmsnorm_fp8(const void *x, const void *residual, const float *weight, void *sum_out,
+                               void *y, float *scales, int64_t T, int N, kda_dtype dtype,
+                               kda_dtype res_dtype, float eps, kda_stream_t stream);
+
+/*
+ * kda_gated_rmsnorm with its output stored as codes and scales, in front of
+ * the output projection: the norm runs over each (token, head) row of D
+ * channels as there, the scales' blocks over the token's H * D channels (one
+ * head per block at D = 128, 128 / D heads below). The activation of the gate
+ * uses the fast exponential and division.
+ *   o, gate [T,H,D] dtype; weight [D] fp32; y [T,H,D] e4m3 codes;
+ *   scales [ceil(H*D/128),T] fp32. y and scales may not alias another argument.
+ * Requires T >= 0 (0 is a no-op), H >= 1, D in {16,32,64,128}, eps >= 0.
+ */
+kda_status kda_gated_rmsnorm_fp8(const void *o, const void *gate, const float *weight, void *y, float *scales,
+                                 int64_t T, int H, int D, kda_dtype dtype, kda_gate_act act, float eps,
+                                 kda_stream_t stream);
+
+/*
+ * Product of 8-bit activations with an 8-bit weight, one scale per block of
+ * 128: the projections into a layer (q, k, v, gates) and out of it.
+ *
+ *   y[m,n] = sum_k a[m,k] a_scales[k/128, m] * w[n,k] w_scales[n/128, k/128]
+ *
+ *   a [M,K] e4m3, row stride lda; a_scales [ceil(K/128),M] fp32
+ *   w [N,K] e4m3, row stride ldw; w_scales [ceil(N/128),ceil(K/128)] fp32
+ *   y [M,N] out_dtype, row stride ldy (strides in elements); elements between
+ *     N and ldy keep their values. y may not alias another argument.
+ * e4m3 products are exact and are summed in fp32; the sums of the K blocks are
+ * scaled and joined in fp32, in an order that depends on the sizes alone: the
+ * same inputs give the same bits.
+ * Requires M >= 0 (0 is a no-op), N >= 1, K a positive multiple of 16, lda and
+ * ldw multiples of 16 that are >= K, ldy >= N. a and w are read by TMA
+ * tensor copies (KDA_ERR_CUDA if the driver's tensor-map encoder rejects
+ * them). A copy that does not land within about a second sets the device error
+ * word (KDA_ERR_TIMEOUT from the next kda_sync_status).
+ */
+kda_status kda_fp8_linear(const void *a, const float *a_scales, const void *w, const float *w_scales, void *y,
+                          int64_t M, int N, int K, int64_t lda, int64_t ldw, int64_t ldy, kda_dtype out_dtype,
+                          kda_stream_t stream);
+
+/*
  * Fused short conv + decode step with the output epilogue of
  * kda_gated_rmsnorm applied before the output is stored, in one launch ([W]
  * "KDA 递推公式先衰减再差分" for the step, [W] "相关源码与文档导航" and [G]

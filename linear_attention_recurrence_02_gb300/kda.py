@@ -78,6 +78,9 @@ _SIGNATURES = {
     "kda_chunk_prefill_noalloc": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _ci, _i64, _ci, _ci, _ci,
                                    _ci, _cf, _vp], _ci),
     "kda_gated_rmsnorm": ([_vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _ci, _cf, _vp], _ci),
+    "kda_add_rmsnorm_fp8": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _cf, _vp], _ci),
+    "kda_gated_rmsnorm_fp8": ([_vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _ci, _cf, _vp], _ci),
+    "kda_fp8_linear": ([_vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _i64, _i64, _i64, _ci, _vp], _ci),
     "kda_chunk_prefill_scan_workspace_bytes": ([_i64, _ci, _ci, _ci, _ci], _sz),
     "kda_chunk_prefill_split": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _ci, _i64, _ci, _ci, _ci, _ci,
                                  _ci, _cf, _vp, _sz, _vp], _ci),
@@ -290,6 +293,105 @@ def kda_gated_rmsnorm(o, gate, weight, y, act="sigmoid", eps=1e-6, stream=None):
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     _check(lib().kda_gated_rmsnorm(_ptr(o), _ptr(gate), _ptr(weight), _ptr(y), T, H, D, _dtype_code(o),
                                    _ACTS[act], float(eps), _stream(stream, o.device)))
+
+
+def _fp8_args(dev, codes, floats):
+    """Checks of the 8-bit operators: every tensor on device `dev`, e4m3 codes, fp32 scales and weights."""
+    import torch
+    for t in codes:
+        if t.dtype != torch.float8_e4m3fn:
+            raise TypeError("8-bit codes must be torch.float8_e4m3fn")
+        if t.device != dev:
+            raise ValueError("tensors must be on one CUDA device")
+    for t in floats:
+        if t.dtype != torch.float32:
+            raise TypeError("scales and norm weights must be float32")
+        if t.device != dev:
+            raise ValueError("tensors must be on one CUDA device")
+
+
+def _on_device(fn, stream, dev, *args):
+    """fn(*args, stream) on `stream`, or on the current stream of `dev` with that device current (the
+    handle of a default stream does not name its device)."""
+    import torch
+    if stream is None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        return
+    _check(fn(*args, _stream(stream, dev)))
+
+
+def _blocks128(n):
+    return (n + 127) // 128
+
+
+def kda_add_rmsnorm_fp8(x, weight, y, scales, residual=None, sum_out=None, eps=1e-6, stream=None):
+    """h = x + residual, then RMSNorm(h) * weight in 8 bits. x [T,N] fp32 or bf16; residual [T,N] fp32
+    or bf16, or None (h = x); weight [N] fp32; sum_out receives h (residual's shape and type; may be
+    residual, or x where the types agree), or None; y [T,N] float8_e4m3fn; scales [ceil(N/128),T] fp32
+    with y about code * scales[channel // 128, token]."""
+    T, N = x.shape
+    if weight.shape != (N,) or y.shape != (T, N) or scales.shape != (_blocks128(N), T) \
+            or (residual is not None and residual.shape != (T, N)) \
+            or (sum_out is not None and sum_out.shape != (T, N)):
+        raise ValueError("shape mismatch")
+    dev = x.device
+    _fp8_args(dev, (y,), (weight, scales))
+    code = res = _dtype_code(x)
+    for t in (residual, sum_out):
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must be on one CUDA device")
+    if residual is not None:
+        res = _dtype_code(residual)
+        if sum_out is not None and sum_out.dtype != residual.dtype:
+            raise TypeError("sum_out must have residual's dtype")
+    elif sum_out is not None:
+        res = _dtype_code(sum_out)
+    _on_device(lib().kda_add_rmsnorm_fp8, stream, dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(sum_out), _ptr(y),
+               _ptr(scales), T, N, code, res, float(eps))
+
+
+def kda_gated_rmsnorm_fp8(o, gate, weight, y, scales, act="sigmoid", eps=1e-6, stream=None):
+    """kda_gated_rmsnorm with its output in 8 bits. o, gate [T,H,D]; weight [D] fp32; y [T,H,D]
+    float8_e4m3fn; scales [ceil(H*D/128),T] fp32, one per token and 128 of its H * D channels."""
+    T, H, D = o.shape
+    if gate.shape != (T, H, D) or y.shape != (T, H, D) or weight.shape != (D,) \
+            or scales.shape != (_blocks128(H * D), T):
+        raise ValueError("shape mismatch")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    if gate.dtype != o.dtype or gate.device != o.device:
+        raise TypeError("gate must have o's dtype and device")
+    _fp8_args(o.device, (y,), (weight, scales))
+    _on_device(lib().kda_gated_rmsnorm_fp8, stream, o.device, _ptr(o), _ptr(gate), _ptr(weight), _ptr(y),
+               _ptr(scales), T, H, D, _dtype_code(o), _ACTS[act], float(eps))
+
+
+def _rows(t, n):
+    """(pointer, row stride in elements) of a matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("rows must be contiguous")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else n)
+
+
+def kda_fp8_linear(a, a_scales, w, w_scales, y, stream=None):
+    """y[m,n] = sum_k a[m,k] a_scales[k//128,m] * w[n,k] w_scales[n//128,k//128]. a [M,K], w [N,K]
+    float8_e4m3fn (rows contiguous, row strides multiples of 16); a_scales [ceil(K/128),M] and w_scales
+    [ceil(N/128),ceil(K/128)] fp32; y [M,N] bf16 or fp32 (rows contiguous)."""
+    M, K = a.shape
+    N = w.shape[0]
+    kb = _blocks128(K)
+    if w.shape[1] != K or y.shape != (M, N) or a_scales.shape != (kb, M) or w_scales.shape != (_blocks128(N), kb):
+        raise ValueError("shape mismatch")
+    dev = a.device
+    _fp8_args(dev, (a, w), (a_scales, w_scales))
+    if y.device != dev:
+        raise ValueError("tensors must be on one CUDA device")
+    (pa, lda), (pw, ldw), (py, ldy) = _rows(a, K), _rows(w, K), _rows(y, N)
+    _on_device(lib().kda_fp8_linear, stream, dev, pa, _ptr(a_scales), pw, _ptr(w_scales), py, M, N, K, lda, ldw,
+               ldy, _dtype_code(y))
 
 
 def kda_chunk_prefill_epi(q, k, v, g, beta, out, out_gate, norm_weight, gate="channel", act="sigmoid",
