@@ -9,6 +9,7 @@
 // so they are summed on the tensor cores (tcgen05 kind::f8f6f4, exact e4m3
 // products, fp32 accumulators in TMEM), and the K blocks' sums are joined
 // outside it: acc += (sa * sw) * block_sum in fp32 registers.
+#include <atomic>
 #include <string>
 
 #include "kda_common.cuh"
@@ -145,13 +146,15 @@ __global__ void __launch_bounds__(192) linear_few_kernel(const __grid_constant__
         float *srow = reinterpret_cast<float *>(sm + F::SBUF) + ew * 2 * NT;
         const float *swp = sw + (int64_t)nt * nkb;
         constexpr int L = NT < 32 ? 1 : NT / 32;
-        float sv[L];  // this lane's token scales of the coming K block
+        // this lane's scales of the coming K block, multiplied only where they are used: a product right
+        // behind its loads would wait for them
+        float sv[L], ws;
         auto fetch = [&](int kb) {
-            const float ws = __ldg(swp + kb);
+            ws = __ldg(swp + kb);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 const int j = lane + 32 * i;
-                sv[i] = j < NT && m0 + j < M ? ws * __ldg(sa + (int64_t)kb * M + m0 + j) : 0.f;
+                sv[i] = j < NT && m0 + j < M ? __ldg(sa + (int64_t)kb * M + m0 + j) : 0.f;
             }
         };
         fetch(0);
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(192) linear_few_kernel(const __grid_constant__
             float *sr = srow + (kb & 1) * NT;
 #pragma unroll
             for (int i = 0; i < L; ++i)
-                if (lane + 32 * i < NT) sr[lane + 32 * i] = sv[i];
+                if (lane + 32 * i < NT) sr[lane + 32 * i] = ws * sv[i];
             if (kb + 1 < nkb) fetch(kb + 1);
             __syncwarp();
             ok = mbar_wait(afull + as, (kb / F::AS) & 1, WAIT_LIMIT);
@@ -212,6 +215,400 @@ static kda_status launch_few(const CUtensorMap &tw, const CUtensorMap &ta, const
     return check_launch("linear_few_kernel");
 }
 
+// ---------------------------------------------------------------- many tokens
+// A pair of CTAs (one cluster, two SMs) owns a 256-token x 256-feature tile:
+// the MMAs of cta_group::2 take 128 token rows and half of the 256 weight rows
+// from each CTA's shared memory, so every operand byte is copied and read once
+// per pair. Each CTA's TMEM holds its 128 tokens (lane = token) in two
+// accumulators of 256 columns, one K block each: 512 cycles of MMAs, in which
+// the other accumulator has to be read and handed back. Per CTA: warps 0-7 join
+// the block sums (warps 0-3 the tile's first 128 features, 4-7 the last; a
+// thread holds 128 fp32 sums of one token, and one product of its token's scale
+// with the features' scale serves the whole K block), warp 8 copies, warp 9 of
+// the even CTA issues the MMAs for both, warps 10 and 11 form the scales'
+// products, four K blocks at a time. Persistent: a pair walks tiles, token
+// tiles first, so that neighbouring pairs share weight tiles in L2, and the next
+// tile's products run while this one's results are stored.
+namespace many {
+constexpr int BM = 256, BN = 256;                 // tile of a pair
+constexpr int A_BYTES = 128 * KB, W_BYTES = 128 * KB;
+constexpr int STAGE = A_BYTES + W_BYTES;          // bytes per CTA: tokens, then weights
+constexpr int ST = 6, AS = 2;
+constexpr int NTHREADS = 384;                     // three warpgroups
+// registers a thread: launched with REGS, split so that the joining warpgroups hold their sums
+constexpr int REGS = 168, REGS_JOIN = 208, REGS_ISSUE = 88;
+static_assert(2 * REGS_JOIN + REGS_ISSUE == 3 * REGS, "the split draws on the launch's registers");
+constexpr int CK = 4, CS = 4;                     // K blocks of scales per chunk, chunks in flight
+constexpr int CHUNK = CK * 256 * 4;               // [CK][feature half][token] products of the two scales
+constexpr int SCALES = ST * STAGE;
+constexpr int BARS = SCALES + CS * CHUNK;
+constexpr int SMEM = BARS + (2 * ST + 2 * AS + 2 * CS) * 8 + 16 + 1024;
+}  // namespace many
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// address in the cluster's shared window of this CTA's `p` in CTA `rank`
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Bounded wait that reads the clock only where the first try fails. The pair's
+// barriers guard TMEM (ordered by the tcgen05 fences) and copies (ordered by
+// the barrier's own transaction count) and no plain memory, so waits and
+// arrivals stay at their default scope: at cluster scope each one waited for
+// the warp's outstanding memory operations (a K block's hand-shakes alone took
+// 1700 cycles).
+__device__ __forceinline__ bool wait_fast(uint64_t *bar, uint32_t parity) {
+    return tc::mbar_try_wait(bar, parity) || tc::mbar_wait(bar, parity, WAIT_LIMIT);
+}
+__device__ __forceinline__ bool test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// one lane of a whole warp. An MMA issued under this predicate takes its
+// descriptors from uniform registers: 45 cycles an MMA, 62 under lane == 0.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(e));
+    return e != 0;
+}
+// copy into this CTA's shared memory, completing on a barrier of the pair's even CTA
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrive on `bar` of both CTAs when every MMA issued so far by this thread completes
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// (a0, a1) += (d0, d1) * (s, s) in one instruction
+__device__ __forceinline__ void fma2(uint64_t &a, uint32_t d0, uint32_t d1, uint64_t s) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(s));
+}
+
+template <typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
+    linear_many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                       const float *__restrict__ sa, const float *__restrict__ sw, TO *__restrict__ y, int M, int N,
+                       int nkb, int64_t ldy, unsigned mt, unsigned tiles, int vec, unsigned *err) {
+    using namespace tc;
+    using namespace many;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + BARS), *empty = full + ST, *afull = empty + ST,
+             *aempty = afull + AS, *sfull = aempty + AS, *sempty = sfull + CS;
+    uint32_t *s_taddr = reinterpret_cast<uint32_t *>(sempty + CS);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const unsigned pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full + i, 1);  // the even CTA's own arrival; both CTAs' bytes
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < AS; ++i) {
+            mbar_init(afull + i, 1);
+            mbar_init(aempty + i, 16);  // eight warps of each CTA
+        }
+        for (int i = 0; i < CS; ++i) {
+            mbar_init(sfull + i, 2);   // warps 10 and 11
+            mbar_init(sempty + i, 8);  // warps 0-7
+        }
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)),
+                     "r"(AS * BN)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tbase = *s_taddr, sbase = smem_u32(sm);
+    bool ok = true;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_JOIN));
+        const int half = warp >> 2;  // features 128 * half of the tile
+        const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
+        const uint32_t rel0 = peer_addr(aempty, 0), rel1 = peer_addr(aempty + 1, 0);
+        const int mrow = (int)rank * 128 + 32 * (warp & 3) + lane;
+        const float *mine = reinterpret_cast<const float *>(sm + SCALES) + half * 128 + 32 * (warp & 3) + lane;
+        int as = 0, cs = 0;
+        uint32_t ph = 0, cph = 0;
+        for (unsigned tile = pair; tile < tiles && ok; tile += npairs) {
+            uint64_t acc[64];  // pairs of fp32
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            for (int kb = 0; kb < nkb; ++kb) {
+                const int ck = kb & (CK - 1);
+                if (ck == 0) ok = wait_fast(sfull + cs, cph);
+                const float s0 = mine[cs * (CHUNK / 4) + ck * 256];
+                uint64_t s2;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s0));
+                ok = wait_fast(afull + as, ph) && ok;
+                if (__any_sync(0xffffffffu, !ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 128; c += 64) {
+                    uint32_t d0[32], d1[32];
+                    tmem_ld32(trow + as * BN + c, d0);
+                    tmem_ld32(trow + as * BN + c + 32, d1);
+                    tmem_ld_wait();
+                    if (c == 64) {  // the accumulator is read: the MMAs may write it again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_peer(as ? rel1 : rel0);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + j], d0[2 * j], d0[2 * j + 1], s2);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + 16 + j], d1[2 * j], d1[2 * j + 1], s2);
+                }
+                as ^= 1;
+                ph ^= as == 0;
+                if (ck == CK - 1 || kb == nkb - 1) {  // the chunk's last: its slot may be filled again
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sempty + cs);
+                    if (++cs == CS) {
+                        cs = 0;
+                        cph ^= 1;
+                    }
+                }
+            }
+            const int m = (int)(tile % mt) * BM + mrow, n0 = (int)(tile / mt) * BN + half * 128;
+            if (ok && m < M && n0 < N) {
+                TO *row = y + m * ldy + n0;
+                constexpr int V = 16 / (int)sizeof(TO);
+                auto at = [&](int j) { return __uint_as_float((uint32_t)(acc[j >> 1] >> (32 * (j & 1)))); };
+                if (vec && n0 + 128 <= N) {
+#pragma unroll
+                    for (int j = 0; j < 128; j += V) {
+                        uint4 raw;
+                        TO *e = reinterpret_cast<TO *>(&raw);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) Elem<TO>::store(e + i, at(j + i));
+                        *reinterpret_cast<uint4 *>(row + j) = raw;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (n0 + j < N) Elem<TO>::store(row + j, at(j));
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
+        if (warp == 8) {
+            if (elect_one()) {
+                int st = 0, used = 0;
+                uint32_t ph = 1;  // the ring starts out free
+                for (unsigned tile = pair; tile < tiles && ok; tile += npairs) {
+                    const int row_a = (int)(tile % mt) * BM + (int)rank * 128, row_w = (int)(tile / mt) * BN + (int)rank * 128;
+                    for (int kb = 0; kb < nkb; ++kb) {
+                        ok = wait_fast(empty + st, ph);
+                        if (!ok) break;
+                        uint8_t *d = sm + st * STAGE;
+                        const uint32_t bar = peer_addr(full + st, 0);
+                        if (rank == 0) mbar_arrive_expect_tx(full + st, 2 * STAGE);
+                        tma_load_pair(d, &tm_a, bar, kb * KB, row_a);
+                        tma_load_pair(d + A_BYTES, &tm_w, bar, kb * KB, row_w);
+                        if (used < ST) ++used;
+                        if (++st == ST) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                    }
+                }
+                // every copy issued has been used by the MMAs (so has landed) before shared memory goes away
+                for (int i = 0; i < used; ++i) {
+                    if (--st < 0) {
+                        st = ST - 1;
+                        ph ^= 1;
+                    }
+                    ok = wait_fast(empty + st, ph ^ 1) && ok;
+                }
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            if (rank == 0 && elect_one()) {
+                int st = 0, as = 0;
+                uint32_t ph = 0, aph = 1;  // the accumulators start out free
+                const uint64_t a0 = sdesc_sw128(sbase, 16, 1024), b0 = sdesc_sw128(sbase + A_BYTES, 16, 1024);
+                bool ready = false;  // the coming stage's copies are known to have landed
+                for (unsigned tile = pair; tile < tiles && ok; tile += npairs) {
+                    for (int kb = 0; kb < nkb; ++kb) {
+                        ok = (ready || wait_fast(full + st, ph)) && wait_fast(aempty + as, aph);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t a = a0 + (uint64_t)(st * (STAGE / 16)), b = b0 + (uint64_t)(st * (STAGE / 16));
+                        uint64_t *done = empty + st;
+                        if (++st == ST) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                        ready = test_wait(full + st, ph);  // its latency passes under the MMAs' issue
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f8_pair(tbase + as * BN, a + 2 * ks, b + 2 * ks, idesc_f8(BM, BN), ks > 0);
+                        commit_pair(afull + as);
+                        commit_pair(done);
+                        as ^= 1;
+                        aph ^= as == 0;
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
+            // warps 10 and 11: the scales' products, two K blocks of a chunk each, CS - 1 chunks ahead of
+            // their use (tokens and features past the end take the last ones' and are not stored)
+            const int nblk = (N + 127) / 128;
+            int cs = 0;
+            uint32_t cph = 1;
+            float *buf = reinterpret_cast<float *>(sm + SCALES) + (warp - 10) * 2 * 256 + lane;
+            for (unsigned tile = pair; tile < tiles && ok; tile += npairs) {
+                const int m0 = (int)(tile % mt) * BM + (int)rank * 128 + lane, nb = (int)(tile / mt) * 2;
+                const float *w0 = sw + (int64_t)nb * nkb, *w1 = nb + 1 < nblk ? w0 + nkb : w0;
+                for (int k0 = 0; k0 < nkb; k0 += CK) {
+                    float av[2][4], wv[2][2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int kb = k0 + (warp - 10) * 2 + i, kc = kb < nkb ? kb : nkb - 1;
+                        wv[i][0] = __ldg(w0 + kc);
+                        wv[i][1] = __ldg(w1 + kc);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int m = m0 + 32 * q;
+                            av[i][q] = __ldg(sa + (int64_t)kc * M + (m < M ? m : M - 1));
+                        }
+                    }
+                    ok = wait_fast(sempty + cs, cph);
+                    if (__any_sync(0xffffffffu, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    float *b = buf + cs * (CHUNK / 4);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            b[i * 256 + 32 * q] = av[i][q] * wv[i][0];
+                            b[i * 256 + 128 + 32 * q] = av[i][q] * wv[i][1];
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sfull + cs);
+                    if (++cs == CS) {
+                        cs = 0;
+                        cph ^= 1;
+                    }
+                }
+            }
+        }
+    }
+    if (!ok) atomicOr(err, DEVERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 9)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(AS * BN) : "memory");
+}
+
+// pairs of CTAs that run at once on the current device
+template <typename TO> static int resident_pairs() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return 0;
+    int n = known[dev].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(many::NTHREADS);
+    cfg.dynamicSmemBytes = many::SMEM;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_many_kernel<TO>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev].store(n, std::memory_order_release);
+    return n;
+}
+
+template <typename TO>
+static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, const float *sa, const float *sw, void *y,
+                              int64_t M, int N, int K, int64_t ldy, unsigned *err, cudaStream_t s) {
+    if (smem_attr_once<linear_many_kernel<TO>>(many::SMEM) != cudaSuccess)
+        return check_launch("linear_many_kernel (shared memory attribute)");
+    // the register split only adds up for the launch register count it was made for
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_acquire) == 0) {
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, linear_many_kernel<TO>) != cudaSuccess)
+            return check_launch("linear_many_kernel (attributes)");
+        regs.store(fa.numRegs, std::memory_order_release);
+    }
+    if (regs.load(std::memory_order_acquire) != many::REGS)
+        return fail(KDA_ERR_UNSUPPORTED, "linear_many_kernel built with a register count its split was not made for");
+    const int pairs = resident_pairs<TO>();
+    if (pairs < 1) return fail(KDA_ERR_CUDA, "no pair of CTAs fits the device");
+    const int64_t mt = (M + many::BM - 1) / many::BM, tiles = mt * (((int64_t)N + many::BN - 1) / many::BN);
+    if (tiles > 0x7fffffffLL) return invalid("M*N too large for one launch");
+    const int vec = (ldy * sizeof(TO)) % 16 == 0;
+    linear_many_kernel<TO><<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), many::NTHREADS, many::SMEM, s>>>(
+        ta, tw, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy, (unsigned)mt, (unsigned)tiles, vec,
+        err);
+    return check_launch("linear_many_kernel");
+}
+
 // map of a row-major [rows][K] byte matrix with row stride ld, box 128 x box_rows, 128-byte swizzle
 static bool byte_map(CUtensorMap *m, const void *p, int K, int64_t rows, int64_t ld, int box_rows) {
     return tcp::make_map_ld(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)rows, (uint64_t)ld, KB,
@@ -221,6 +618,12 @@ static bool byte_map(CUtensorMap *m, const void *p, int K, int64_t rows, int64_t
 template <typename TO>
 static kda_status run_linear(const void *a, const float *sa, const void *w, const float *sw, void *y, int64_t M,
                              int N, int K, int64_t lda, int64_t ldw, int64_t ldy, unsigned *err, cudaStream_t s) {
+    if (M > 256) {
+        CUtensorMap ta, tw;
+        if (!byte_map(&ta, a, K, M, lda, 128) || !byte_map(&tw, w, K, N, ldw, 128))
+            return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+        return launch_many<TO>(ta, tw, sa, sw, y, M, N, K, ldy, err, s);
+    }
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     CUtensorMap tw, ta;
     if (!byte_map(&tw, w, K, N, ldw, 128) || !byte_map(&ta, a, K, M, lda, nt))
