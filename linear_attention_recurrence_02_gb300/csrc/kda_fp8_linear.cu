@@ -234,10 +234,12 @@ constexpr int BM = 256, BN = 256;                 // tile of a pair
 constexpr int A_BYTES = 128 * KB, W_BYTES = 128 * KB;
 constexpr int STAGE = A_BYTES + W_BYTES;          // bytes per CTA: tokens, then weights
 constexpr int ST = 6, AS = 2;
-constexpr int NTHREADS = 384;                     // three warpgroups
-// registers a thread: launched with REGS, split so that the joining warpgroups hold their sums
-constexpr int REGS = 168, REGS_JOIN = 208, REGS_ISSUE = 88;
-static_assert(2 * REGS_JOIN + REGS_ISSUE == 3 * REGS, "the split draws on the launch's registers");
+constexpr int JW = 8, JC = 128;                   // joining warps, features of each
+constexpr int NTHREADS = 32 * (JW + 4);
+// Registers a thread: launched with REGS, split so that the joining warps hold their sums and neither
+// side spills (208 / 88 and 240 / 24 spill inside the K loop: a third slower).
+constexpr int REGS = 168, REGS_JOIN = 216, REGS_ISSUE = 72;
+static_assert(JW * REGS_JOIN + 4 * REGS_ISSUE == (JW + 4) * REGS, "the split draws on the launch's registers");
 constexpr int CK = 4, CS = 4;                     // K blocks of scales per chunk, chunks in flight
 constexpr int CHUNK = CK * 256 * 4;               // [CK][feature half][token] products of the two scales
 constexpr int SCALES = ST * STAGE;
@@ -262,28 +264,20 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
 __device__ __forceinline__ void arrive_peer(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Bounded wait that reads the clock only where the first try fails. The pair's
-// barriers guard TMEM (ordered by the tcgen05 fences) and copies (ordered by
-// the barrier's own transaction count) and no plain memory, so waits and
-// arrivals stay at their default scope: at cluster scope each one waited for
-// the warp's outstanding memory operations (a K block's hand-shakes alone took
-// 1700 cycles).
-__device__ __forceinline__ bool wait_fast(uint64_t *bar, uint32_t parity) {
-    return tc::mbar_try_wait(bar, parity) || tc::mbar_wait(bar, parity, WAIT_LIMIT);
+// The pair's barriers guard TMEM (ordered by the tcgen05 fences) and copies
+// (ordered by the barrier's own transaction count) and no plain memory, so
+// waits and arrivals stay at their default scope: at cluster scope each one
+// waited for the warp's outstanding memory operations (a K block's hand-shakes
+// alone took 1700 cycles).
+// Once a wait has given up (ok is false) the later ones only look, so that a
+// loop of waits has no exit in its middle and ends in bounded time.
+__device__ __forceinline__ bool wait_more(uint64_t *bar, uint32_t parity, bool ok) {
+    if (tc::mbar_try_wait(bar, parity)) return ok;
+    return ok && tc::mbar_wait(bar, parity, WAIT_LIMIT);
 }
-__device__ __forceinline__ bool test_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// one lane of a whole warp. An MMA issued under this predicate takes its
-// descriptors from uniform registers: 45 cycles an MMA, 62 under lane == 0.
+// One lane of a whole warp. The issuing warps run their loops with all lanes and
+// single one out only around the copies and MMAs: under `lane == 0` an MMA took
+// 62 cycles to issue, as its descriptors were not in uniform registers.
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
     asm volatile(
@@ -319,10 +313,37 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
         : "memory");
 }
 
-// (a0, a1) += (d0, d1) * (s, s) in one instruction
-__device__ __forceinline__ void fma2(uint64_t &a, uint32_t d0, uint32_t d1, uint64_t s) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
+// 32 TMEM columns of the thread's lane as 16 pairs, waited for
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, uint64_t (&d)[16]) {
+    asm volatile(
+        "{\n\t.reg .b32 t<32>;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,"
+        "t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "mov.b64 %0, {t0,t1};\n\t"
+        "mov.b64 %1, {t2,t3};\n\t"
+        "mov.b64 %2, {t4,t5};\n\t"
+        "mov.b64 %3, {t6,t7};\n\t"
+        "mov.b64 %4, {t8,t9};\n\t"
+        "mov.b64 %5, {t10,t11};\n\t"
+        "mov.b64 %6, {t12,t13};\n\t"
+        "mov.b64 %7, {t14,t15};\n\t"
+        "mov.b64 %8, {t16,t17};\n\t"
+        "mov.b64 %9, {t18,t19};\n\t"
+        "mov.b64 %10, {t20,t21};\n\t"
+        "mov.b64 %11, {t22,t23};\n\t"
+        "mov.b64 %12, {t24,t25};\n\t"
+        "mov.b64 %13, {t26,t27};\n\t"
+        "mov.b64 %14, {t28,t29};\n\t"
+        "mov.b64 %15, {t30,t31};\n\t"
+        "}\n"
+        : "=l"(d[0]), "=l"(d[1]), "=l"(d[2]), "=l"(d[3]), "=l"(d[4]), "=l"(d[5]), "=l"(d[6]), "=l"(d[7]), "=l"(d[8]),
+          "=l"(d[9]), "=l"(d[10]), "=l"(d[11]), "=l"(d[12]), "=l"(d[13]), "=l"(d[14]), "=l"(d[15])
+        : "r"(taddr)
+        : "memory");
+}
+// both halves: a += d * s
+__device__ __forceinline__ void fma2(uint64_t &a, uint64_t d, uint64_t s) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(s));
 }
 
@@ -338,7 +359,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + BARS), *empty = full + ST, *afull = empty + ST,
              *aempty = afull + AS, *sfull = aempty + AS, *sempty = sfull + CS;
     uint32_t *s_taddr = reinterpret_cast<uint32_t *>(sempty + CS);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
     const uint32_t rank = cluster_rank();
     const unsigned pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     if (tid == 0) {
@@ -348,15 +370,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
         }
         for (int i = 0; i < AS; ++i) {
             mbar_init(afull + i, 1);
-            mbar_init(aempty + i, 16);  // eight warps of each CTA
+            mbar_init(aempty + i, 2 * JW);  // the joining warps of both CTAs
         }
         for (int i = 0; i < CS; ++i) {
-            mbar_init(sfull + i, 2);   // warps 10 and 11
-            mbar_init(sempty + i, 8);  // warps 0-7
+            mbar_init(sfull + i, 2);  // the two warps that form scales
+            mbar_init(sempty + i, JW);
         }
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == JW + 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)),
                      "r"(AS * BN)
                      : "memory");
@@ -366,9 +388,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tbase = *s_taddr, sbase = smem_u32(sm);
+    static_assert(AS * BN == 512, "the whole TMEM: its first column is 0");
+    constexpr uint32_t tbase = 0;
+    const uint32_t sbase = smem_u32(sm);
     bool ok = true;
-    if (warp < 8) {
+    if (warp < JW) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_JOIN));
         const int half = warp >> 2;  // features 128 * half of the tile
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
@@ -377,37 +401,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
         const float *mine = reinterpret_cast<const float *>(sm + SCALES) + half * 128 + 32 * (warp & 3) + lane;
         int as = 0, cs = 0;
         uint32_t ph = 0, cph = 0;
-        for (unsigned tile = pair; tile < tiles && ok; tile += npairs) {
-            uint64_t acc[64];  // pairs of fp32
+        for (unsigned tile = pair; tile < tiles; tile += npairs) {
+            uint64_t acc[JC / 2];  // pairs of fp32
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            for (int j = 0; j < JC / 2; ++j) acc[j] = 0;
             for (int kb = 0; kb < nkb; ++kb) {
                 const int ck = kb & (CK - 1);
-                if (ck == 0) ok = wait_fast(sfull + cs, cph);
+                if (ck == 0) ok = wait_more(sfull + cs, cph, ok);
                 const float s0 = mine[cs * (CHUNK / 4) + ck * 256];
                 uint64_t s2;
                 asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s0));
-                ok = wait_fast(afull + as, ph) && ok;
-                if (__any_sync(0xffffffffu, !ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait_more(afull + as, ph, ok);
+                __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t d0[32], d1[32];
-                    tmem_ld32(trow + as * BN + c, d0);
-                    tmem_ld32(trow + as * BN + c + 32, d1);
-                    tmem_ld_wait();
-                    if (c == 64) {  // the accumulator is read: the MMAs may write it again
+                for (int c = 0; c < JC; c += 32) {
+                    uint64_t d[16];
+                    tmem_ld_pairs(trow + as * BN + c, d);
+                    if (c == JC - 32) {  // the accumulator is read: the MMAs may write it again
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_peer(as ? rel1 : rel0);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + j], d0[2 * j], d0[2 * j + 1], s2);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + 16 + j], d1[2 * j], d1[2 * j + 1], s2);
+                    for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + j], d[j], s2);
                 }
                 as ^= 1;
                 ph ^= as == 0;
@@ -423,122 +440,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
             const int m = (int)(tile % mt) * BM + mrow, n0 = (int)(tile / mt) * BN + half * 128;
             if (ok && m < M && n0 < N) {
                 TO *row = y + m * ldy + n0;
-                constexpr int V = 16 / (int)sizeof(TO);
                 auto at = [&](int j) { return __uint_as_float((uint32_t)(acc[j >> 1] >> (32 * (j & 1)))); };
-                if (vec && n0 + 128 <= N) {
+                if (vec && n0 + JC <= N) {  // whole 32-byte sectors
+                    constexpr int V = 32 / (int)sizeof(TO);
 #pragma unroll
-                    for (int j = 0; j < 128; j += V) {
-                        uint4 raw;
-                        TO *e = reinterpret_cast<TO *>(&raw);
+                    for (int j = 0; j < JC; j += V) {
+                        TO e[V];
 #pragma unroll
                         for (int i = 0; i < V; ++i) Elem<TO>::store(e + i, at(j + i));
-                        *reinterpret_cast<uint4 *>(row + j) = raw;
+                        uint32_t r[8];
+                        memcpy(r, e, 32);
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + j),
+                                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                                     "r"(r[7])
+                                     : "memory");
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 128; ++j)
+                    for (int j = 0; j < JC; ++j)
                         if (n0 + j < N) Elem<TO>::store(row + j, at(j));
                 }
             }
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
-        if (warp == 8) {
-            if (elect_one()) {
-                int st = 0, used = 0;
-                uint32_t ph = 1;  // the ring starts out free
-                for (unsigned tile = pair; tile < tiles && ok; tile += npairs) {
-                    const int row_a = (int)(tile % mt) * BM + (int)rank * 128, row_w = (int)(tile / mt) * BN + (int)rank * 128;
-                    for (int kb = 0; kb < nkb; ++kb) {
-                        ok = wait_fast(empty + st, ph);
-                        if (!ok) break;
+        if (warp == JW) {
+            int st = 0;
+            uint32_t ph = 1;  // the ring starts out free
+            for (unsigned tile = pair; tile < tiles; tile += npairs) {
+                const int row_a = (int)(tile % mt) * BM + (int)rank * 128;
+                const int row_w = (int)(tile / mt) * BN + (int)rank * 128;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    ok = wait_more(empty + st, ph, ok);
+                    __syncwarp();
+                    if (elect_one()) {
                         uint8_t *d = sm + st * STAGE;
                         const uint32_t bar = peer_addr(full + st, 0);
                         if (rank == 0) mbar_arrive_expect_tx(full + st, 2 * STAGE);
                         tma_load_pair(d, &tm_a, bar, kb * KB, row_a);
                         tma_load_pair(d + A_BYTES, &tm_w, bar, kb * KB, row_w);
-                        if (used < ST) ++used;
-                        if (++st == ST) {
-                            st = 0;
-                            ph ^= 1;
-                        }
+                    }
+                    if (++st == ST) {
+                        st = 0;
+                        ph ^= 1;
                     }
                 }
-                // every copy issued has been used by the MMAs (so has landed) before shared memory goes away
-                for (int i = 0; i < used; ++i) {
+            }
+            // Every copy of both CTAs lands before shared memory goes away (the even CTA's barriers count
+            // them): the ring's next phase of each stage is the one that the last copies complete.
+            if (rank == 0)
+                for (int i = 0; i < ST; ++i) {
                     if (--st < 0) {
                         st = ST - 1;
                         ph ^= 1;
                     }
-                    ok = wait_fast(empty + st, ph ^ 1) && ok;
+                    if (!tc::mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
                 }
-            }
-            __syncwarp();
-        } else if (warp == 9) {
-            if (rank == 0 && elect_one()) {
+        } else if (warp == JW + 1) {
+            if (rank == 0) {
                 int st = 0, as = 0;
                 uint32_t ph = 0, aph = 1;  // the accumulators start out free
                 const uint64_t a0 = sdesc_sw128(sbase, 16, 1024), b0 = sdesc_sw128(sbase + A_BYTES, 16, 1024);
-                bool ready = false;  // the coming stage's copies are known to have landed
-                for (unsigned tile = pair; tile < tiles && ok; tile += npairs) {
+                for (unsigned tile = pair; tile < tiles; tile += npairs) {
                     for (int kb = 0; kb < nkb; ++kb) {
-                        ok = (ready || wait_fast(full + st, ph)) && wait_fast(aempty + as, aph);
-                        if (!ok) break;
-                        tc_fence_after();
                         const uint64_t a = a0 + (uint64_t)(st * (STAGE / 16)), b = b0 + (uint64_t)(st * (STAGE / 16));
-                        uint64_t *done = empty + st;
+                        ok = wait_more(full + st, ph, ok);
+                        ok = wait_more(aempty + as, aph, ok);
+                        __syncwarp();
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f8_pair(tbase + as * BN, a + 2 * ks, b + 2 * ks, idesc_f8(BM, BN), ks > 0);
+                            commit_pair(afull + as);
+                            commit_pair(empty + st);
+                        }
+                        as ^= 1;
+                        aph ^= as == 0;
                         if (++st == ST) {
                             st = 0;
                             ph ^= 1;
                         }
-                        ready = test_wait(full + st, ph);  // its latency passes under the MMAs' issue
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f8_pair(tbase + as * BN, a + 2 * ks, b + 2 * ks, idesc_f8(BM, BN), ks > 0);
-                        commit_pair(afull + as);
-                        commit_pair(done);
-                        as ^= 1;
-                        aph ^= as == 0;
                     }
                 }
             }
-            __syncwarp();
         } else {
-            // warps 10 and 11: the scales' products, two K blocks of a chunk each, CS - 1 chunks ahead of
+            // the last two warps: the scales' products, two K blocks of a chunk each, CS - 1 chunks ahead of
             // their use (tokens and features past the end take the last ones' and are not stored)
-            const int nblk = (N + 127) / 128;
+            const int nblk = (N + 127) / 128, w2 = (warp - JW - 2) * 2;
             int cs = 0;
             uint32_t cph = 1;
-            float *buf = reinterpret_cast<float *>(sm + SCALES) + (warp - 10) * 2 * 256 + lane;
-            for (unsigned tile = pair; tile < tiles && ok; tile += npairs) {
+            for (unsigned tile = pair; tile < tiles; tile += npairs) {
                 const int m0 = (int)(tile % mt) * BM + (int)rank * 128 + lane, nb = (int)(tile / mt) * 2;
                 const float *w0 = sw + (int64_t)nb * nkb, *w1 = nb + 1 < nblk ? w0 + nkb : w0;
                 for (int k0 = 0; k0 < nkb; k0 += CK) {
-                    float av[2][4], wv[2][2];
+                    ok = wait_more(sempty + cs, cph, ok);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int kb = k0 + (warp - 10) * 2 + i, kc = kb < nkb ? kb : nkb - 1;
-                        wv[i][0] = __ldg(w0 + kc);
-                        wv[i][1] = __ldg(w1 + kc);
+                        const int kc = k0 + w2 + i < nkb ? k0 + w2 + i : nkb - 1;
+                        const float *ap = sa + (int64_t)kc * M;
+                        float *b = reinterpret_cast<float *>(sm + SCALES) + cs * (CHUNK / 4) + (w2 + i) * 256 + lane;
+                        float av[4];
+                        const float wa = __ldg(w0 + kc), wb = __ldg(w1 + kc);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) av[q] = __ldg(ap + (m0 + 32 * q < M ? m0 + 32 * q : M - 1));
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const int m = m0 + 32 * q;
-                            av[i][q] = __ldg(sa + (int64_t)kc * M + (m < M ? m : M - 1));
+                            b[32 * q] = av[q] * wa;
+                            b[128 + 32 * q] = av[q] * wb;
                         }
                     }
-                    ok = wait_fast(sempty + cs, cph);
-                    if (__any_sync(0xffffffffu, !ok)) {
-                        ok = false;
-                        break;
-                    }
-                    float *b = buf + cs * (CHUNK / 4);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            b[i * 256 + 32 * q] = av[i][q] * wv[i][0];
-                            b[i * 256 + 128 + 32 * q] = av[i][q] * wv[i][1];
-                        }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sfull + cs);
                     if (++cs == CS) {
@@ -554,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    if (warp == 9)
+    if (warp == JW + 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(AS * BN) : "memory");
 }
 
@@ -602,7 +613,7 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
     if (pairs < 1) return fail(KDA_ERR_CUDA, "no pair of CTAs fits the device");
     const int64_t mt = (M + many::BM - 1) / many::BM, tiles = mt * (((int64_t)N + many::BN - 1) / many::BN);
     if (tiles > 0x7fffffffLL) return invalid("M*N too large for one launch");
-    const int vec = (ldy * sizeof(TO)) % 16 == 0;
+    const int vec = (ldy * sizeof(TO)) % 32 == 0 && (reinterpret_cast<uintptr_t>(y) & 31) == 0;
     linear_many_kernel<TO><<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), many::NTHREADS, many::SMEM, s>>>(
         ta, tw, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy, (unsigned)mt, (unsigned)tiles, vec,
         err);
