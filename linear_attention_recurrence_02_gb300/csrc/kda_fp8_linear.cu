@@ -10,6 +10,7 @@
 // products, fp32 accumulators in TMEM), and the K blocks' sums are joined
 // outside it: acc += (sa * sw) * block_sum in fp32 registers.
 #include <atomic>
+#include <cstring>
 #include <string>
 
 #include "kda_common.cuh"
@@ -233,7 +234,7 @@ namespace many {
 constexpr int BM = 256, BN = 256;                 // tile of a pair
 constexpr int A_BYTES = 128 * KB, W_BYTES = 128 * KB;
 constexpr int STAGE = A_BYTES + W_BYTES;          // bytes per CTA: tokens, then weights
-constexpr int ST = 6, AS = 2;
+constexpr int ST = 5, AS = 2;
 constexpr int JW = 8, JC = 128;                   // joining warps, features of each
 constexpr int NTHREADS = 32 * (JW + 4);
 // Registers a thread: launched with REGS, split so that the joining warps hold their sums and neither
@@ -242,7 +243,8 @@ constexpr int REGS = 168, REGS_JOIN = 216, REGS_ISSUE = 72;
 static_assert(JW * REGS_JOIN + 4 * REGS_ISSUE == (JW + 4) * REGS, "the split draws on the launch's registers");
 constexpr int CK = 4, CS = 4;                     // K blocks of scales per chunk, chunks in flight
 constexpr int CHUNK = CK * 256 * 4;               // [CK][feature half][token] products of the two scales
-constexpr int SCALES = ST * STAGE;
+constexpr int OUT = ST * STAGE;                   // results on their way out: per joining warp 32 rows of 128 B
+constexpr int SCALES = OUT + JW * 4096;
 constexpr int BARS = SCALES + CS * CHUNK;
 constexpr int SMEM = BARS + (2 * ST + 2 * AS + 2 * CS) * 8 + 16 + 1024;
 }  // namespace many
@@ -350,8 +352,8 @@ __device__ __forceinline__ void fma2(uint64_t &a, uint64_t d, uint64_t s) {
 template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                       const float *__restrict__ sa, const float *__restrict__ sw, TO *__restrict__ y, int M, int N,
-                       int nkb, int64_t ldy, unsigned mt, unsigned tiles, int vec, unsigned *err) {
+                       const __grid_constant__ CUtensorMap tm_y, const float *__restrict__ sa, const float *__restrict__ sw, TO *__restrict__ y, int M, int N,
+                       int nkb, int64_t ldy, unsigned mt, unsigned tiles, int by_tma, unsigned *err) {
     using namespace tc;
     using namespace many;
     extern __shared__ uint8_t smem_raw[];
@@ -399,6 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
         const uint32_t rel0 = peer_addr(aempty, 0), rel1 = peer_addr(aempty + 1, 0);
         const int mrow = (int)rank * 128 + 32 * (warp & 3) + lane;
         const float *mine = reinterpret_cast<const float *>(sm + SCALES) + half * 128 + 32 * (warp & 3) + lane;
+        uint8_t *out = sm + OUT + warp * 4096;
         int as = 0, cs = 0;
         uint32_t ph = 0, cph = 0;
         for (unsigned tile = pair; tile < tiles; tile += npairs) {
@@ -437,31 +440,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
                     }
                 }
             }
-            const int m = (int)(tile % mt) * BM + mrow, n0 = (int)(tile / mt) * BN + half * 128;
-            if (ok && m < M && n0 < N) {
-                TO *row = y + m * ldy + n0;
-                auto at = [&](int j) { return __uint_as_float((uint32_t)(acc[j >> 1] >> (32 * (j & 1)))); };
-                if (vec && n0 + JC <= N) {  // whole 32-byte sectors
-                    constexpr int V = 32 / (int)sizeof(TO);
+            // The results leave through shared memory, 128 bytes of each of the warp's 32 rows at a time (a
+            // row's stores straight from its thread take a cycle per 32 bytes): swizzled 16-byte pieces, then
+            // one tensor copy, or whole rows by the warp where y's rows do not suit a tensor map.
+            const int mw = (int)(tile % mt) * BM + mrow - lane, n0 = (int)(tile / mt) * BN + half * 128;
+            auto at = [&](int j) { return __uint_as_float((uint32_t)(acc[j >> 1] >> (32 * (j & 1)))); };
+            if (__all_sync(0xffffffffu, ok) && mw < M) {
+                constexpr int V = 16 / (int)sizeof(TO), JR = 8 * V;
 #pragma unroll
-                    for (int j = 0; j < JC; j += V) {
-                        TO e[V];
+                for (int r = 0; r < JC / JR; ++r) {
+                    const int n = n0 + r * JR;
+                    if (n >= N) break;
+                    if (lane == 0) bulk_wait_read();  // the buffer's last copy has read it
+                    __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < V; ++i) Elem<TO>::store(e + i, at(j + i));
-                        uint32_t r[8];
-                        memcpy(r, e, 32);
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + j),
-                                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-                                     "r"(r[7])
-                                     : "memory");
+                    for (int q = 0; q < 8; ++q) {
+                        uint4 raw;
+                        TO *e = reinterpret_cast<TO *>(&raw);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) Elem<TO>::store(e + i, at(r * JR + q * V + i));
+                        *reinterpret_cast<uint4 *>(out + lane * 128 + ((q ^ (lane & 7)) << 4)) = raw;
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < JC; ++j)
-                        if (n0 + j < N) Elem<TO>::store(row + j, at(j));
+                    fence_async_smem();
+                    __syncwarp();
+                    if (by_tma) {
+                        if (lane == 0) {
+                            tma_store_2d(&tm_y, out, n, mw);
+                            bulk_commit();
+                        }
+                    } else {
+                        const int rows = M - mw < 32 ? M - mw : 32;
+                        for (int i = 0; i < rows; ++i)
+                            for (int c = lane; c < JR && n + c < N; c += 32)
+                                y[(mw + i) * ldy + n + c] = *reinterpret_cast<const TO *>(
+                                    out + i * 128 + (((c / V) ^ (i & 7)) << 4) + (c % V) * (int)sizeof(TO));
+                    }
                 }
             }
         }
+        if (lane == 0) bulk_wait_all();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
         if (warp == JW) {
@@ -613,10 +630,18 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
     if (pairs < 1) return fail(KDA_ERR_CUDA, "no pair of CTAs fits the device");
     const int64_t mt = (M + many::BM - 1) / many::BM, tiles = mt * (((int64_t)N + many::BN - 1) / many::BN);
     if (tiles > 0x7fffffffLL) return invalid("M*N too large for one launch");
-    const int vec = (ldy * sizeof(TO)) % 32 == 0 && (reinterpret_cast<uintptr_t>(y) & 31) == 0;
+    // y's rows suit a tensor map where their stride is a multiple of 16 bytes
+    const int by_tma = (ldy * sizeof(TO)) % 16 == 0 && ldy < (1LL << 36);
+    CUtensorMap ty;
+    memset(&ty, 0, sizeof(ty));
+    if (by_tma && !tcp::make_map_ld(&ty, y, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                                    (uint64_t)N, (uint64_t)M, (uint64_t)ldy * sizeof(TO), 128 / sizeof(TO), 32,
+                                    CU_TENSOR_MAP_SWIZZLE_128B))
+        return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     linear_many_kernel<TO><<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), many::NTHREADS, many::SMEM, s>>>(
-        ta, tw, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy, (unsigned)mt, (unsigned)tiles, vec,
-        err);
+        ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy, (unsigned)mt, (unsigned)tiles,
+        by_tma, err);
     return check_launch("linear_many_kernel");
 }
 
