@@ -48,207 +48,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-// ---------------------------------------------------------------- few tokens
-// A CTA owns 128 weight rows (the MMA's M axis: TMEM lane = output feature)
-// and NT tokens (its N axis), so that a step with few tokens still feeds whole
-// 128-row tiles: the weights, read once, are what bounds it. Warp 0 streams
-// the weight and token tiles of each K block through a ring of ST stages,
-// warp 1 issues the block's four MMAs into one of AS accumulator stages, and
-// warps 2-5 join the block sums: each multiplies the block's token scales by
-// the weight block's scale once, and then has one fused multiply-add per
-// feature and token.
-template <int NT> struct Few {
-    static constexpr int STAGE = 128 * KB + NT * KB;  // bytes: weights, then tokens
-    static constexpr int ST = NT <= 32 ? 10 : NT <= 64 ? 8 : 6;
-    static constexpr int AS = NT <= 64 ? 4 : 2;       // accumulator stages
-    static constexpr int COLS = NT * AS;              // TMEM columns (64, 128, 256, 256)
-    static constexpr int SBUF = ST * STAGE;           // scale rows: 4 warps x 2 x NT floats
-    static constexpr int BARS = SBUF + 4 * 2 * NT * 4;
-    static constexpr int SMEM = BARS + (2 * ST + 2 * AS) * 8 + 16 + 1024;
-    static constexpr int NTHREADS = 192;
-};
-
-template <int NT, typename TO>
-__global__ void __launch_bounds__(192) linear_few_kernel(const __grid_constant__ CUtensorMap tm_w,
-                                                         const __grid_constant__ CUtensorMap tm_a,
-                                                         const float *__restrict__ sa, const float *__restrict__ sw,
-                                                         TO *__restrict__ y, int64_t M, int N, int nkb, int64_t ldy,
-                                                         int mt, unsigned *err) {
-    using namespace tc;
-    using F = Few<NT>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + F::BARS), *empty = full + F::ST, *afull = empty + F::ST,
-             *aempty = afull + F::AS;
-    uint32_t *s_taddr = reinterpret_cast<uint32_t *>(aempty + F::AS);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nt = blockIdx.x / mt;
-    const int64_t m0 = (int64_t)(blockIdx.x % mt) * NT;
-    const int n0 = nt * 128;
-    if (tid == 0) {
-        for (int i = 0; i < F::ST; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
-        }
-        for (int i = 0; i < F::AS; ++i) {
-            mbar_init(afull + i, 1);
-            mbar_init(aempty + i, 4);
-        }
-        fence_mbar_init();
-    }
-    if (warp == 1) {
-        tmem_alloc(s_taddr, F::COLS);
-        tmem_relinquish();
-    }
-    sync_tc();
-    const uint32_t tbase = *s_taddr, sbase = smem_u32(sm);
-    bool ok = true;
-    float acc[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j] = 0.f;
-    if (warp == 0) {
-        if (lane == 0) {
-            int kb = 0;
-            for (; kb < nkb && ok; ++kb) {
-                const int st = kb % F::ST;
-                if (kb >= F::ST) ok = mbar_wait(empty + st, (kb / F::ST - 1) & 1, WAIT_LIMIT);
-                if (!ok) break;
-                uint8_t *d = sm + st * F::STAGE;
-                mbar_arrive_expect_tx(full + st, F::STAGE);
-                tma_load_2d(d, &tm_w, full + st, kb * KB, n0);
-                tma_load_2d(d + 128 * KB, &tm_a, full + st, kb * KB, (int)m0);
-            }
-            // every copy issued has landed before shared memory goes away
-            for (int i = kb > F::ST ? kb - F::ST : 0; i < kb; ++i)
-                ok = mbar_wait(full + i % F::ST, (i / F::ST) & 1, WAIT_LIMIT) && ok;
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            for (int kb = 0; kb < nkb; ++kb) {
-                const int st = kb % F::ST, as = kb % F::AS;
-                if (kb >= F::AS) ok = mbar_wait(aempty + as, (kb / F::AS - 1) & 1, WAIT_LIMIT);
-                ok = ok && mbar_wait(full + st, (kb / F::ST) & 1, WAIT_LIMIT);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t a = sbase + st * F::STAGE, b = a + 128 * KB;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f8(tbase + as * NT, sdesc_sw128(a + ks * 32, 16, 1024), sdesc_sw128(b + ks * 32, 16, 1024),
-                           idesc_f8(128, NT), ks > 0);
-                mma_commit(empty + st);
-                mma_commit(afull + as);
-            }
-        }
-        __syncwarp();
-    } else {
-        const int ew = warp - 2;
-        const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
-        float *srow = reinterpret_cast<float *>(sm + F::SBUF) + ew * 2 * NT;
-        const float *swp = sw + (int64_t)nt * nkb;
-        constexpr int L = NT < 32 ? 1 : NT / 32;
-        // this lane's scales of the coming K block, multiplied only where they are used: a product right
-        // behind its loads would wait for them
-        float sv[L], ws;
-        auto fetch = [&](int kb) {
-            ws = __ldg(swp + kb);
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const int j = lane + 32 * i;
-                sv[i] = j < NT && m0 + j < M ? __ldg(sa + (int64_t)kb * M + m0 + j) : 0.f;
-            }
-        };
-        fetch(0);
-        for (int kb = 0; kb < nkb; ++kb) {
-            const int as = kb % F::AS;
-            float *sr = srow + (kb & 1) * NT;
-#pragma unroll
-            for (int i = 0; i < L; ++i)
-                if (lane + 32 * i < NT) sr[lane + 32 * i] = ws * sv[i];
-            if (kb + 1 < nkb) fetch(kb + 1);
-            __syncwarp();
-            ok = mbar_wait(afull + as, (kb / F::AS) & 1, WAIT_LIMIT);
-            if (__any_sync(0xffffffffu, !ok)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < NT; c += 16) {
-                uint32_t d[16];
-                tmem_ld16(trow + as * NT + c, d);
-                tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 s = *reinterpret_cast<const float4 *>(sr + c + 4 * q);
-                    acc[c + 4 * q] = fmaf(__uint_as_float(d[4 * q]), s.x, acc[c + 4 * q]);
-                    acc[c + 4 * q + 1] = fmaf(__uint_as_float(d[4 * q + 1]), s.y, acc[c + 4 * q + 1]);
-                    acc[c + 4 * q + 2] = fmaf(__uint_as_float(d[4 * q + 2]), s.z, acc[c + 4 * q + 2]);
-                    acc[c + 4 * q + 3] = fmaf(__uint_as_float(d[4 * q + 3]), s.w, acc[c + 4 * q + 3]);
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(aempty + as);
-        }
-        const int n = n0 + 32 * (warp & 3) + lane;
-        if (ok && n < N) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (m0 + j < M) Elem<TO>::store(y + (m0 + j) * ldy + n, acc[j]);
-        }
-    }
-    if (!ok && lane == 0) atomicOr(err, DEVERR_TIMEOUT);
-    sync_tc();
-    if (warp == 1) tmem_dealloc(tbase, F::COLS);
-}
-
-template <int NT, typename TO>
-static kda_status launch_few(const CUtensorMap &tw, const CUtensorMap &ta, const float *sa, const float *sw, void *y,
-                             int64_t M, int N, int K, int64_t ldy, unsigned *err, cudaStream_t s) {
-    using F = Few<NT>;
-    if (smem_attr_once<linear_few_kernel<NT, TO>>(F::SMEM) != cudaSuccess)
-        return check_launch("linear_few_kernel (shared memory attribute)");
-    const int64_t mt = (M + NT - 1) / NT, grid = mt * ((N + 127) / 128);
-    if (grid > 0x7fffffffLL) return invalid("M*N too large for one launch");
-    linear_few_kernel<NT, TO><<<(unsigned)grid, F::NTHREADS, F::SMEM, s>>>(
-        tw, ta, sa, sw, static_cast<TO *>(y), M, N, (K + KB - 1) / KB, ldy, (int)mt, err);
-    return check_launch("linear_few_kernel");
-}
-
-// ---------------------------------------------------------------- many tokens
-// A pair of CTAs (one cluster, two SMs) owns a 256-token x 256-feature tile:
-// the MMAs of cta_group::2 take 128 token rows and half of the 256 weight rows
-// from each CTA's shared memory, so every operand byte is copied and read once
-// per pair. Each CTA's TMEM holds its 128 tokens (lane = token) in two
-// accumulators of 256 columns, one K block each: 512 cycles of MMAs, in which
-// the other accumulator has to be read and handed back. Per CTA: warps 0-7 join
-// the block sums (warps 0-3 the tile's first 128 features, 4-7 the last; a
-// thread holds 128 fp32 sums of one token, and one product of its token's scale
-// with the features' scale serves the whole K block), warp 8 copies, warp 9 of
-// the even CTA issues the MMAs for both, warps 10 and 11 form the scales'
-// products, four K blocks at a time. Persistent: a pair walks tiles, token
-// tiles first, so that neighbouring pairs share weight tiles in L2, and the next
-// tile's products run while this one's results are stored.
-namespace many {
-constexpr int BM = 256, BN = 256;                 // tile of a pair
-constexpr int A_BYTES = 128 * KB, W_BYTES = 128 * KB;
-constexpr int STAGE = A_BYTES + W_BYTES;          // bytes per CTA: tokens, then weights
-constexpr int ST = 5, AS = 2;
-constexpr int JW = 8, JC = 128;                   // joining warps, features of each
-constexpr int NTHREADS = 32 * (JW + 4);
-// Registers a thread: launched with REGS, split so that the joining warps hold their sums and neither
-// side spills (208 / 88 and 240 / 24 spill inside the K loop: a third slower).
-constexpr int REGS = 168, REGS_JOIN = 216, REGS_ISSUE = 72;
-static_assert(JW * REGS_JOIN + 4 * REGS_ISSUE == (JW + 4) * REGS, "the split draws on the launch's registers");
-constexpr int CK = 4, CS = 4;                     // K blocks of scales per chunk, chunks in flight
-constexpr int CHUNK = CK * 256 * 4;               // [CK][feature half][token] products of the two scales
-constexpr int OUT = ST * STAGE;                   // results on their way out: per joining warp 32 rows of 128 B
-constexpr int SCALES = OUT + JW * 4096;
-constexpr int BARS = SCALES + CS * CHUNK;
-constexpr int SMEM = BARS + (2 * ST + 2 * AS + 2 * CS) * 8 + 16 + 1024;
-}  // namespace many
-
+// ---------------------------------------------------------------- waits, clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -289,6 +89,328 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(e));
     return e != 0;
 }
+// fp32 value at the place of `p` in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ float peer_load(const float *p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(p, rank)) : "memory");
+    return v;
+}
+// wait for the warp's TMEM loads; the loaded registers pass through it, so that no use moves ahead of it
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- few tokens
+// A CTA owns 128 weight rows (the MMA's M axis: TMEM lane = output feature),
+// NT tokens (its N axis) and, as one of the S CTAs of a cluster, a run of K
+// blocks, so that a step with few tokens still feeds whole 128-row tiles from
+// every SM: the weights, read once, are what bounds it. Warps 0-3 join the
+// block sums (a thread holds its feature's NT fp32 sums; the products of the
+// token scales with the weight block's come from shared memory), warp 4
+// streams the weight and token tiles through a ring of ST stages, warp 5 issues
+// a block's four MMAs into one of AS accumulators, warps 6 and 7 form the
+// scales' products of CK blocks at a time. The cluster's partial sums meet in
+// shared memory: each CTA adds up its share of the tokens over the S CTAs in
+// their order. Two CTAs fit an SM.
+// A programmatic dependent launch: before the kernel ahead of it on the stream
+// has completed it only prefetches weight tiles into L2, which cannot serve a
+// stale value; every read and write comes after griddepcontrol.wait.
+template <int NT> struct Few {
+    static constexpr int STAGE = 128 * KB + NT * KB;  // bytes: weights, then tokens
+    static constexpr int ST = NT == 16 ? 6 : NT == 32 ? 5 : 4;
+    static constexpr int AS = 4;                      // accumulators
+    static constexpr int COLS = NT * AS;              // TMEM columns (64, 128 or 256)
+    static constexpr int CK = 4, CS = 2;              // K blocks of scales per chunk, chunks in flight
+    static constexpr int SCALES = ST * STAGE;
+    static constexpr int BARS = SCALES + CS * CK * NT * 4;
+    static constexpr int SMEM = BARS + (2 * ST + 2 * AS + 2 * CS) * 8 + 16 + 1024;
+    static_assert(NT * 128 * 4 <= ST * STAGE, "the partial sums take the ring's place");
+};
+
+template <int NT, typename TO>
+__global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constant__ CUtensorMap tm_w,
+                                                         const __grid_constant__ CUtensorMap tm_a,
+                                                         const float *__restrict__ sa, const float *__restrict__ sw,
+                                                         TO *__restrict__ y, int M, int N, int nkb, int64_t ldy, int mt,
+                                                         int S, unsigned *err) {
+    using namespace tc;
+    using F = Few<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + F::BARS), *empty = full + F::ST, *afull = empty + F::ST,
+             *aempty = afull + F::AS, *sfull = aempty + F::AS, *sempty = sfull + F::CS;
+    uint32_t *s_taddr = reinterpret_cast<uint32_t *>(sempty + F::CS);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
+    const int r = (int)(blockIdx.x % (unsigned)S), unit = (int)(blockIdx.x / (unsigned)S);
+    const int nt = unit / mt, n0 = nt * 128, m0 = (unit - nt * mt) * NT;
+    const int k0 = (int)((int64_t)nkb * r / S), k1 = (int)((int64_t)nkb * (r + 1) / S);  // K blocks of this CTA
+    if (tid == 0) {
+        for (int i = 0; i < F::ST; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < F::AS; ++i) {
+            mbar_init(afull + i, 1);
+            mbar_init(aempty + i, 4);
+        }
+        for (int i = 0; i < F::CS; ++i) {
+            mbar_init(sfull + i, 2);
+            mbar_init(sempty + i, 4);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 4 && elect_one()) {
+        tma_prefetch_desc(&tm_w);
+        tma_prefetch_desc(&tm_a);
+        for (int i = 0; i < F::ST && k0 + i < k1; ++i) tma_prefetch_l2_2d(&tm_w, (k0 + i) * KB, n0);
+    }
+    if (warp == 5) {
+        tmem_alloc(s_taddr, F::COLS);
+        tmem_relinquish();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    sync_tc();
+    const uint32_t tbase = *s_taddr, sbase = smem_u32(sm);
+    bool ok = true;
+    float acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = 0.f;
+    if (warp < 4) {
+        const uint32_t trow = tbase + ((uint32_t)(32 * warp) << 16);
+        const float *chunks = reinterpret_cast<const float *>(sm + F::SCALES);
+        int as = 0, cs = 0;
+        uint32_t ph = 0, cph = 0;
+        for (int kb = k0; kb < k1; ++kb) {
+            const int ck = (kb - k0) % F::CK;
+            if (ck == 0) ok = wait_more(sfull + cs, cph, ok);
+            const float *sr = chunks + (cs * F::CK + ck) * NT;
+            ok = wait_more(afull + as, ph, ok);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < NT; c += 16) {
+                uint32_t d[16];
+                tmem_ld16(trow + as * NT + c, d);
+                tmem_ld_wait_for(d);
+                if (c == NT - 16) {  // the accumulator is read: the MMAs may write it again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(aempty + as);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 s = *reinterpret_cast<const float4 *>(sr + c + 4 * q);
+                    acc[c + 4 * q] = fmaf(__uint_as_float(d[4 * q]), s.x, acc[c + 4 * q]);
+                    acc[c + 4 * q + 1] = fmaf(__uint_as_float(d[4 * q + 1]), s.y, acc[c + 4 * q + 1]);
+                    acc[c + 4 * q + 2] = fmaf(__uint_as_float(d[4 * q + 2]), s.z, acc[c + 4 * q + 2]);
+                    acc[c + 4 * q + 3] = fmaf(__uint_as_float(d[4 * q + 3]), s.w, acc[c + 4 * q + 3]);
+                }
+            }
+            if (++as == F::AS) {
+                as = 0;
+                ph ^= 1;
+            }
+            if (ck == F::CK - 1 || kb == k1 - 1) {  // the chunk's last: its slot may be filled again
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sempty + cs);
+                if (++cs == F::CS) {
+                    cs = 0;
+                    cph ^= 1;
+                }
+            }
+        }
+    } else if (warp == 4) {
+        int st = 0;
+        uint32_t ph = 1;  // the ring starts out free
+        for (int kb = k0; kb < k1; ++kb) {
+            ok = wait_more(empty + st, ph, ok);
+            __syncwarp();
+            if (elect_one()) {
+                uint8_t *d = sm + st * F::STAGE;
+                mbar_arrive_expect_tx(full + st, F::STAGE);
+                tma_load_2d(d, &tm_w, full + st, kb * KB, n0);
+                tma_load_2d(d + 128 * KB, &tm_a, full + st, kb * KB, m0);
+            }
+            if (++st == F::ST) {
+                st = 0;
+                ph ^= 1;
+            }
+        }
+        // every copy lands before shared memory is used otherwise or goes away
+        for (int i = 0; i < F::ST; ++i) {
+            if (--st < 0) {
+                st = F::ST - 1;
+                ph ^= 1;
+            }
+            if (!mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
+        }
+    } else if (warp == 5) {
+        int st = 0, as = 0;
+        uint32_t ph = 0, aph = 1;  // the accumulators start out free
+        const uint64_t a0 = sdesc_sw128(sbase, 16, 1024), b0 = sdesc_sw128(sbase + 128 * KB, 16, 1024);
+        for (int kb = k0; kb < k1; ++kb) {
+            const uint64_t a = a0 + (uint64_t)(st * (F::STAGE / 16)), b = b0 + (uint64_t)(st * (F::STAGE / 16));
+            ok = wait_more(full + st, ph, ok);
+            ok = wait_more(aempty + as, aph, ok);
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_f8(tbase + as * NT, a + 2 * ks, b + 2 * ks, idesc_f8(128, NT), ks > 0);
+                mma_commit(empty + st);
+                mma_commit(afull + as);
+            }
+            if (++as == F::AS) {
+                as = 0;
+                aph ^= 1;
+            }
+            if (++st == F::ST) {
+                st = 0;
+                ph ^= 1;
+            }
+        }
+    } else {
+        // the scales' products (tokens past the end take the last one's and are not stored)
+        const float *swp = sw + (int64_t)nt * nkb;
+        float *chunks = reinterpret_cast<float *>(sm + F::SCALES);
+        int cs = 0;
+        uint32_t cph = 1;
+        constexpr int PER = F::CK * NT / 64;  // products of a chunk per lane
+        for (int kc = k0; kc < k1; kc += F::CK) {
+            float av[PER], wv[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int e = tid - 192 + 64 * i, j = e % NT, kb = kc + e / NT < k1 ? kc + e / NT : k1 - 1;
+                av[i] = __ldg(sa + (int64_t)kb * M + (m0 + j < M ? m0 + j : M - 1));
+                wv[i] = __ldg(swp + kb);
+            }
+            ok = wait_more(sempty + cs, cph, ok);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) chunks[cs * F::CK * NT + tid - 192 + 64 * i] = av[i] * wv[i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sfull + cs);
+            if (++cs == F::CS) {
+                cs = 0;
+                cph ^= 1;
+            }
+        }
+    }
+    if (!ok) atomicOr(err, DEVERR_TIMEOUT);
+    sync_tc();
+    if (warp == 5) tmem_dealloc(tbase, F::COLS);
+    const int n = n0 + tid;
+    if (S == 1) {
+        if (warp < 4 && ok && n < N) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (m0 + j < M) Elem<TO>::store(y + (int64_t)(m0 + j) * ldy + n, acc[j]);
+        }
+        return;
+    }
+    // Partial sums [token][feature] in the ring's place; each CTA adds up `per` tokens over the cluster, in
+    // the CTAs' order, all of a token's loads on their way at once.
+    const int per = (NT + S - 1) / S, f = tid & 127;
+    float *part = reinterpret_cast<float *>(sm);
+    if (warp < 4) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) part[j * 128 + tid] = ok ? acc[j] : __uint_as_float(0x7fffffffu);
+    }
+    cluster_sync();
+    for (int j = r * per + (tid >> 7); j < (r + 1) * per && j < NT && m0 + j < M; j += 2) {
+        float v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) v[p] = p < S ? peer_load(part + j * 128 + f, (uint32_t)p) : 0.f;
+        float sum = v[0];
+#pragma unroll
+        for (int p = 1; p < 8; ++p) sum += v[p];
+        if (n0 + f < N) Elem<TO>::store(y + (int64_t)(m0 + j) * ldy + n0 + f, sum);
+    }
+    cluster_sync();  // no CTA leaves while another still reads its sums
+}
+
+// CTAs of a cluster (a split of K) for `units` tiles of nkb K blocks on `slots` CTA slots
+// (two per SM). A split costs about two K blocks' time for the meeting of the partial sums
+// and pays where it fills slots that would stay idle.
+static int few_split(int64_t units, int nkb, int slots) {
+    int best = 1;
+    int64_t cost = INT64_MAX;
+    for (int S = 1; S <= 8 && S <= nkb; ++S) {
+        const int64_t waves = (units * S + slots - 1) / slots, c = waves * ((nkb + S - 1) / S + 4) + (S > 1 ? 2 : 0);
+        if (c < cost) {
+            cost = c;
+            best = S;
+        }
+    }
+    return best;
+}
+
+template <int NT, typename TO>
+static kda_status launch_few(const CUtensorMap &tw, const CUtensorMap &ta, const float *sa, const float *sw, void *y,
+                             int64_t M, int N, int K, int64_t ldy, unsigned *err, cudaStream_t s) {
+    using F = Few<NT>;
+    if (smem_attr_once<linear_few_kernel<NT, TO>>(F::SMEM) != cudaSuccess)
+        return check_launch("linear_few_kernel (shared memory attribute)");
+    const int64_t mt = (M + NT - 1) / NT, units = mt * (((int64_t)N + 127) / 128);
+    const int nkb = (K + KB - 1) / KB, S = few_split(units, nkb, 2 * current_sms());
+    if (units * S > 0x7fffffffLL) return invalid("M*N too large for one launch");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * S));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = F::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)S;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, linear_few_kernel<NT, TO>, tw, ta, sa, sw, static_cast<TO *>(y), (int)M, N, nkb, ldy,
+                       (int)mt, S, err);  // an error is left for check_launch
+    return check_launch("linear_few_kernel");
+}
+
+// ---------------------------------------------------------------- many tokens
+// A pair of CTAs (one cluster, two SMs) owns a 256-token x 256-feature tile:
+// the MMAs of cta_group::2 take 128 token rows and half of the 256 weight rows
+// from each CTA's shared memory, so every operand byte is copied and read once
+// per pair. Each CTA's TMEM holds its 128 tokens (lane = token) in two
+// accumulators of 256 columns, one K block each: 512 cycles of MMAs, in which
+// the other accumulator has to be read and handed back. Per CTA: warps 0-7 join
+// the block sums (warps 0-3 the tile's first 128 features, 4-7 the last; a
+// thread holds 128 fp32 sums of one token, and one product of its token's scale
+// with the features' scale serves the whole K block), warp 8 copies, warp 9 of
+// the even CTA issues the MMAs for both, warps 10 and 11 form the scales'
+// products, four K blocks at a time. Persistent: a pair walks tiles, token
+// tiles first, so that neighbouring pairs share weight tiles in L2, and the next
+// tile's products run while this one's results are stored.
+namespace many {
+constexpr int BM = 256, BN = 256;                 // tile of a pair
+constexpr int A_BYTES = 128 * KB, W_BYTES = 128 * KB;
+constexpr int STAGE = A_BYTES + W_BYTES;          // bytes per CTA: tokens, then weights
+constexpr int ST = 5, AS = 2;
+constexpr int JW = 8, JC = 128;                   // joining warps, features of each
+constexpr int NTHREADS = 32 * (JW + 4);
+// Registers a thread: launched with REGS, split so that the joining warps hold their sums and neither
+// side spills (208 / 88 and 240 / 24 spill inside the K loop: a third slower).
+constexpr int REGS = 168, REGS_JOIN = 216, REGS_ISSUE = 72;
+static_assert(JW * REGS_JOIN + 4 * REGS_ISSUE == (JW + 4) * REGS, "the split draws on the launch's registers");
+constexpr int CK = 4, CS = 4;                     // K blocks of scales per chunk, chunks in flight
+constexpr int CHUNK = CK * 256 * 4;               // [CK][feature half][token] products of the two scales
+constexpr int OUT = ST * STAGE;                   // results on their way out: per joining warp 32 rows of 128 B
+constexpr int SCALES = OUT + JW * 4096;
+constexpr int BARS = SCALES + CS * CHUNK;
+constexpr int SMEM = BARS + (2 * ST + 2 * AS + 2 * CS) * 8 + 16 + 1024;
+}  // namespace many
+
 // copy into this CTA's shared memory, completing on a barrier of the pair's even CTA
 __device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
     asm volatile(
@@ -654,21 +776,20 @@ static bool byte_map(CUtensorMap *m, const void *p, int K, int64_t rows, int64_t
 template <typename TO>
 static kda_status run_linear(const void *a, const float *sa, const void *w, const float *sw, void *y, int64_t M,
                              int N, int K, int64_t lda, int64_t ldw, int64_t ldy, unsigned *err, cudaStream_t s) {
-    if (M > 256) {
+    if (M > 64) {
         CUtensorMap ta, tw;
         if (!byte_map(&ta, a, K, M, lda, 128) || !byte_map(&tw, w, K, N, ldw, 128))
             return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
         return launch_many<TO>(ta, tw, sa, sw, y, M, N, K, ldy, err, s);
     }
-    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     CUtensorMap tw, ta;
     if (!byte_map(&tw, w, K, N, ldw, 128) || !byte_map(&ta, a, K, M, lda, nt))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     switch (nt) {
     case 16: return launch_few<16, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
     case 32: return launch_few<32, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
-    case 64: return launch_few<64, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
-    default: return launch_few<128, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
+    default: return launch_few<64, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
     }
 }
 
