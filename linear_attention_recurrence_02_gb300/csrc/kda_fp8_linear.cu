@@ -335,16 +335,19 @@ __global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constan
     cluster_sync();  // no CTA leaves while another still reads its sums
 }
 
-// CTAs of a cluster (a split of K) for `units` tiles of nkb K blocks on `slots` CTA slots
-// (two per SM). A split costs about two K blocks' time for the meeting of the partial sums
-// and pays where it fills slots that would stay idle.
-static int few_split(int64_t units, int nkb, int slots) {
+// CTAs of a cluster (a split of K) for `units` tiles of nkb K blocks on `slots` CTA slots (two
+// per SM), and the time in ns that this takes where the weights' bytes are not what bounds it.
+// Measured: 410 ns a K block with both slots of an SM busy, 3 us for a wave's start and end,
+// 2 us for the meeting of the partial sums. (1 x 12288 x 4096: 96 tiles, 10.6 us at S = 3, 11.5
+// at 1, 14.0 at 4; 64 x 4096 x 12288: 32 tiles, 13.1 us at 8, 30 at 1.)
+static int few_split(int64_t units, int nkb, int slots, int64_t *ns) {
     int best = 1;
-    int64_t cost = INT64_MAX;
+    *ns = INT64_MAX;
     for (int S = 1; S <= 8 && S <= nkb; ++S) {
-        const int64_t waves = (units * S + slots - 1) / slots, c = waves * ((nkb + S - 1) / S + 4) + (S > 1 ? 2 : 0);
-        if (c < cost) {
-            cost = c;
+        const int64_t waves = (units * S + slots - 1) / slots;
+        const int64_t t = waves * ((int64_t)((nkb + S - 1) / S) * 410 + 3000) + (S > 1 ? 2000 : 0) + 1000;
+        if (t < *ns) {
+            *ns = t;
             best = S;
         }
     }
@@ -358,7 +361,8 @@ static kda_status launch_few(const CUtensorMap &tw, const CUtensorMap &ta, const
     if (smem_attr_once<linear_few_kernel<NT, TO>>(F::SMEM) != cudaSuccess)
         return check_launch("linear_few_kernel (shared memory attribute)");
     const int64_t mt = (M + NT - 1) / NT, units = mt * (((int64_t)N + 127) / 128);
-    const int nkb = (K + KB - 1) / KB, S = few_split(units, nkb, 2 * current_sms());
+    int64_t ns = 0;
+    const int nkb = (K + KB - 1) / KB, S = few_split(units, nkb, 2 * current_sms(), &ns);
     if (units * S > 0x7fffffffLL) return invalid("M*N too large for one launch");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * S));
@@ -776,7 +780,21 @@ static bool byte_map(CUtensorMap *m, const void *p, int K, int64_t rows, int64_t
 template <typename TO>
 static kda_status run_linear(const void *a, const float *sa, const void *w, const float *sw, void *y, int64_t M,
                              int N, int K, int64_t lda, int64_t ldw, int64_t ldy, unsigned *err, cudaStream_t s) {
+    // Up to 64 tokens a weight tile is read once and its bytes bound the call: the few-token kernel. With
+    // more, whichever is estimated faster: CTA pairs take 370 ns a K block, 1 us a tile and 3.5 us a
+    // launch. (Measured few / many: 128 x 4096 x 4096 9.4 / 16.1 us, 256 x 4096 x 4096 13.9 / 16.2,
+    // 512 x 4096 x 4096 17.2 / 16.4, 1024 x 4096 x 4096 33 / 17, 128 x 36864 x 4096 36.9 / 34.4.)
+    bool many_tokens = false;
     if (M > 64) {
+        const int sms = current_sms(), nkb = (K + KB - 1) / KB;
+        if (sms < 2) return fail(KDA_ERR_CUDA, "the device's SM count is unavailable");
+        const int64_t units = ((M + 63) / 64) * (((int64_t)N + 127) / 128), pairs = sms / 2;
+        const int64_t tiles = ((M + many::BM - 1) / many::BM) * (((int64_t)N + many::BN - 1) / many::BN);
+        int64_t few_ns = 0;
+        few_split(units, nkb, 2 * sms, &few_ns);
+        many_tokens = ((tiles + pairs - 1) / pairs) * ((int64_t)nkb * 370 + 1000) + 3500 < few_ns;
+    }
+    if (many_tokens) {
         CUtensorMap ta, tw;
         if (!byte_map(&ta, a, K, M, lda, 128) || !byte_map(&tw, w, K, N, ldw, 128))
             return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");

@@ -15,8 +15,29 @@
 #include <string>
 
 #include "kda_fp8.cuh"
+#include "kda_prefill.cuh"
 
 namespace kda {
+
+// Both are programmatic dependent launches that wait for the kernel before
+// them first thing, then let the kernel behind them start: a kda_fp8_linear
+// that reads their output sets itself up and prefetches its weights meanwhile.
+__device__ __forceinline__ void dependent_launch() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+static void launch_dependent(void (*kern)(P...), unsigned grid, dim3 block, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = block;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kern, args...);  // an error is left for check_launch
+}
 
 // ---------------------------------------------------------------- residual add + RMSNorm
 // A row of N channels is held by blockDim.x threads, VPT vectors of 8
@@ -29,7 +50,7 @@ template <typename TX, typename TR, bool RES, int VPT>
 __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX *x, const TR *res,
                                                                const float *__restrict__ w, TR *sum_out,
                                                                uint8_t *__restrict__ y, float *__restrict__ scales,
-                                                               int64_t T, int N, float eps) {
+                                                               int64_t T, int N, float inv_n, float eps) {
     __shared__ float red[32];
     const int nv = N / 8, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -37,6 +58,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX *x, cons
     const int64_t row = t * (int64_t)N;
     float h[VPT][8];
     float ss = 0.f;
+    dependent_launch();
     Raw8<TX> rx[VPT];
     Raw8<TR> rr[VPT];
 #pragma unroll
@@ -77,7 +99,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX *x, cons
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    const float inv = rms_inv(ss / (float)N + eps);
+    const float inv = rms_inv(fmaf(ss, inv_n, eps));
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
         const int v = c * blockDim.x + threadIdx.x;
@@ -93,8 +115,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX *x, cons
         }
         const float m = block_amax(h[c]);
         if (in) {
-            __stcs(reinterpret_cast<uint2 *>(y + row + 8 * v), codes8(h[c], QMAX / m));
-            if ((v & 15) == 0) scales[(int64_t)(v >> 4) * T + t] = m / QMAX;
+            __stcs(reinterpret_cast<uint2 *>(y + row + 8 * v), codes8(h[c], block_inv(m)));
+            if ((v & 15) == 0) scales[(int64_t)(v >> 4) * T + t] = block_scale(m);
         }
     }
 }
@@ -102,16 +124,22 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX *x, cons
 template <typename TX, typename TR, bool RES>
 static kda_status launch_add(const void *x, const void *res, const float *w, void *sum_out, void *y, float *scales,
                              int64_t T, int N, float eps, cudaStream_t s) {
-    const int nv = N / 8;
-    const int vpt = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
+    // Many rows: about 256 threads a row (512 where an input is fp32, whose vectors take twice the
+    // registers), so that an SM has several rows in flight and one row's reductions hide behind another's
+    // loads. Few rows: as many threads a row as it has vectors, for latency. (8192 x 8192 bf16: 72 us at
+    // four vectors a thread, 82 at two, 90 at one; fp32: 137 at four, 127 at two. 4096 x 4096 bf16: 21.5
+    // at four, 20.6 at two.)
+    const int nv = N / 8, sms = current_sms();
+    const int most = T <= 2 * sms ? 1024 : sizeof(TX) + (RES ? sizeof(TR) : 0) > 4 ? 512 : 256;
+    const int vpt = nv <= most ? 1 : nv <= 2 * most ? 2 : 4;
     const int nt = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
     const int rows = nt >= 128 ? 1 : 128 / nt;
     const int64_t blocks = (T + rows - 1) / rows;
     if (blocks > 0x7fffffffLL) return invalid("T too large for one launch");
-    const dim3 grid((unsigned)blocks), block((unsigned)nt, (unsigned)rows);
     auto go = [&](auto kern) {
-        kern<<<grid, block, 0, s>>>(static_cast<const TX *>(x), static_cast<const TR *>(res), w,
-                                    static_cast<TR *>(sum_out), static_cast<uint8_t *>(y), scales, T, N, eps);
+        launch_dependent(kern, (unsigned)blocks, dim3((unsigned)nt, (unsigned)rows), s, static_cast<const TX *>(x),
+                         static_cast<const TR *>(res), w, static_cast<TR *>(sum_out), static_cast<uint8_t *>(y),
+                         scales, T, N, 1.0f / (float)N, eps);
     };
     if (vpt == 1) go(add_rmsnorm_fp8_kernel<TX, TR, RES, 1>);
     else if (vpt == 2) go(add_rmsnorm_fp8_kernel<TX, TR, RES, 2>);
@@ -130,47 +158,105 @@ static kda_status dispatch_add(bool res_bf16, const void *x, const void *res, co
 }
 
 // ---------------------------------------------------------------- gated RMSNorm
-// A half-warp owns one (token, block of 128 channels): 128 / D whole heads,
-// D / 8 lanes each. The gate's activation is taken with the fast exponential
-// and division (a few ulp, far below the 2^-4 step of e4m3).
+// Eight lanes own one (token, block of 128 channels), 16 channels each, so a
+// head is D / 16 lanes and a shuffle reduction has at most three steps. Issue
+// slots bound the bf16 form, so the per-element work is kept short: products
+// two at a time (f32x2), the gate's activation by the hardware exponential
+// and reciprocal without their handling of denormals (a few ulp, far below the
+// 2^-4 step of e4m3; a gate below about -87 closes fully), three-way maxima.
+// 4096 x 96 heads x 128, bf16: 41.4 us (42.1 without the bound to ten blocks
+// an SM; 45.1 with blocks of 256 threads, 52.2 with 64; 44.1 at best as a
+// persistent grid that loads a unit ahead; 56.5 with 8 channels a lane and one
+// product at a time).
+constexpr int GATED_NT = 128;
+__device__ __forceinline__ float sigmoid_fast(float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 template <int D, typename T, int ACT>
-__global__ void __launch_bounds__(256) gated_rmsnorm_fp8_kernel(const T *__restrict__ o, const T *__restrict__ gate,
+__global__ void __launch_bounds__(GATED_NT, 10) gated_rmsnorm_fp8_kernel(const T *__restrict__ o, const T *__restrict__ gate,
                                                                 const float *__restrict__ w, uint8_t *__restrict__ y,
                                                                 float *__restrict__ scales, int64_t Ttot, int C,
                                                                 int nb, float eps) {
-    const int ln = threadIdx.x & 15;
-    const int64_t unit = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 4;  // t * nb + b
+    const int ln = threadIdx.x & 7;
+    const int64_t unit = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;  // t * nb + b
     const int64_t t = unit / nb;
-    const int b = (int)(unit - t * nb), c = b * QBLOCK + 8 * ln;  // the lane's first channel of the token
+    const int b = (int)(unit - t * nb), c = b * QBLOCK + 16 * ln;  // the lane's first channel of the token
     const bool in = t < Ttot && c < C;
     const int64_t at = t * C + c;
-    float ov[8], gv[8], ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ov[i] = gv[i] = 0.f;
+    dependent_launch();
+    Raw8<T> ro[2], rg[2];
     if (in) {
-        Raw8<T> ro, rg;
-        load8(o + at, ro);
-        load8(gate + at, rg);
-        unpack8(ro, ov);
-        unpack8(rg, gv);
+        load8(o + at, ro[0]);
+        load8(o + at + 8, ro[1]);
+        load8(gate + at, rg[0]);
+        load8(gate + at + 8, rg[1]);
+    }
+    const int j = (16 * ln) % D;
+    float2 v[8], ss = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float f[8];
+        if (in) {
+            unpack8(ro[q], f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[4 * q + i] = make_float2(f[2 * i], f[2 * i + 1]);
+            ss = __ffma2_rn(v[4 * q + i], v[4 * q + i], ss);
+        }
+    }
+    float sum = ss.x + ss.y;
+#pragma unroll
+    for (int m = D / 32; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    const float inv = rms_inv(fmaf(sum, 1.0f / (float)D, eps));
+    float m = QAMAX_MIN;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float z[8];
+        if (in) {
+            unpack8(rg[q], z);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = 0.f;
+        }
+        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + j + 8 * q)),
+                     w1 = __ldg(reinterpret_cast<const float4 *>(w + j + 8 * q) + 1);
+        const float2 wv[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
+                              make_float2(w1.z, w1.w)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 g = make_float2(sigmoid_fast(z[2 * i]), sigmoid_fast(z[2 * i + 1]));
+            if (ACT == KDA_ACT_SILU) g = __fmul2_rn(g, make_float2(z[2 * i], z[2 * i + 1]));
+            float2 &x = v[4 * q + i];
+            x = __fmul2_rn(__fmul2_rn(x, __fmul2_rn(wv[i], make_float2(inv, inv))), g);
+            m = max3(m, fabsf(x.x), fabsf(x.y));
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(ov[i], ov[i], ss);
-#pragma unroll
-    for (int m = D / 16; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    const float inv = rms_inv(ss / (float)D + eps);
-    const int j = (8 * ln) % D;
-    const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + j)), w1 = __ldg(reinterpret_cast<const float4 *>(w + j) + 1);
-    const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float sg = __fdividef(1.0f, 1.0f + __expf(-gv[i]));
-        ov[i] = ov[i] * (wv[i] * inv) * (ACT == KDA_ACT_SILU ? gv[i] * sg : sg);
-    }
-    const float m = block_amax(ov);
+    for (int k = 4; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
     if (in) {
-        __stcs(reinterpret_cast<uint2 *>(y + at), codes8(ov, QMAX / m));
-        if (ln == 0) scales[(int64_t)b * Ttot + t] = m / QMAX;
+        const float bi = block_inv(m);
+        uint32_t code[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 p = __fmul2_rn(v[2 * i], make_float2(bi, bi)), r = __fmul2_rn(v[2 * i + 1], make_float2(bi, bi));
+            code[i] = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3) |
+                      ((uint32_t)__nv_cvt_float2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3) << 16);
+        }
+        __stcs(reinterpret_cast<uint4 *>(y + at), make_uint4(code[0], code[1], code[2], code[3]));
+        if (ln == 0) scales[(int64_t)b * Ttot + t] = block_scale(m);
     }
 }
 
@@ -178,11 +264,11 @@ template <typename T, int ACT>
 static kda_status dispatch_gated(int D, const void *o, const void *gate, const float *w, void *y, float *scales,
                                  int64_t Ttot, int H, float eps, cudaStream_t s) {
     const int C = H * D, nb = (C + QBLOCK - 1) / QBLOCK;
-    const int64_t blocks = (Ttot * nb + 15) / 16;
+    const int64_t blocks = (Ttot * nb + GATED_NT / 8 - 1) / (GATED_NT / 8);
     if (blocks > 0x7fffffffLL) return invalid("T*H*D too large for one launch");
     auto go = [&](auto kern) {
-        kern<<<(unsigned)blocks, 256, 0, s>>>(static_cast<const T *>(o), static_cast<const T *>(gate), w,
-                                              static_cast<uint8_t *>(y), scales, Ttot, C, nb, eps);
+        launch_dependent(kern, (unsigned)blocks, dim3(GATED_NT), s, static_cast<const T *>(o), static_cast<const T *>(gate),
+                         w, static_cast<uint8_t *>(y), scales, Ttot, C, nb, eps);
     };
     switch (D) {
     case 16: go(gated_rmsnorm_fp8_kernel<16, T, ACT>); break;

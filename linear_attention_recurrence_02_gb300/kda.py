@@ -295,34 +295,44 @@ def kda_gated_rmsnorm(o, gate, weight, y, act="sigmoid", eps=1e-6, stream=None):
                                    _ACTS[act], float(eps), _stream(stream, o.device)))
 
 
-def _fp8_args(dev, codes, floats):
-    """Checks of the 8-bit operators: every tensor on device `dev`, e4m3 codes, fp32 scales and weights."""
-    import torch
-    for t in codes:
-        if t.dtype != torch.float8_e4m3fn:
-            raise TypeError("8-bit codes must be torch.float8_e4m3fn")
-        if t.device != dev:
-            raise ValueError("tensors must be on one CUDA device")
-    for t in floats:
-        if t.dtype != torch.float32:
-            raise TypeError("scales and norm weights must be float32")
-        if t.device != dev:
-            raise ValueError("tensors must be on one CUDA device")
+class _Fast:
+    """What the 8-bit operators' calls need each time, looked up once: torch's types, its stream lookup by
+    device index, and the library's functions. A single decode step spends more time on the host than on
+    the GPU, so these bindings read each tensor's attributes once and call no helpers."""
+
+    def __init__(self):
+        import torch
+        self.f8, self.f32 = torch.float8_e4m3fn, torch.float32
+        self.codes = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.current_device = torch.cuda.current_device
+        self.device = torch.cuda.device
+        handle = lib()
+        self.add_rmsnorm, self.gated_rmsnorm, self.linear = \
+            handle.kda_add_rmsnorm_fp8, handle.kda_gated_rmsnorm_fp8, handle.kda_fp8_linear
 
 
-def _on_device(fn, stream, dev, *args):
-    """fn(*args, stream) on `stream`, or on the current stream of `dev` with that device current (the
+_fast = None
+
+
+def _on_device(f, fn, stream, dev, *args):
+    """fn(*args, stream) on `stream`, or on the current stream of device `dev` with that device current (the
     handle of a default stream does not name its device)."""
-    import torch
-    if stream is None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
-        return
-    _check(fn(*args, _stream(stream, dev)))
+    if stream is not None:
+        status = fn(*args, stream.cuda_stream)
+    elif dev == f.current_device():
+        status = fn(*args, f.raw_stream(dev))
+    else:
+        with f.device(dev):
+            status = fn(*args, f.raw_stream(dev))
+    if status != KDA_OK:
+        _check(status)
 
 
-def _blocks128(n):
-    return (n + 127) // 128
+def _not_on(dev):
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    raise ValueError("tensors must be contiguous and on one CUDA device")
 
 
 def kda_add_rmsnorm_fp8(x, weight, y, scales, residual=None, sum_out=None, eps=1e-6, stream=None):
@@ -330,68 +340,113 @@ def kda_add_rmsnorm_fp8(x, weight, y, scales, residual=None, sum_out=None, eps=1
     or bf16, or None (h = x); weight [N] fp32; sum_out receives h (residual's shape and type; may be
     residual, or x where the types agree), or None; y [T,N] float8_e4m3fn; scales [ceil(N/128),T] fp32
     with y about code * scales[channel // 128, token]."""
-    T, N = x.shape
-    if weight.shape != (N,) or y.shape != (T, N) or scales.shape != (_blocks128(N), T) \
-            or (residual is not None and residual.shape != (T, N)) \
-            or (sum_out is not None and sum_out.shape != (T, N)):
+    global _fast
+    f = _fast
+    if f is None:
+        f = _fast = _Fast()
+    shape = x.shape
+    T, N = shape
+    if weight.shape != (N,) or y.shape != shape or scales.shape != ((N + 127) // 128, T):
         raise ValueError("shape mismatch")
-    dev = x.device
-    _fp8_args(dev, (y,), (weight, scales))
-    code = res = _dtype_code(x)
-    for t in (residual, sum_out):
-        if t is not None and t.device != dev:
-            raise ValueError("tensors must be on one CUDA device")
+    if y.dtype is not f.f8:
+        raise TypeError("8-bit codes must be torch.float8_e4m3fn")
+    if weight.dtype is not f.f32 or scales.dtype is not f.f32:
+        raise TypeError("scales and norm weights must be float32")
+    code = res = f.codes.get(x.dtype, -1)
+    dev = x.get_device()
+    rp = sp = None
+    if code < 0:
+        raise TypeError("unsupported dtype; use float32 or bfloat16")
+    ok = dev >= 0
     if residual is not None:
-        res = _dtype_code(residual)
-        if sum_out is not None and sum_out.dtype != residual.dtype:
+        if residual.shape != shape:
+            raise ValueError("shape mismatch")
+        res = f.codes.get(residual.dtype, -1)
+        ok = ok and residual.get_device() == dev and residual.is_contiguous()
+        rp = residual.data_ptr()
+    if sum_out is not None:
+        if sum_out.shape != shape:
+            raise ValueError("shape mismatch")
+        if residual is None:
+            res = f.codes.get(sum_out.dtype, -1)
+        elif sum_out.dtype is not residual.dtype:
             raise TypeError("sum_out must have residual's dtype")
-    elif sum_out is not None:
-        res = _dtype_code(sum_out)
-    _on_device(lib().kda_add_rmsnorm_fp8, stream, dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(sum_out), _ptr(y),
-               _ptr(scales), T, N, code, res, float(eps))
+        ok = ok and sum_out.get_device() == dev and sum_out.is_contiguous()
+        sp = sum_out.data_ptr()
+    if not (ok and weight.get_device() == y.get_device() == scales.get_device() == dev and x.is_contiguous()
+            and weight.is_contiguous() and y.is_contiguous() and scales.is_contiguous()):
+        _not_on(dev)
+    if res < 0:
+        raise TypeError("unsupported dtype; use float32 or bfloat16")
+    _on_device(f, f.add_rmsnorm, stream, dev, x.data_ptr(), rp, weight.data_ptr(), sp, y.data_ptr(),
+               scales.data_ptr(), T, N, code, res, eps)
 
 
 def kda_gated_rmsnorm_fp8(o, gate, weight, y, scales, act="sigmoid", eps=1e-6, stream=None):
     """kda_gated_rmsnorm with its output in 8 bits. o, gate [T,H,D]; weight [D] fp32; y [T,H,D]
     float8_e4m3fn; scales [ceil(H*D/128),T] fp32, one per token and 128 of its H * D channels."""
-    T, H, D = o.shape
-    if gate.shape != (T, H, D) or y.shape != (T, H, D) or weight.shape != (D,) \
-            or scales.shape != (_blocks128(H * D), T):
+    global _fast
+    f = _fast
+    if f is None:
+        f = _fast = _Fast()
+    shape = o.shape
+    T, H, D = shape
+    if gate.shape != shape or y.shape != shape or weight.shape != (D,) or scales.shape != ((H * D + 127) // 128, T):
         raise ValueError("shape mismatch")
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    if gate.dtype != o.dtype or gate.device != o.device:
-        raise TypeError("gate must have o's dtype and device")
-    _fp8_args(o.device, (y,), (weight, scales))
-    _on_device(lib().kda_gated_rmsnorm_fp8, stream, o.device, _ptr(o), _ptr(gate), _ptr(weight), _ptr(y),
-               _ptr(scales), T, H, D, _dtype_code(o), _ACTS[act], float(eps))
+    if gate.dtype is not o.dtype:
+        raise TypeError("gate must have o's dtype")
+    if y.dtype is not f.f8:
+        raise TypeError("8-bit codes must be torch.float8_e4m3fn")
+    if weight.dtype is not f.f32 or scales.dtype is not f.f32:
+        raise TypeError("scales and norm weights must be float32")
+    code = f.codes.get(o.dtype, -1)
+    if code < 0:
+        raise TypeError("unsupported dtype; use float32 or bfloat16")
+    dev = o.get_device()
+    if not (dev >= 0 and gate.get_device() == weight.get_device() == y.get_device() == scales.get_device() == dev
+            and o.is_contiguous() and gate.is_contiguous() and weight.is_contiguous() and y.is_contiguous()
+            and scales.is_contiguous()):
+        _not_on(dev)
+    _on_device(f, f.gated_rmsnorm, stream, dev, o.data_ptr(), gate.data_ptr(), weight.data_ptr(), y.data_ptr(),
+               scales.data_ptr(), T, H, D, code, _ACTS[act], eps)
 
 
-def _rows(t, n):
-    """(pointer, row stride in elements) of a matrix whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _row_stride(t, rows, n):
+    """Row stride in elements of a [rows, n] matrix whose rows are contiguous."""
+    ld, inner = t.stride()
+    if inner != 1 and n > 1:
         raise ValueError("rows must be contiguous")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else n)
+    return ld if rows > 1 else n
 
 
 def kda_fp8_linear(a, a_scales, w, w_scales, y, stream=None):
     """y[m,n] = sum_k a[m,k] a_scales[k//128,m] * w[n,k] w_scales[n//128,k//128]. a [M,K], w [N,K]
     float8_e4m3fn (rows contiguous, row strides multiples of 16); a_scales [ceil(K/128),M] and w_scales
     [ceil(N/128),ceil(K/128)] fp32; y [M,N] bf16 or fp32 (rows contiguous)."""
+    global _fast
+    f = _fast
+    if f is None:
+        f = _fast = _Fast()
     M, K = a.shape
-    N = w.shape[0]
-    kb = _blocks128(K)
-    if w.shape[1] != K or y.shape != (M, N) or a_scales.shape != (kb, M) or w_scales.shape != (_blocks128(N), kb):
+    N, Kw = w.shape
+    kb = (K + 127) // 128
+    if Kw != K or y.shape != (M, N) or a_scales.shape != (kb, M) or w_scales.shape != ((N + 127) // 128, kb):
         raise ValueError("shape mismatch")
-    dev = a.device
-    _fp8_args(dev, (a, w), (a_scales, w_scales))
-    if y.device != dev:
-        raise ValueError("tensors must be on one CUDA device")
-    (pa, lda), (pw, ldw), (py, ldy) = _rows(a, K), _rows(w, K), _rows(y, N)
-    _on_device(lib().kda_fp8_linear, stream, dev, pa, _ptr(a_scales), pw, _ptr(w_scales), py, M, N, K, lda, ldw,
-               ldy, _dtype_code(y))
+    if a.dtype is not f.f8 or w.dtype is not f.f8:
+        raise TypeError("8-bit codes must be torch.float8_e4m3fn")
+    if a_scales.dtype is not f.f32 or w_scales.dtype is not f.f32:
+        raise TypeError("scales and norm weights must be float32")
+    code = f.codes.get(y.dtype, -1)
+    if code < 0:
+        raise TypeError("unsupported dtype; use float32 or bfloat16")
+    dev = a.get_device()
+    if not (dev >= 0 and w.get_device() == a_scales.get_device() == w_scales.get_device() == y.get_device() == dev
+            and a_scales.is_contiguous() and w_scales.is_contiguous()):
+        _not_on(dev)
+    _on_device(f, f.linear, stream, dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+               y.data_ptr(), M, N, K, _row_stride(a, M, K), _row_stride(w, N, K), _row_stride(y, M, N), code)
 
 
 def kda_chunk_prefill_epi(q, k, v, g, beta, out, out_gate, norm_weight, gate="channel", act="sigmoid",
