@@ -345,6 +345,44 @@ kda_status kda_shortconv_decode_step_epi(const void *x, void *ring, const float 
                                          float norm_eps, unsigned flags, kda_stream_t stream);
 
 /*
+ * A layer's way out in one call: kda_shortconv_decode_step_ex, then
+ * kda_gated_rmsnorm_fp8 on its output, then the output projection by
+ * kda_fp8_linear.
+ *   proj [Nout,H*D] e4m3; proj_scales [ceil(Nout/128),ceil(H*D/128)] fp32
+ *   y [B,Nout] dtype: the projected output; it may not alias another argument
+ *   workspace: kda_shortconv_decode_step_proj_workspace_bytes(B, H, D) bytes,
+ *     scratch (the step's output in dtype, its codes and scales). Calls that
+ *     may overlap on the GPU need workspaces of their own.
+ * Other arguments and errors as the three calls; all of them are checked
+ * before the first launch. B = 0 is a no-op.
+ */
+kda_status kda_shortconv_decode_step_proj(const void *x, void *ring, const float *w, const float *g,
+                                          const float *beta, float *state, const void *out_gate,
+                                          const float *norm_weight, const void *proj, const float *proj_scales,
+                                          void *y, int B, int H, int D, int Nout, kda_dtype dtype, kda_gate gate,
+                                          kda_gate_act act, float l2_eps, float norm_eps, unsigned flags,
+                                          void *workspace, size_t workspace_bytes, kda_stream_t stream);
+size_t kda_shortconv_decode_step_proj_workspace_bytes(int B, int H, int D);
+
+/*
+ * The same for a prompt batch: kda_chunk_prefill_gated, then
+ * kda_gated_rmsnorm_fp8 on its output, then the output projection.
+ *   y [T,Nout] dtype; workspace: kda_chunk_prefill_proj_workspace_bytes(T, N,
+ *   H, D, C) bytes (the prefill's own workspace included), scratch.
+ * Sequences that the prefill skips (invalid cu_seqlens, reported by
+ * kda_sync_status) leave their rows of y undefined. T = 0 only passes the
+ * states through. Other arguments and errors as the three calls; all of them
+ * are checked before the first launch.
+ */
+kda_status kda_chunk_prefill_proj(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                  const float *initial_state, float *final_state, const int64_t *cu_seqlens, int N,
+                                  int64_t T, int H, int D, int C, kda_dtype dtype, kda_gate gate, float l2_eps,
+                                  const void *out_gate, const float *norm_weight, kda_gate_act act, float norm_eps,
+                                  const void *proj, const float *proj_scales, void *y, int Nout, void *workspace,
+                                  size_t workspace_bytes, kda_stream_t stream);
+size_t kda_chunk_prefill_proj_workspace_bytes(int64_t total_tokens, int num_seqs, int H, int D, int C);
+
+/*
  * Chunked prefill of ONE sequence of T tokens, split into `segments` runs of
  * whole chunks that are processed side by side ([G] section 5: each chunk
  * step is affine in the state, S <- A S + B with A acting on the key axis,

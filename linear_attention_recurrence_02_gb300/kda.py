@@ -81,6 +81,11 @@ _SIGNATURES = {
     "kda_add_rmsnorm_fp8": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _cf, _vp], _ci),
     "kda_gated_rmsnorm_fp8": ([_vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _ci, _cf, _vp], _ci),
     "kda_fp8_linear": ([_vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _i64, _i64, _i64, _ci, _vp], _ci),
+    "kda_shortconv_decode_step_proj": ([_vp] * 11 + [_ci] * 7 + [_cf, _cf, ctypes.c_uint, _vp, _sz, _vp], _ci),
+    "kda_shortconv_decode_step_proj_workspace_bytes": ([_ci, _ci, _ci], _sz),
+    "kda_chunk_prefill_proj": ([_vp] * 8 + [_ci, _i64, _ci, _ci, _ci, _ci, _ci, _cf, _vp, _vp, _ci, _cf, _vp, _vp, _vp,
+                                _ci, _vp, _sz, _vp], _ci),
+    "kda_chunk_prefill_proj_workspace_bytes": ([_i64, _ci, _ci, _ci, _ci], _sz),
     "kda_chunk_prefill_scan_workspace_bytes": ([_i64, _ci, _ci, _ci, _ci], _sz),
     "kda_chunk_prefill_split": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _ci, _i64, _ci, _ci, _ci, _ci,
                                  _ci, _cf, _vp, _sz, _vp], _ci),
@@ -447,6 +452,92 @@ def kda_fp8_linear(a, a_scales, w, w_scales, y, stream=None):
         _not_on(dev)
     _on_device(f, f.linear, stream, dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
                y.data_ptr(), M, N, K, _row_stride(a, M, K), _row_stride(w, N, K), _row_stride(y, M, N), code)
+
+
+def _check_proj(out_gate, norm_weight, proj, proj_scales, y, lead, H, D, x):
+    """Shapes, types and devices of the output projection's arguments; returns Nout."""
+    import torch
+    Nout = proj.shape[0]
+    if tuple(out_gate.shape) != (lead, H, D) or tuple(norm_weight.shape) != (D,) \
+            or tuple(proj.shape) != (Nout, H * D) or tuple(y.shape) != (lead, Nout) \
+            or tuple(proj_scales.shape) != ((Nout + 127) // 128, (H * D + 127) // 128):
+        raise ValueError("shape mismatch")
+    if proj.dtype != torch.float8_e4m3fn:
+        raise TypeError("8-bit codes must be torch.float8_e4m3fn")
+    if proj_scales.dtype != torch.float32 or norm_weight.dtype != torch.float32:
+        raise TypeError("scales and norm weights must be float32")
+    if out_gate.dtype != x.dtype or y.dtype != x.dtype:
+        raise TypeError("out_gate and y must have the inputs' dtype")
+    for t in (out_gate, norm_weight, proj, proj_scales, y):
+        if t.device != x.device:
+            raise ValueError("tensors must be on one CUDA device")
+    return Nout
+
+
+def _proj_workspace(workspace, need, device):
+    """The caller's workspace and its size, or one allocated here when None."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def kda_shortconv_decode_step_proj(x, ring, w, g, beta, state, out_gate, norm_weight, proj, proj_scales, y,
+                                   gate="channel", act="sigmoid", l2_eps=1e-6, norm_eps=1e-6, overlap_prev=False,
+                                   workspace=None, stream=None):
+    """Fused short conv + decode step, gated RMSNorm in 8 bits and output projection in one call. proj
+    [Nout,H*D] float8_e4m3fn with proj_scales [ceil(Nout/128),ceil(H*D/128)] fp32; y [B,Nout] like x;
+    workspace: a device uint8 tensor of kda_shortconv_decode_step_proj_workspace_bytes (allocated here when
+    None); other arguments as kda_shortconv_decode_step_epi."""
+    B, P, H, D = x.shape
+    code = _check_gate(g, gate, (B,), H, D)
+    if P != 3 or tuple(ring.shape) != (B, 3, H, 3, D) or tuple(w.shape) != (3, H, D, 4) \
+            or tuple(beta.shape) != (B, H) or tuple(state.shape) != (B, H, D, D):
+        raise ValueError("shape mismatch")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, B, H, D, x)
+    workspace, size = _proj_workspace(workspace, kda_shortconv_decode_step_proj_workspace_bytes(B, H, D), x.device)
+    flags = KDA_DECODE_OVERLAP_PREV if overlap_prev else 0
+    _check(lib().kda_shortconv_decode_step_proj(
+        _ptr(x), _ptr(ring), _ptr(w), _ptr(g), _ptr(beta), _ptr(state), _ptr(out_gate), _ptr(norm_weight), _ptr(proj),
+        _ptr(proj_scales), _ptr(y), B, H, D, Nout, _dtype_code(x), code, _ACTS[act], float(l2_eps), float(norm_eps),
+        flags, _ptr(workspace), size, _stream(stream, x.device)))
+
+
+def kda_shortconv_decode_step_proj_workspace_bytes(B, H, D) -> int:
+    return int(lib().kda_shortconv_decode_step_proj_workspace_bytes(B, H, D))
+
+
+def kda_chunk_prefill_proj(q, k, v, g, beta, out_gate, norm_weight, proj, proj_scales, y, gate="channel",
+                           act="sigmoid", norm_eps=1e-6, initial_state=None, final_state=None, cu_seqlens=None,
+                           chunk_size=64, l2_eps=1e-6, workspace=None, stream=None):
+    """Chunked prefill, gated RMSNorm in 8 bits and output projection in one call. proj, proj_scales as
+    kda_shortconv_decode_step_proj; y [T,Nout] like q; workspace: a device uint8 tensor of
+    kda_chunk_prefill_proj_workspace_bytes (allocated here when None); other arguments as
+    kda_chunk_prefill_epi."""
+    T, H, D = q.shape
+    code = _check_gate(g, gate, (T,), H, D)
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if tuple(k.shape) != (T, H, D) or tuple(v.shape) != (T, H, D) or tuple(beta.shape) != (T, H):
+        raise ValueError("shape mismatch")
+    for st in (initial_state, final_state):
+        if st is not None and st.numel() != N * H * D * D:
+            raise ValueError("state shape mismatch")
+    Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, T, H, D, q)
+    workspace, size = _proj_workspace(workspace, kda_chunk_prefill_proj_workspace_bytes(T, N, H, D, chunk_size),
+                                      q.device)
+    _check(lib().kda_chunk_prefill_proj(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens), N, T,
+        H, D, chunk_size, _dtype_code(q), code, float(l2_eps), _ptr(out_gate), _ptr(norm_weight), _ACTS[act],
+        float(norm_eps), _ptr(proj), _ptr(proj_scales), _ptr(y), Nout, _ptr(workspace), size,
+        _stream(stream, q.device)))
+
+
+def kda_chunk_prefill_proj_workspace_bytes(total_tokens, num_seqs, H, D, C) -> int:
+    return int(lib().kda_chunk_prefill_proj_workspace_bytes(total_tokens, num_seqs, H, D, C))
 
 
 def kda_chunk_prefill_epi(q, k, v, g, beta, out, out_gate, norm_weight, gate="channel", act="sigmoid",

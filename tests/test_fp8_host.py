@@ -160,3 +160,72 @@ def test_fp64_statements():
     sa, sw = rng.uniform(0.5, 2, (2, 3)), rng.uniform(0.5, 2, (2, 2))
     full = (a * _fp8.per_channel(sa, 144)) @ (w * np.repeat(np.repeat(sw, 128, 0)[:130], 128, 1)[:, :144]).T
     assert np.allclose(_fp8.linear(a, sa, w, sw)[0], full)
+
+
+_DECODE_PROJ = dict(x=0x10000, ring=0x20000, w=0x30000, g=0x40000, beta=0x50000, state=0x60000, og=0x70000,
+                    nw=0x80000, proj=0x90000, ps=0xa0000, y=0xb0000, B=2, H=3, D=128, Nout=100, dtype=1, gate=0, act=0,
+                    l2=1e-6, eps=1e-6, flags=0, ws=0xc0000, wsz=1 << 20)
+
+
+@pytest.mark.parametrize("case,detail", [
+    (dict(B=-1), "B must be"),
+    (dict(H=0), "H must be"),
+    (dict(D=40), "D must be"),
+    (dict(Nout=0), "Nout must be"),
+    (dict(dtype=4), "dtype must be"),
+    (dict(act=3), "act must be"),
+    (dict(eps=-1.0), "norm_eps must be"),
+    (dict(wsz=100), "workspace too small"),
+    (dict(ws=None), "workspace is NULL"),
+    (dict(og=None), "out_gate is NULL"),
+    (dict(ps=0xa0004), "proj_scales is not 16-byte aligned"),
+    (dict(y=0x10000), "y must not alias"),
+    (dict(y=0x90000), "y must not alias"),
+    (dict(flags=2), "flags"),
+    (dict(gate=9), "gate must be"),
+    (dict(beta=None), "beta is NULL"),
+])
+def test_decode_proj_refusals(kda, case, detail):
+    """Refused before the first launch, the later calls' arguments as well as the step's own."""
+    a = dict(_DECODE_PROJ)
+    a.update(case)
+    _refused(kda, kda.lib().kda_shortconv_decode_step_proj(
+        a["x"], a["ring"], a["w"], a["g"], a["beta"], a["state"], a["og"], a["nw"], a["proj"], a["ps"], a["y"], a["B"],
+        a["H"], a["D"], a["Nout"], a["dtype"], a["gate"], a["act"], a["l2"], a["eps"], a["flags"], a["ws"], a["wsz"],
+        None), detail)
+
+
+@pytest.mark.parametrize("case,detail", [
+    (dict(N=0), "N must be"),
+    (dict(T=-1), "tokens must be"),
+    (dict(C=65), "C must be"),
+    (dict(Nout=0), "Nout must be"),
+    (dict(act=-1), "act must be"),
+    (dict(wsz=1000), "workspace too small"),
+    (dict(proj=None), "proj is NULL"),
+    (dict(nw=0x80008), "norm_weight is not 16-byte aligned"),
+    (dict(y=0x10000), "y must not alias"),
+    (dict(N=2), "cu_seqlens is NULL"),
+    (dict(k=None), "k is NULL"),
+])
+def test_prefill_proj_refusals(kda, case, detail):
+    a = dict(q=0x10000, k=0x20000, v=0x30000, g=0x40000, beta=0x50000, N=1, T=10, H=3, D=128, C=64, dtype=1, gate=0,
+             og=0x70000, nw=0x80000, act=0, proj=0x90000, ps=0xa0000, y=0xb0000, Nout=100, ws=0xc0000, wsz=1 << 20)
+    a.update(case)
+    _refused(kda, kda.lib().kda_chunk_prefill_proj(
+        a["q"], a["k"], a["v"], a["g"], a["beta"], None, None, None, a["N"], a["T"], a["H"], a["D"], a["C"], a["dtype"],
+        a["gate"], 1e-6, a["og"], a["nw"], a["act"], 1e-6, a["proj"], a["ps"], a["y"], a["Nout"], a["ws"], a["wsz"],
+        None), detail)
+
+
+def test_proj_workspace_sizes(kda):
+    """The output in fp32, its codes and its scales, each rounded up to 256 bytes, and the prefill's own."""
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    want = up(5 * 3 * 64 * 4) + up(5 * 3 * 64) + up(2 * 5 * 4)
+    assert kda.kda_shortconv_decode_step_proj_workspace_bytes(5, 3, 64) == want
+    assert kda.kda_shortconv_decode_step_proj_workspace_bytes(0, 3, 64) == 0
+    assert kda.kda_chunk_prefill_proj_workspace_bytes(5, 1, 3, 64, 64) == want
+    assert kda.kda_chunk_prefill_proj_workspace_bytes(5, 8, 3, 64, 64) == want + 256
+    L = kda.lib()
+    assert L.kda_shortconv_decode_step_proj(*[None] * 11, 0, 3, 128, 100, 1, 0, 0, 1e-6, 1e-6, 0, None, 0,
+                                            None) == kda.KDA_OK
