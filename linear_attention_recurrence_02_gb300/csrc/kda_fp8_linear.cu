@@ -512,6 +512,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    // A programmatic dependent launch, as the few-token kernel: before the wait only weight tiles move, to L2.
+    if (warp == JW && elect_one()) {
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_w);
+        for (int kb = 0; kb < ST && kb < nkb; ++kb)
+            tma_prefetch_l2_2d(&tm_w, kb * KB, (int)(pair / mt) * BN + (int)rank * 128);
+    }
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -765,9 +773,18 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
                                     (uint64_t)N, (uint64_t)M, (uint64_t)ldy * sizeof(TO), 128 / sizeof(TO), 32,
                                     CU_TENSOR_MAP_SWIZZLE_128B))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    linear_many_kernel<TO><<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), many::NTHREADS, many::SMEM, s>>>(
-        ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy, (unsigned)mt, (unsigned)tiles,
-        by_tma, err);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(many::NTHREADS);
+    cfg.dynamicSmemBytes = many::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, linear_many_kernel<TO>, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N,
+                       (K + KB - 1) / KB, ldy, (unsigned)mt, (unsigned)tiles, by_tma, err);  // an error is left for check_launch
     return check_launch("linear_many_kernel");
 }
 

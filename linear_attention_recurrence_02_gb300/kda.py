@@ -300,44 +300,44 @@ def kda_gated_rmsnorm(o, gate, weight, y, act="sigmoid", eps=1e-6, stream=None):
                                    _ACTS[act], float(eps), _stream(stream, o.device)))
 
 
-class _Fast:
-    """What the 8-bit operators' calls need each time, looked up once: torch's types, its stream lookup by
-    device index, and the library's functions. A single decode step spends more time on the host than on
-    the GPU, so these bindings read each tensor's attributes once and call no helpers."""
+_calls = None
 
-    def __init__(self):
+
+def _fastcall():
+    """The extension that checks the 8-bit operators' tensors and calls the library (raises if not built)."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
         import torch
-        self.f8, self.f32 = torch.float8_e4m3fn, torch.float32
-        self.codes = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
-        self.current_device = torch.cuda.current_device
-        self.device = torch.cuda.device
+        path = _build.FASTCALL
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        spec = importlib.util.spec_from_loader(
+            "kda_fastcall", importlib.machinery.ExtensionFileLoader("kda_fastcall", path))
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
         handle = lib()
-        self.add_rmsnorm, self.gated_rmsnorm, self.linear = \
-            handle.kda_add_rmsnorm_fp8, handle.kda_gated_rmsnorm_fp8, handle.kda_fp8_linear
+        mod.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in (handle.kda_add_rmsnorm_fp8,
+                                                                     handle.kda_gated_rmsnorm_fp8,
+                                                                     handle.kda_fp8_linear)),
+                  torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch._C._cuda_getDevice,
+                  torch._C._cuda_getCurrentRawStream)
+        _calls = mod
+    return _calls
 
 
-_fast = None
-
-
-def _on_device(f, fn, stream, dev, *args):
-    """fn(*args, stream) on `stream`, or on the current stream of device `dev` with that device current (the
-    handle of a default stream does not name its device)."""
-    if stream is not None:
-        status = fn(*args, stream.cuda_stream)
-    elif dev == f.current_device():
-        status = fn(*args, f.raw_stream(dev))
-    else:
-        with f.device(dev):
-            status = fn(*args, f.raw_stream(dev))
+def _settle(status, fn, device, *args):
+    """A call's status other than KDA_OK: an error, or (-1) tensors on another device than the current one
+    and no stream given: the call again with that device current (the handle of a default stream does not
+    name its device)."""
+    if status == -1:
+        import torch
+        with torch.cuda.device(device):
+            status = fn(*args)
     if status != KDA_OK:
         _check(status)
-
-
-def _not_on(dev):
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    raise ValueError("tensors must be contiguous and on one CUDA device")
 
 
 def kda_add_rmsnorm_fp8(x, weight, y, scales, residual=None, sum_out=None, eps=1e-6, stream=None):
@@ -345,113 +345,32 @@ def kda_add_rmsnorm_fp8(x, weight, y, scales, residual=None, sum_out=None, eps=1
     or bf16, or None (h = x); weight [N] fp32; sum_out receives h (residual's shape and type; may be
     residual, or x where the types agree), or None; y [T,N] float8_e4m3fn; scales [ceil(N/128),T] fp32
     with y about code * scales[channel // 128, token]."""
-    global _fast
-    f = _fast
-    if f is None:
-        f = _fast = _Fast()
-    shape = x.shape
-    T, N = shape
-    if weight.shape != (N,) or y.shape != shape or scales.shape != ((N + 127) // 128, T):
-        raise ValueError("shape mismatch")
-    if y.dtype is not f.f8:
-        raise TypeError("8-bit codes must be torch.float8_e4m3fn")
-    if weight.dtype is not f.f32 or scales.dtype is not f.f32:
-        raise TypeError("scales and norm weights must be float32")
-    code = res = f.codes.get(x.dtype, -1)
-    dev = x.get_device()
-    rp = sp = None
-    if code < 0:
-        raise TypeError("unsupported dtype; use float32 or bfloat16")
-    ok = dev >= 0
-    if residual is not None:
-        if residual.shape != shape:
-            raise ValueError("shape mismatch")
-        res = f.codes.get(residual.dtype, -1)
-        ok = ok and residual.get_device() == dev and residual.is_contiguous()
-        rp = residual.data_ptr()
-    if sum_out is not None:
-        if sum_out.shape != shape:
-            raise ValueError("shape mismatch")
-        if residual is None:
-            res = f.codes.get(sum_out.dtype, -1)
-        elif sum_out.dtype is not residual.dtype:
-            raise TypeError("sum_out must have residual's dtype")
-        ok = ok and sum_out.get_device() == dev and sum_out.is_contiguous()
-        sp = sum_out.data_ptr()
-    if not (ok and weight.get_device() == y.get_device() == scales.get_device() == dev and x.is_contiguous()
-            and weight.is_contiguous() and y.is_contiguous() and scales.is_contiguous()):
-        _not_on(dev)
-    if res < 0:
-        raise TypeError("unsupported dtype; use float32 or bfloat16")
-    _on_device(f, f.add_rmsnorm, stream, dev, x.data_ptr(), rp, weight.data_ptr(), sp, y.data_ptr(),
-               scales.data_ptr(), T, N, code, res, eps)
+    fn = (_calls or _fastcall()).add_rmsnorm
+    status = fn(x, weight, y, scales, residual, sum_out, eps, stream)
+    if status:
+        _settle(status, fn, x.device, x, weight, y, scales, residual, sum_out, eps, stream)
 
 
 def kda_gated_rmsnorm_fp8(o, gate, weight, y, scales, act="sigmoid", eps=1e-6, stream=None):
     """kda_gated_rmsnorm with its output in 8 bits. o, gate [T,H,D]; weight [D] fp32; y [T,H,D]
     float8_e4m3fn; scales [ceil(H*D/128),T] fp32, one per token and 128 of its H * D channels."""
-    global _fast
-    f = _fast
-    if f is None:
-        f = _fast = _Fast()
-    shape = o.shape
-    T, H, D = shape
-    if gate.shape != shape or y.shape != shape or weight.shape != (D,) or scales.shape != ((H * D + 127) // 128, T):
-        raise ValueError("shape mismatch")
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    if gate.dtype is not o.dtype:
-        raise TypeError("gate must have o's dtype")
-    if y.dtype is not f.f8:
-        raise TypeError("8-bit codes must be torch.float8_e4m3fn")
-    if weight.dtype is not f.f32 or scales.dtype is not f.f32:
-        raise TypeError("scales and norm weights must be float32")
-    code = f.codes.get(o.dtype, -1)
-    if code < 0:
-        raise TypeError("unsupported dtype; use float32 or bfloat16")
-    dev = o.get_device()
-    if not (dev >= 0 and gate.get_device() == weight.get_device() == y.get_device() == scales.get_device() == dev
-            and o.is_contiguous() and gate.is_contiguous() and weight.is_contiguous() and y.is_contiguous()
-            and scales.is_contiguous()):
-        _not_on(dev)
-    _on_device(f, f.gated_rmsnorm, stream, dev, o.data_ptr(), gate.data_ptr(), weight.data_ptr(), y.data_ptr(),
-               scales.data_ptr(), T, H, D, code, _ACTS[act], eps)
-
-
-def _row_stride(t, rows, n):
-    """Row stride in elements of a [rows, n] matrix whose rows are contiguous."""
-    ld, inner = t.stride()
-    if inner != 1 and n > 1:
-        raise ValueError("rows must be contiguous")
-    return ld if rows > 1 else n
+    fn = (_calls or _fastcall()).gated_rmsnorm
+    status = fn(o, gate, weight, y, scales, code, eps, stream)
+    if status:
+        _settle(status, fn, o.device, o, gate, weight, y, scales, code, eps, stream)
 
 
 def kda_fp8_linear(a, a_scales, w, w_scales, y, stream=None):
     """y[m,n] = sum_k a[m,k] a_scales[k//128,m] * w[n,k] w_scales[n//128,k//128]. a [M,K], w [N,K]
     float8_e4m3fn (rows contiguous, row strides multiples of 16); a_scales [ceil(K/128),M] and w_scales
     [ceil(N/128),ceil(K/128)] fp32; y [M,N] bf16 or fp32 (rows contiguous)."""
-    global _fast
-    f = _fast
-    if f is None:
-        f = _fast = _Fast()
-    M, K = a.shape
-    N, Kw = w.shape
-    kb = (K + 127) // 128
-    if Kw != K or y.shape != (M, N) or a_scales.shape != (kb, M) or w_scales.shape != ((N + 127) // 128, kb):
-        raise ValueError("shape mismatch")
-    if a.dtype is not f.f8 or w.dtype is not f.f8:
-        raise TypeError("8-bit codes must be torch.float8_e4m3fn")
-    if a_scales.dtype is not f.f32 or w_scales.dtype is not f.f32:
-        raise TypeError("scales and norm weights must be float32")
-    code = f.codes.get(y.dtype, -1)
-    if code < 0:
-        raise TypeError("unsupported dtype; use float32 or bfloat16")
-    dev = a.get_device()
-    if not (dev >= 0 and w.get_device() == a_scales.get_device() == w_scales.get_device() == y.get_device() == dev
-            and a_scales.is_contiguous() and w_scales.is_contiguous()):
-        _not_on(dev)
-    _on_device(f, f.linear, stream, dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
-               y.data_ptr(), M, N, K, _row_stride(a, M, K), _row_stride(w, N, K), _row_stride(y, M, N), code)
+    fn = (_calls or _fastcall()).linear
+    status = fn(a, a_scales, w, w_scales, y, stream)
+    if status:
+        _settle(status, fn, a.device, a, a_scales, w, w_scales, y, stream)
 
 
 def _check_proj(out_gate, norm_weight, proj, proj_scales, y, lead, H, D, x):

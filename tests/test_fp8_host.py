@@ -229,3 +229,28 @@ def test_proj_workspace_sizes(kda):
     L = kda.lib()
     assert L.kda_shortconv_decode_step_proj(*[None] * 11, 0, 3, 128, 100, 1, 0, 0, 1e-6, 1e-6, 0, None, 0,
                                             None) == kda.KDA_OK
+
+
+def test_binding_refuses_wrong_types_of_arguments(kda):
+    """Arguments that are no tensors raise, a wrong number of them too, and nothing is called."""
+    import torch
+    f8 = torch.float8_e4m3fn
+    x, w = torch.zeros(3, 256), torch.ones(256)
+    y, s = torch.zeros(3, 256, dtype=f8), torch.zeros(2, 3)
+    with pytest.raises(AttributeError):
+        kda.kda_add_rmsnorm_fp8([[1.0]], w, y, s)
+    with pytest.raises(TypeError):
+        kda.kda_add_rmsnorm_fp8(x.cuda() if torch.cuda.is_available() else x, w)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.kda_add_rmsnorm_fp8(x, w, y, s)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.kda_gated_rmsnorm_fp8(torch.zeros(3, 2, 128), torch.zeros(3, 2, 128), torch.ones(128),
+                                  torch.zeros(3, 2, 128, dtype=f8), s)
+    calls = kda._fastcall()
+    with pytest.raises(TypeError, match="number of arguments"):
+        calls.linear(1, 2)
+    with pytest.raises(ValueError, match="shape"):
+        kda.kda_gated_rmsnorm_fp8(x, x, w, y, s)
+    with pytest.raises(ValueError, match="shape"):
+        kda.kda_fp8_linear(torch.zeros(256, dtype=f8), s, torch.zeros(5, 256, dtype=f8), torch.zeros(1, 2),
+                           torch.zeros(3, 5))
