@@ -333,3 +333,77 @@ def test_linear_two_streams_at_once(env):
     for i in range(3):
         for k in range(4):
             assert torch.equal(outs[i][k], alone[i])
+
+
+@pytest.mark.parametrize("M,N,K", [(130, 520, 4112), (20, 300, 2064), (64, 96, 4096), (2600, 2600, 272), (2600, 2601, 128),
+                                   (1000, 640, 3600)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_splits_and_several_tiles(env, M, N, K, out):
+    """K split over a cluster with uneven runs and several token tiles, and CTA pairs that take more than one
+    tile; a sample of rows from every tile, and the same bits twice."""
+    torch, kda = env
+    a, sa, w, sw = _lin_case(torch, 70 + M, M, N, K)
+    y = torch.full((M, N), float("nan"), dtype=_dt(torch, out), device="cuda")
+    kda.kda_fp8_linear(a, sa, w, sw, y)
+    kda.kda_sync_status()
+    assert bool(torch.isfinite(y).all())
+    rows = torch.arange(0, M, 1 if M < 200 else 13, device="cuda")
+    _lin_check(torch, y[rows], a.view(torch.uint8)[rows].view(a.dtype), sa[:, rows], w, sw, f"{M}x{N}x{K}")
+    again = torch.empty_like(y)
+    kda.kda_fp8_linear(a, sa, w, sw, again)
+    assert torch.equal(y, again)
+
+
+def test_norms_zero_tokens(env):
+    torch, kda = env
+    f8 = torch.float8_e4m3fn
+    e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+    kda.kda_add_rmsnorm_fp8(e(0, 256), e(256), e(0, 256, dt=f8), e(2, 0))
+    kda.kda_gated_rmsnorm_fp8(e(0, 3, 64), e(0, 3, 64), e(64), e(0, 3, 64, dt=f8), e(2, 0))
+    kda.kda_sync_status()
+
+
+def test_calls_on_a_given_stream_follow_it(env):
+    """stream= names the stream: work queued on it ahead of the call is seen, without any other order."""
+    torch, kda = env
+    M, N, K = 40, 300, 1040
+    _, sa, w, sw = _lin_case(torch, 91, M, N, K)
+    x, r, nw = _add_case(torch, 92, M, K, "f32", "f32")
+    q, s = torch.empty((M, K), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty_like(sa)
+    want, got = torch.empty((M, N), device="cuda"), torch.empty((M, N), device="cuda")
+    kda.kda_add_rmsnorm_fp8(x, nw, q, s, residual=r)
+    kda.kda_fp8_linear(q, s, w, sw, want)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    x2, q2, s2 = torch.zeros_like(x), torch.zeros_like(q), torch.zeros_like(s)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(20):
+            x2.copy_(x)
+    kda.kda_add_rmsnorm_fp8(x2, nw, q2, s2, residual=r, stream=st)
+    kda.kda_fp8_linear(q2, s2, w, sw, got, stream=st)
+    st.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_linear_behind_a_kernel_that_rewrites_its_operands(env):
+    """The product is launched while the kernel before it still runs: operands (the weight as well) that
+    this kernel writes are read only when it has finished."""
+    torch, kda = env
+    for M in (16, 600):
+        N, K = 512, 2048
+        a, sa, w, sw = _lin_case(torch, 95 + M, M, N, K)
+        want, got = torch.empty((M, N), device="cuda"), torch.empty((M, N), device="cuda")
+        kda.kda_fp8_linear(a, sa, w, sw, want)
+        a2, w2 = torch.zeros_like(a.view(torch.uint8)), torch.zeros_like(w.view(torch.uint8))
+        sa2, sw2 = torch.zeros_like(sa), torch.zeros_like(sw)
+        for _ in range(5):
+            for t in (a2, w2, sa2, sw2):
+                t.zero_()
+            kda.kda_fp8_linear(a2.view(a.dtype), sa2, w2.view(w.dtype), sw2, got)
+            sa2.copy_(sa)
+            sw2.copy_(sw)
+            a2.copy_(a.view(torch.uint8))
+            w2.copy_(w.view(torch.uint8))
+            kda.kda_fp8_linear(a2.view(a.dtype), sa2, w2.view(w.dtype), sw2, got)
+            assert torch.equal(got, want)
