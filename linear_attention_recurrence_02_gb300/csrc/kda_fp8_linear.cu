@@ -18,6 +18,13 @@
 #include "kda_tc.cuh"
 
 namespace kda {
+namespace tcp {
+// the driver's tensor-map encoder, looked up once (kda_prefill_tc.cu)
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+}  // namespace tcp
 namespace lin {
 
 constexpr int KB = 128;                             // K block: channels per scale
@@ -735,6 +742,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(AS * BN) : "memory");
 }
 
+// 2-D tiled map over [rows][inner] with a row stride of its own (bytes, a multiple of 16), 128-byte swizzle
+static bool row_map(CUtensorMap *m, const void *p, CUtensorMapDataType dt, uint64_t inner, uint64_t rows,
+                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows) {
+    tcp::EncodeTiledFn fn = tcp::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {box_inner, box_rows}, es[2] = {1, 1};
+    return fn(m, dt, 2, const_cast<void *>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// of a byte matrix [rows][K], box 128 x box_rows
+static bool byte_map(CUtensorMap *m, const void *p, int K, int64_t rows, int64_t ld, int box_rows) {
+    return row_map(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)rows, (uint64_t)ld, KB,
+                   (uint32_t)box_rows);
+}
+
 // pairs of CTAs that run at once on the current device
 template <typename TO> static int resident_pairs() {
     static std::atomic<int> known[64];
@@ -783,10 +807,8 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
     const int by_tma = (ldy * sizeof(TO)) % 16 == 0 && ldy < (1LL << 36);
     CUtensorMap ty;
     memset(&ty, 0, sizeof(ty));
-    if (by_tma && !tcp::make_map_ld(&ty, y, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                                    (uint64_t)N, (uint64_t)M, (uint64_t)ldy * sizeof(TO), 128 / sizeof(TO), 32,
-                                    CU_TENSOR_MAP_SWIZZLE_128B))
+    if (by_tma && !row_map(&ty, y, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                           (uint64_t)N, (uint64_t)M, (uint64_t)ldy * sizeof(TO), 128 / sizeof(TO), 32))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
@@ -801,12 +823,6 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
     cudaLaunchKernelEx(&cfg, linear_many_kernel<TO>, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N,
                        (K + KB - 1) / KB, ldy, (unsigned)mt, (unsigned)tiles, by_tma, err);  // an error is left for check_launch
     return check_launch("linear_many_kernel");
-}
-
-// map of a row-major [rows][K] byte matrix with row stride ld, box 128 x box_rows, 128-byte swizzle
-static bool byte_map(CUtensorMap *m, const void *p, int K, int64_t rows, int64_t ld, int box_rows) {
-    return tcp::make_map_ld(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)rows, (uint64_t)ld, KB,
-                            (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <typename TO>

@@ -60,9 +60,6 @@ namespace tcp {
 // elements with a box of box_inner x box_rows; false if the encoder fails.
 bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint32_t elem, uint64_t inner,
               uint64_t rows, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw);
-// The same with a row stride of its own (bytes, a multiple of 16).
-bool make_map_ld(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t inner, uint64_t rows,
-                 uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw);
 }  // namespace tcp
 
 // Validated [start, end) of sequence n; on invalid cu_seqlens sets the

@@ -1348,21 +1348,16 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-bool make_map_ld(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t inner, uint64_t rows,
-                 uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw) {
+bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint32_t elem, uint64_t inner,
+                     uint64_t rows, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {inner, rows};
-    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint64_t strides[1] = {inner * elem};
     const cuuint32_t box[2] = {box_inner, box_rows};
     const cuuint32_t es[2] = {1, 1};
     return fn(m, dt, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint32_t elem, uint64_t inner,
-                     uint64_t rows, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw) {
-    return make_map_ld(m, base, dt, inner, rows, inner * elem, box_inner, box_rows, sw);
 }
 
 // 3-D map over [T][H][d] (dims innermost first: d, H, T), box box_d x 1 x box_t. A box reaching

@@ -1,7 +1,7 @@
 """Run one workload of the library a fixed number of times, for profiler captures.
 
     python -m linear_attention_recurrence_02_gb300.profile_cases CASE [--B 64] [--T 4096] [--H 96]
-        [--gate channel|head|none] [--dtype bf16|f32] [--warmup 3] [--reps 2]
+        [--gate channel|head|none] [--dtype bf16|f32] [--N 4096] [--K 4096] [--warmup 3] [--reps 2]
 
 Every call goes through the C ABI exactly as a user's does. Inputs are drawn
 on the device by a seeded torch generator with the workloads' distributions
@@ -17,6 +17,9 @@ each (the prefill adds no other launch for one sequence). Cases:
   prefill         chunked prefill of one T-token sequence (C = 64)
   shortconv_prefill  the short conv over one T-token prompt with rings in and out
   epilogue        the gated RMSNorm output epilogue over T x H rows (sigmoid gate)
+  epilogue_fp8    the same with its output in 8 bits (kda_gated_rmsnorm_fp8)
+  add_norm_fp8    residual addition + RMSNorm in 8 bits over T tokens of K channels (kda_add_rmsnorm_fp8)
+  linear_fp8      the 8-bit product of T tokens of K channels with N features (kda_fp8_linear)
 """
 from __future__ import annotations
 
@@ -31,13 +34,15 @@ from linear_attention_recurrence_02_gb300 import kda
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["decode", "decode_epi", "decode_unfused", "shortconv_step", "prefill",
-                                     "shortconv_prefill", "epilogue"])
+                                     "shortconv_prefill", "epilogue", "epilogue_fp8", "add_norm_fp8", "linear_fp8"])
     ap.add_argument("--B", type=int, default=64)
     ap.add_argument("--T", type=int, default=4096)
     ap.add_argument("--H", type=int, default=96)
     ap.add_argument("--D", type=int, default=128)
     ap.add_argument("--gate", default="channel", choices=["channel", "head", "none"])
     ap.add_argument("--dtype", default="bf16", choices=["bf16", "f32"])
+    ap.add_argument("--N", type=int, default=4096)
+    ap.add_argument("--K", type=int, default=4096)
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--reps", type=int, default=2)
     a = ap.parse_args(argv)
@@ -86,6 +91,29 @@ def main(argv=None) -> int:
 
         def call():
             kda.kda_gated_rmsnorm(o, og, nw, y)
+    elif a.case in ("epilogue_fp8", "add_norm_fp8", "linear_fp8"):
+        f8, C = torch.float8_e4m3fn, H * D if a.case == "epilogue_fp8" else a.K
+        dt = bf if a.dtype == "bf16" else torch.float32
+        codes, scales = torch.empty((T, C), dtype=f8, device=dev), torch.rand(((C + 127) // 128, T), device=dev) / 100
+        if a.case == "linear_fp8":
+            codes.copy_((rnd(T, C) * 120).clamp_(-448, 448))
+            w = (rnd(a.N, C) * 110).clamp_(-448, 448).to(f8)
+            ws = torch.rand(((a.N + 127) // 128, (C + 127) // 128), device=dev) / 100
+            y = torch.empty((T, a.N), dtype=dt, device=dev)
+        elif a.case == "add_norm_fp8":
+            x, r, nw = rnd(T, C).to(dt), rnd(T, C, scale=2.0).to(dt), torch.rand((C,), generator=gen, device=dev) + 0.5
+            so = torch.empty_like(r)
+        else:
+            x, og = rnd(T, H, D).to(dt), rnd(T, H, D, scale=2.0).to(dt)
+            nw = torch.rand((D,), generator=gen, device=dev) + 0.5
+
+        def call():
+            if a.case == "linear_fp8":
+                kda.kda_fp8_linear(codes, scales, w, ws, y)
+            elif a.case == "add_norm_fp8":
+                kda.kda_add_rmsnorm_fp8(x, nw, codes, scales, residual=r, sum_out=so)
+            else:
+                kda.kda_gated_rmsnorm_fp8(x, og, nw, codes.view(T, H, D), scales)
     else:
         dt = bf if a.dtype == "bf16" else torch.float32
         q, k, v = rnd(T, H, D).to(dt), rnd(T, H, D).to(dt), rnd(T, H, D).to(dt)
