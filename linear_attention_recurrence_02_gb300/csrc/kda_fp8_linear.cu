@@ -463,37 +463,10 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
         : "memory");
 }
 
-// 32 TMEM columns of the thread's lane as 16 pairs, waited for
-__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, uint64_t (&d)[16]) {
-    asm volatile(
-        "{\n\t.reg .b32 t<32>;\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,"
-        "t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t"
-        "mov.b64 %0, {t0,t1};\n\t"
-        "mov.b64 %1, {t2,t3};\n\t"
-        "mov.b64 %2, {t4,t5};\n\t"
-        "mov.b64 %3, {t6,t7};\n\t"
-        "mov.b64 %4, {t8,t9};\n\t"
-        "mov.b64 %5, {t10,t11};\n\t"
-        "mov.b64 %6, {t12,t13};\n\t"
-        "mov.b64 %7, {t14,t15};\n\t"
-        "mov.b64 %8, {t16,t17};\n\t"
-        "mov.b64 %9, {t18,t19};\n\t"
-        "mov.b64 %10, {t20,t21};\n\t"
-        "mov.b64 %11, {t22,t23};\n\t"
-        "mov.b64 %12, {t24,t25};\n\t"
-        "mov.b64 %13, {t26,t27};\n\t"
-        "mov.b64 %14, {t28,t29};\n\t"
-        "mov.b64 %15, {t30,t31};\n\t"
-        "}\n"
-        : "=l"(d[0]), "=l"(d[1]), "=l"(d[2]), "=l"(d[3]), "=l"(d[4]), "=l"(d[5]), "=l"(d[6]), "=l"(d[7]), "=l"(d[8]),
-          "=l"(d[9]), "=l"(d[10]), "=l"(d[11]), "=l"(d[12]), "=l"(d[13]), "=l"(d[14]), "=l"(d[15])
-        : "r"(taddr)
-        : "memory");
-}
-// both halves: a += d * s
-__device__ __forceinline__ void fma2(uint64_t &a, uint64_t d, uint64_t s) {
+// (a.lo, a.hi) += (d0, d1) * (s, s) in one instruction
+__device__ __forceinline__ void fma2(uint64_t &a, uint32_t d0, uint32_t d1, uint64_t s) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(s));
 }
 
@@ -573,17 +546,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
                 ok = wait_more(afull + as, ph, ok);
                 __syncwarp();
                 tc_fence_after();
+                // 16 columns at a time, the next 16 on their way while these are joined
+                uint32_t d[2][16];
+                tmem_ld16(trow + as * BN, d[0]);
+                tmem_ld_wait_for(d[0]);
 #pragma unroll
-                for (int c = 0; c < JC; c += 32) {
-                    uint64_t d[16];
-                    tmem_ld_pairs(trow + as * BN + c, d);
-                    if (c == JC - 32) {  // the accumulator is read: the MMAs may write it again
+                for (int c = 0; c < JC / 16; ++c) {
+                    if (c + 1 < JC / 16) tmem_ld16(trow + as * BN + 16 * (c + 1), d[(c + 1) & 1]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) fma2(acc[8 * c + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], s2);
+                    if (c + 1 < JC / 16) tmem_ld_wait_for(d[(c + 1) & 1]);
+                    if (c + 2 == JC / 16) {  // the accumulator is read: the MMAs may write it again
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_peer(as ? rel1 : rel0);
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + j], d[j], s2);
                 }
                 as ^= 1;
                 ph ^= as == 0;
