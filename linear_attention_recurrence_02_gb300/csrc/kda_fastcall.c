@@ -10,8 +10,8 @@
  * is given.
  *
  * Each returns the library's status (0 = KDA_OK), or -1 where the tensors live
- * on another device than the current one and no stream was given: the caller
- * makes that device current and calls again.
+ * on another device than the current one and no stream of theirs was named: the
+ * caller makes that device current and calls again.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -115,20 +115,26 @@ static int one_device(const Tensor *t, const Tensor *const *others, int n) {
 }
 
 /* Handle of `stream`, or of the current stream of device `dev` where it is None. 1: found, 0: error set,
- * -1: `dev` is not the current device. */
+ * -1: a default stream (whose handle, 0, names no device) of a device that is not the current one, or None
+ * there. */
 static int find_stream(PyObject *stream, long dev, void **handle) {
     PyObject *o;
+    *handle = NULL;
     if (stream != Py_None) {
-        o = PyObject_GetAttr(stream, n_cuda_stream);
-    } else {
-        long long cur;
-        if (!long_of(PyObject_CallNoArgs(S.get_device), &cur)) return 0;
-        if (cur != dev) return -1;
-        PyObject *d = PyLong_FromLong(dev);
-        if (d == NULL) return 0;
-        o = PyObject_CallOneArg(S.raw_stream, d);
-        Py_DECREF(d);
+        if ((o = PyObject_GetAttr(stream, n_cuda_stream)) == NULL) return 0;
+        *handle = PyLong_AsVoidPtr(o);
+        Py_DECREF(o);
+        if (*handle != NULL) return 1;
+        if (PyErr_Occurred()) return 0;
     }
+    long long cur;
+    if (!long_of(PyObject_CallNoArgs(S.get_device), &cur)) return 0;
+    if (cur != dev) return -1;
+    if (stream != Py_None) return 1;
+    PyObject *d = PyLong_FromLong(dev);
+    if (d == NULL) return 0;
+    o = PyObject_CallOneArg(S.raw_stream, d);
+    Py_DECREF(d);
     if (o == NULL) return 0;
     *handle = PyLong_AsVoidPtr(o);
     Py_DECREF(o);

@@ -473,8 +473,9 @@ __device__ __forceinline__ void fma2(uint64_t &a, uint32_t d0, uint32_t d1, uint
 template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                       const __grid_constant__ CUtensorMap tm_y, const float *__restrict__ sa, const float *__restrict__ sw, TO *__restrict__ y, int M, int N,
-                       int nkb, int64_t ldy, unsigned mt, unsigned tiles, int by_tma, unsigned *err) {
+                       const __grid_constant__ CUtensorMap tm_y, const float *__restrict__ sa,
+                       const float *__restrict__ sw, TO *__restrict__ y, int M, int N, int nkb, int64_t ldy,
+                       unsigned mt, unsigned tiles, int by_tma, unsigned *err) {
     using namespace tc;
     using namespace many;
     extern __shared__ uint8_t smem_raw[];

@@ -330,7 +330,7 @@ def _fastcall():
 
 def _settle(status, fn, device, *args):
     """A call's status other than KDA_OK: an error, or (-1) tensors on another device than the current one
-    and no stream given: the call again with that device current (the handle of a default stream does not
+    and no stream named: the call again with that device current (the handle of a default stream does not
     name its device)."""
     if status == -1:
         import torch
@@ -393,6 +393,14 @@ def _check_proj(out_gate, norm_weight, proj, proj_scales, y, lead, H, D, x):
     return Nout
 
 
+def _current(device):
+    """Context in which `device` is current (a default stream's handle does not name its device)."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    return torch.cuda.device(device)
+
+
 def _proj_workspace(workspace, need, device):
     """The caller's workspace and its size, or one allocated here when None."""
     import torch
@@ -418,10 +426,11 @@ def kda_shortconv_decode_step_proj(x, ring, w, g, beta, state, out_gate, norm_we
     Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, B, H, D, x)
     workspace, size = _proj_workspace(workspace, kda_shortconv_decode_step_proj_workspace_bytes(B, H, D), x.device)
     flags = KDA_DECODE_OVERLAP_PREV if overlap_prev else 0
-    _check(lib().kda_shortconv_decode_step_proj(
-        _ptr(x), _ptr(ring), _ptr(w), _ptr(g), _ptr(beta), _ptr(state), _ptr(out_gate), _ptr(norm_weight), _ptr(proj),
-        _ptr(proj_scales), _ptr(y), B, H, D, Nout, _dtype_code(x), code, _ACTS[act], float(l2_eps), float(norm_eps),
-        flags, _ptr(workspace), size, _stream(stream, x.device)))
+    with _current(x.device):
+        _check(lib().kda_shortconv_decode_step_proj(
+            _ptr(x), _ptr(ring), _ptr(w), _ptr(g), _ptr(beta), _ptr(state), _ptr(out_gate), _ptr(norm_weight),
+            _ptr(proj), _ptr(proj_scales), _ptr(y), B, H, D, Nout, _dtype_code(x), code, _ACTS[act], float(l2_eps),
+            float(norm_eps), flags, _ptr(workspace), size, _stream(stream, x.device)))
 
 
 def kda_shortconv_decode_step_proj_workspace_bytes(B, H, D) -> int:
@@ -448,11 +457,12 @@ def kda_chunk_prefill_proj(q, k, v, g, beta, out_gate, norm_weight, proj, proj_s
     Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, T, H, D, q)
     workspace, size = _proj_workspace(workspace, kda_chunk_prefill_proj_workspace_bytes(T, N, H, D, chunk_size),
                                       q.device)
-    _check(lib().kda_chunk_prefill_proj(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens), N, T,
-        H, D, chunk_size, _dtype_code(q), code, float(l2_eps), _ptr(out_gate), _ptr(norm_weight), _ACTS[act],
-        float(norm_eps), _ptr(proj), _ptr(proj_scales), _ptr(y), Nout, _ptr(workspace), size,
-        _stream(stream, q.device)))
+    with _current(q.device):
+        _check(lib().kda_chunk_prefill_proj(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens),
+            N, T, H, D, chunk_size, _dtype_code(q), code, float(l2_eps), _ptr(out_gate), _ptr(norm_weight), _ACTS[act],
+            float(norm_eps), _ptr(proj), _ptr(proj_scales), _ptr(y), Nout, _ptr(workspace), size,
+            _stream(stream, q.device)))
 
 
 def kda_chunk_prefill_proj_workspace_bytes(total_tokens, num_seqs, H, D, C) -> int:

@@ -407,3 +407,66 @@ def test_linear_behind_a_kernel_that_rewrites_its_operands(env):
             w2.copy_(w.view(torch.uint8))
             kda.kda_fp8_linear(a2.view(a.dtype), sa2, w2.view(w.dtype), sw2, got)
             assert torch.equal(got, want)
+
+
+def test_capture_with_forked_streams(env):
+    """Captured with the two norms on a stream of their own between event waits, a copy ahead of them: the
+    replay gives the bits of direct calls."""
+    torch, kda = env
+    M, N, K = 40, 260, 1024
+    _, sa, w, sw = _lin_case(torch, 101, M, N, K)
+    x, r, nw = _add_case(torch, 102, M, K, "bf16", "bf16")
+    src = x.clone()
+    q, s = torch.empty((M, K), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty_like(sa)
+    y, z = torch.empty((M, N), device="cuda"), torch.empty((M, N), device="cuda")
+    og, gw = torch.randn((M, 8, 128), device="cuda").bfloat16(), torch.ones(128, device="cuda")
+    q2, s2 = torch.empty((M, 8, 128), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty_like(sa)
+    side = torch.cuda.Stream()
+
+    def work():
+        x.copy_(src)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            kda.kda_gated_rmsnorm_fp8(x.view(M, 8, 128), og, gw, q2, s2)
+        kda.kda_add_rmsnorm_fp8(x, nw, q, s, residual=r)
+        kda.kda_fp8_linear(q, s, w, sw, y)
+        torch.cuda.current_stream().wait_stream(side)
+        kda.kda_fp8_linear(q2.view(M, K), s2, w, sw, z)
+
+    work()
+    torch.cuda.synchronize()
+    want = y.clone(), z.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for _ in range(3):
+        y.zero_()
+        z.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+
+
+def test_linear_result_feeds_the_next_calls_input(env):
+    """Ten products in a row, each reading what the one before wrote (through the norm), without any
+    synchronisation, against the same calls made one at a time."""
+    torch, kda = env
+    for M in (1, 30, 300):
+        K = 512
+        w, sw = _lin_case(torch, 110 + M, 1, K, K)[2:]
+        nw = torch.ones(K, device="cuda")
+        start = torch.randn((M, K), generator=_gen(torch, M), device="cuda")
+        q, s = torch.empty((M, K), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty((4, M), device="cuda")
+
+        def chain(wait):
+            h = start.clone()
+            for _ in range(10):
+                kda.kda_add_rmsnorm_fp8(h, nw, q, s)
+                if wait:
+                    torch.cuda.synchronize()
+                kda.kda_fp8_linear(q, s, w, sw, h)
+                if wait:
+                    torch.cuda.synchronize()
+            return h
+
+        assert torch.equal(chain(False), chain(True))
