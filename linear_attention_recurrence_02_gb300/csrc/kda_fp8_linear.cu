@@ -417,7 +417,9 @@ static kda_status launch_few(const CUtensorMap &tw, const CUtensorMap &ta, const
 // the even CTA issues the MMAs for both, warps 10 and 11 form the scales'
 // products, four K blocks at a time. Persistent: a pair walks tiles, token
 // tiles first, so that neighbouring pairs share weight tiles in L2, and the next
-// tile's products run while this one's results are stored.
+// tile's products run while this one's results are stored. Where the tiles would
+// leave most pairs idle, 2 or 4 pairs of one cluster take a run of K blocks of
+// the same tile each (SPLIT) and exchange their sums at the end.
 namespace many {
 constexpr int BM = 256, BN = 256;                 // tile of a pair
 constexpr int A_BYTES = 128 * KB, W_BYTES = 128 * KB;
@@ -454,12 +456,13 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uin
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// arrive on `bar` of both CTAs when every MMA issued so far by this thread completes
-__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+// arrive on `bar` of both CTAs of the pair (cluster ranks lead and lead + 1) when every MMA issued so far by
+// this thread completes
+__device__ __forceinline__ void commit_pair(uint64_t *bar, uint32_t lead) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             tc::smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << lead))
         : "memory");
 }
 
@@ -470,12 +473,24 @@ __device__ __forceinline__ void fma2(uint64_t &a, uint32_t d0, uint32_t d1, uint
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(s));
 }
 
-template <typename TO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
+// 16 bytes to an address of the cluster's shared window
+__device__ __forceinline__ void peer_store16(uint32_t at, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
+}
+// (a.lo, a.hi) += (x, y)
+__device__ __forceinline__ void add2(uint64_t &a, float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(d));
+}
+
+template <typename TO, bool SPLIT>
+__global__ void __launch_bounds__(many::NTHREADS, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_y, const float *__restrict__ sa,
                        const float *__restrict__ sw, TO *__restrict__ y, int M, int N, int nkb, int64_t ldy,
-                       unsigned mt, unsigned tiles, int by_tma, unsigned *err) {
+                       unsigned mt, unsigned tiles, int by_tma, int S, unsigned *err) {
     using namespace tc;
     using namespace many;
     extern __shared__ uint8_t smem_raw[];
@@ -485,8 +500,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
     uint32_t *s_taddr = reinterpret_cast<uint32_t *>(sempty + CS);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
-    const uint32_t rank = cluster_rank();
-    const unsigned pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    // rank: this CTA in its pair, lead: the cluster rank of the pair's even CTA, sp: the pair in its cluster
+    const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;
+    const int sp = SPLIT ? (int)(crank >> 1) : 0;
+    const unsigned pair = SPLIT ? blockIdx.x / (2u * (unsigned)S) : blockIdx.x >> 1;
+    const unsigned npairs = SPLIT ? gridDim.x / (2u * (unsigned)S) : gridDim.x >> 1;
+    // K blocks of this pair
+    const int kb0 = SPLIT ? (int)((int64_t)nkb * sp / S) : 0, kb1 = SPLIT ? (int)((int64_t)nkb * (sp + 1) / S) : nkb;
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(full + i, 1);  // the even CTA's own arrival; both CTAs' bytes
@@ -512,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
     if (warp == JW && elect_one()) {
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_w);
-        for (int kb = 0; kb < ST && kb < nkb; ++kb)
+        for (int kb = kb0; kb < kb0 + ST && kb < kb1; ++kb)
             tma_prefetch_l2_2d(&tm_w, kb * KB, (int)(pair / mt) * BN + (int)rank * 128);
     }
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
@@ -528,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_JOIN));
         const int half = warp >> 2;  // features 128 * half of the tile
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
-        const uint32_t rel0 = peer_addr(aempty, 0), rel1 = peer_addr(aempty + 1, 0);
+        const uint32_t rel0 = peer_addr(aempty, lead), rel1 = peer_addr(aempty + 1, lead);
         const int mrow = (int)rank * 128 + 32 * (warp & 3) + lane;
         const float *mine = reinterpret_cast<const float *>(sm + SCALES) + half * 128 + 32 * (warp & 3) + lane;
         uint8_t *out = sm + OUT + warp * 4096;
@@ -538,8 +558,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
             uint64_t acc[JC / 2];  // pairs of fp32
 #pragma unroll
             for (int j = 0; j < JC / 2; ++j) acc[j] = 0;
-            for (int kb = 0; kb < nkb; ++kb) {
-                const int ck = kb & (CK - 1);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const int ck = (kb - kb0) & (CK - 1);
                 if (ck == 0) ok = wait_more(sfull + cs, cph, ok);
                 const float s0 = mine[cs * (CHUNK / 4) + ck * 256];
                 uint64_t s2;
@@ -565,12 +585,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
                 }
                 as ^= 1;
                 ph ^= as == 0;
-                if (ck == CK - 1 || kb == nkb - 1) {  // the chunk's last: its slot may be filled again
+                if (ck == CK - 1 || kb == kb1 - 1) {  // the chunk's last: its slot may be filled again
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sempty + cs);
                     if (++cs == CS) {
                         cs = 0;
                         cph ^= 1;
+                    }
+                }
+            }
+            if constexpr (SPLIT) {
+                // The pairs' sums meet: each group of 64 features belongs to one pair of the cluster; the
+                // others send it theirs, [group][pair][feature / 4][token] in the ring's place, and it adds them
+                // to its own in the pairs' order. (One tile per cluster: the rings are free from here on.)
+                cluster_sync();
+                const int per = 4 / S, row = 32 * (warp & 3) + lane;  // groups of a pair
+                auto val = [&](int j) { return __uint_as_float((uint32_t)(acc[j >> 1] >> (32 * (j & 1)))); };
+#pragma unroll
+                for (int gi = 0; gi < 2; ++gi) {
+                    const int g = 2 * half + gi, o = g / per, slot = (g - o * per) * (S - 1) + (sp < o ? sp : sp - 1);
+                    if (o == sp) continue;
+                    const uint32_t to = peer_addr(sm, 2u * (uint32_t)o + rank) + (uint32_t)(slot * 32768 + row * 16);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        peer_store16(to + c * 2048, val(64 * gi + 4 * c), val(64 * gi + 4 * c + 1),
+                                     val(64 * gi + 4 * c + 2), val(64 * gi + 4 * c + 3));
+                }
+                cluster_sync();
+#pragma unroll
+                for (int gi = 0; gi < 2; ++gi) {
+                    const int g = 2 * half + gi, o = g / per;
+                    if (o != sp) continue;
+                    const float4 *from = reinterpret_cast<const float4 *>(sm) + (g - o * per) * (S - 1) * 2048 + row;
+                    for (int q = 0; q < S - 1; ++q, from += 2048) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float4 x = from[c * 128];
+                            add2(acc[32 * gi + 2 * c], x.x, x.y);
+                            add2(acc[32 * gi + 2 * c + 1], x.z, x.w);
+                        }
                     }
                 }
             }
@@ -585,6 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
                 for (int r = 0; r < JC / JR; ++r) {
                     const int n = n0 + r * JR;
                     if (n >= N) break;
+                    if (SPLIT && (2 * half + r * JR / 64) / (4 / S) != sp) continue;  // another pair's
                     if (lane == 0) bulk_wait_read();  // the buffer's last copy has read it
                     __syncwarp();
 #pragma unroll
@@ -621,12 +675,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
             for (unsigned tile = pair; tile < tiles; tile += npairs) {
                 const int row_a = (int)(tile % mt) * BM + (int)rank * 128;
                 const int row_w = (int)(tile / mt) * BN + (int)rank * 128;
-                for (int kb = 0; kb < nkb; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = wait_more(empty + st, ph, ok);
                     __syncwarp();
                     if (elect_one()) {
                         uint8_t *d = sm + st * STAGE;
-                        const uint32_t bar = peer_addr(full + st, 0);
+                        const uint32_t bar = peer_addr(full + st, lead);
                         if (rank == 0) mbar_arrive_expect_tx(full + st, 2 * STAGE);
                         tma_load_pair(d, &tm_a, bar, kb * KB, row_a);
                         tma_load_pair(d + A_BYTES, &tm_w, bar, kb * KB, row_w);
@@ -653,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
                 uint32_t ph = 0, aph = 1;  // the accumulators start out free
                 const uint64_t a0 = sdesc_sw128(sbase, 16, 1024), b0 = sdesc_sw128(sbase + A_BYTES, 16, 1024);
                 for (unsigned tile = pair; tile < tiles; tile += npairs) {
-                    for (int kb = 0; kb < nkb; ++kb) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
                         const uint64_t a = a0 + (uint64_t)(st * (STAGE / 16)), b = b0 + (uint64_t)(st * (STAGE / 16));
                         ok = wait_more(full + st, ph, ok);
                         ok = wait_more(aempty + as, aph, ok);
@@ -663,8 +717,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_f8_pair(tbase + as * BN, a + 2 * ks, b + 2 * ks, idesc_f8(BM, BN), ks > 0);
-                            commit_pair(afull + as);
-                            commit_pair(empty + st);
+                            commit_pair(afull + as, lead);
+                            commit_pair(empty + st, lead);
                         }
                         as ^= 1;
                         aph ^= as == 0;
@@ -684,11 +738,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
             for (unsigned tile = pair; tile < tiles; tile += npairs) {
                 const int m0 = (int)(tile % mt) * BM + (int)rank * 128 + lane, nb = (int)(tile / mt) * 2;
                 const float *w0 = sw + (int64_t)nb * nkb, *w1 = nb + 1 < nblk ? w0 + nkb : w0;
-                for (int k0 = 0; k0 < nkb; k0 += CK) {
+                for (int k0 = kb0; k0 < kb1; k0 += CK) {
                     ok = wait_more(sempty + cs, cph, ok);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int kc = k0 + w2 + i < nkb ? k0 + w2 + i : nkb - 1;
+                        const int kc = k0 + w2 + i < kb1 ? k0 + w2 + i : kb1 - 1;
                         const float *ap = sa + (int64_t)kc * M;
                         float *b = reinterpret_cast<float *>(sm + SCALES) + cs * (CHUNK / 4) + (w2 + i) * 256 + lane;
                         float av[4];
@@ -709,6 +763,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(many::NTHREADS, 1)
                     }
                 }
             }
+        }
+        if (SPLIT) {  // the joining warps' two meetings
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
         }
     }
     if (!ok) atomicOr(err, DEVERR_TIMEOUT);
@@ -737,48 +796,72 @@ static bool byte_map(CUtensorMap *m, const void *p, int K, int64_t rows, int64_t
                    (uint32_t)box_rows);
 }
 
-// pairs of CTAs that run at once on the current device
-template <typename TO> static int resident_pairs() {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return 0;
-    int n = known[dev].load(std::memory_order_acquire);
-    if (n > 0) return n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
+static void many_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], unsigned clusters, int S, cudaStream_t s) {
+    cfg.gridDim = dim3(clusters * 2u * (unsigned)S);
     cfg.blockDim = dim3(many::NTHREADS);
     cfg.dynamicSmemBytes = many::SMEM;
-    cudaLaunchAttribute at[1];
+    cfg.stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.x = 2u * (unsigned)S;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, linear_many_kernel<TO>, &cfg) != cudaSuccess) {
+    cfg.numAttrs = 2;
+}
+
+// Clusters of S pairs that run at once on the current device (0: none, or an error), and the kernel
+// made ready to launch there.
+template <typename TO, bool SPLIT> static int resident_clusters(int S) {
+    static std::atomic<int> known[3][64];  // value + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return 0;
+    std::atomic<int> &slot = known[S >> 1][dev];
+    int n = slot.load(std::memory_order_acquire);
+    if (n > 0) return n - 1;
+    // the register split only adds up for the launch register count it was made for
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, linear_many_kernel<TO, SPLIT>) != cudaSuccess || fa.numRegs != many::REGS ||
+        smem_attr_once<linear_many_kernel<TO, SPLIT>>(many::SMEM) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
-    known[dev].store(n, std::memory_order_release);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    many_config(cfg, at, 1, S, nullptr);
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_many_kernel<TO, SPLIT>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    slot.store(n + 1, std::memory_order_release);
     return n;
+}
+
+// The estimated time of the CTA-pair kernel in ns and the pairs of a cluster (a split of K in S) that
+// give it: 370 ns a K block, 1 us a tile and 3.5 us a launch; a split takes one tile per cluster and 3 or
+// 5.5 us (2 or 4 pairs) for the meeting of the partial sums, and pays where the tiles leave most pairs idle
+// and K is long. (512 x 4096 x 12288: 26 us at S = 2, 35.5 at 1; 240 x 3800 x 12288: 19 at 4, 35 at 1.)
+template <typename TO> static int64_t many_estimate(int64_t M, int N, int nkb, int *best) {
+    const int64_t tiles = ((M + many::BM - 1) / many::BM) * (((int64_t)N + many::BN - 1) / many::BN);
+    const int pairs = resident_clusters<TO, false>(1);
+    *best = 0;
+    if (pairs < 1) return INT64_MAX;
+    int64_t ns = ((tiles + pairs - 1) / pairs) * ((int64_t)nkb * 370 + 1000) + 3500;
+    *best = 1;
+    for (int S = 2; S <= 4 && S <= nkb && tiles * S <= pairs; S *= 2) {
+        const int64_t t = (int64_t)((nkb + S - 1) / S) * 370 + 1000 + 3500 + (S == 2 ? 3000 : 5500);
+        if (t < ns && tiles <= resident_clusters<TO, true>(S)) {
+            ns = t;
+            *best = S;
+        }
+    }
+    return ns;
 }
 
 template <typename TO>
 static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, const float *sa, const float *sw, void *y,
-                              int64_t M, int N, int K, int64_t ldy, unsigned *err, cudaStream_t s) {
-    if (smem_attr_once<linear_many_kernel<TO>>(many::SMEM) != cudaSuccess)
-        return check_launch("linear_many_kernel (shared memory attribute)");
-    // the register split only adds up for the launch register count it was made for
-    static std::atomic<int> regs{0};
-    if (regs.load(std::memory_order_acquire) == 0) {
-        cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, linear_many_kernel<TO>) != cudaSuccess)
-            return check_launch("linear_many_kernel (attributes)");
-        regs.store(fa.numRegs, std::memory_order_release);
-    }
-    if (regs.load(std::memory_order_acquire) != many::REGS)
-        return fail(KDA_ERR_UNSUPPORTED, "linear_many_kernel built with a register count its split was not made for");
-    const int pairs = resident_pairs<TO>();
-    if (pairs < 1) return fail(KDA_ERR_CUDA, "no pair of CTAs fits the device");
+                              int64_t M, int N, int K, int64_t ldy, int S, unsigned *err, cudaStream_t s) {
     const int64_t mt = (M + many::BM - 1) / many::BM, tiles = mt * (((int64_t)N + many::BN - 1) / many::BN);
     if (tiles > 0x7fffffffLL) return invalid("M*N too large for one launch");
     // y's rows suit a tensor map where their stride is a multiple of 16 bytes
@@ -788,18 +871,16 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
     if (by_tma && !row_map(&ty, y, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                            (uint64_t)N, (uint64_t)M, (uint64_t)ldy * sizeof(TO), 128 / sizeof(TO), 32))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    const int64_t most = S > 1 ? tiles : resident_clusters<TO, false>(1);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-    cfg.blockDim = dim3(many::NTHREADS);
-    cfg.dynamicSmemBytes = many::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, linear_many_kernel<TO>, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N,
-                       (K + KB - 1) / KB, ldy, (unsigned)mt, (unsigned)tiles, by_tma, err);  // an error is left for check_launch
+    cudaLaunchAttribute at[2];
+    many_config(cfg, at, (unsigned)(tiles < most ? tiles : most), S, s);
+    auto go = [&](auto kern) {
+        cudaLaunchKernelEx(&cfg, kern, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy,
+                           (unsigned)mt, (unsigned)tiles, by_tma, S, err);  // an error is left for check_launch
+    };
+    if (S > 1) go(linear_many_kernel<TO, true>);
+    else go(linear_many_kernel<TO, false>);
     return check_launch("linear_many_kernel");
 }
 
@@ -807,25 +888,22 @@ template <typename TO>
 static kda_status run_linear(const void *a, const float *sa, const void *w, const float *sw, void *y, int64_t M,
                              int N, int K, int64_t lda, int64_t ldw, int64_t ldy, unsigned *err, cudaStream_t s) {
     // Up to 64 tokens a weight tile is read once and its bytes bound the call: the few-token kernel. With
-    // more, whichever is estimated faster: CTA pairs take 370 ns a K block, 1 us a tile and 3.5 us a
-    // launch. (Measured few / many: 128 x 4096 x 4096 9.4 / 16.1 us, 256 x 4096 x 4096 13.9 / 16.2,
-    // 512 x 4096 x 4096 17.2 / 16.4, 1024 x 4096 x 4096 33 / 17, 128 x 36864 x 4096 36.9 / 34.4.)
-    bool many_tokens = false;
+    // more, whichever is estimated faster.
     const int sms = current_sms();
     if (sms < 2) return fail(KDA_ERR_CUDA, "the device's SM count is unavailable");
+    int S = 0;
     if (M > 64) {
         const int nkb = (K + KB - 1) / KB;
-        const int64_t units = ((M + 63) / 64) * (((int64_t)N + 127) / 128), pairs = sms / 2;
-        const int64_t tiles = ((M + many::BM - 1) / many::BM) * (((int64_t)N + many::BN - 1) / many::BN);
+        const int64_t units = ((M + 63) / 64) * (((int64_t)N + 127) / 128), many_ns = many_estimate<TO>(M, N, nkb, &S);
         int64_t few_ns = 0;
         few_split(units, nkb, 2 * sms, &few_ns);
-        many_tokens = ((tiles + pairs - 1) / pairs) * ((int64_t)nkb * 370 + 1000) + 3500 < few_ns;
+        if (few_ns <= many_ns) S = 0;
     }
-    if (many_tokens) {
+    if (S > 0) {
         CUtensorMap ta, tw;
         if (!byte_map(&ta, a, K, M, lda, 128) || !byte_map(&tw, w, K, N, ldw, 128))
             return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-        return launch_many<TO>(ta, tw, sa, sw, y, M, N, K, ldy, err, s);
+        return launch_many<TO>(ta, tw, sa, sw, y, M, N, K, ldy, S, err, s);
     }
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     CUtensorMap tw, ta;
