@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_y, const float *__restrict__ sa,
                        const float *__restrict__ sw, TO *__restrict__ y, int M, int N, int nkb, int64_t ldy,
-                       unsigned mt, unsigned tiles, int by_tma, int S, unsigned *err) {
+                       unsigned mt, unsigned tile0, unsigned tiles, int by_tma, int S,
+                       unsigned *err) {
     using namespace tc;
     using namespace many;
     extern __shared__ uint8_t smem_raw[];
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
     // rank: this CTA in its pair, lead: the cluster rank of the pair's even CTA, sp: the pair in its cluster
     const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;
     const int sp = SPLIT ? (int)(crank >> 1) : 0;
-    const unsigned pair = SPLIT ? blockIdx.x / (2u * (unsigned)S) : blockIdx.x >> 1;
+    const unsigned first = tile0 + (SPLIT ? blockIdx.x / (2u * (unsigned)S) : blockIdx.x >> 1);
     const unsigned npairs = SPLIT ? gridDim.x / (2u * (unsigned)S) : gridDim.x >> 1;
     // K blocks of this pair
     const int kb0 = SPLIT ? (int)((int64_t)nkb * sp / S) : 0, kb1 = SPLIT ? (int)((int64_t)nkb * (sp + 1) / S) : nkb;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_w);
         for (int kb = kb0; kb < kb0 + ST && kb < kb1; ++kb)
-            tma_prefetch_l2_2d(&tm_w, kb * KB, (int)(pair / mt) * BN + (int)rank * 128);
+            tma_prefetch_l2_2d(&tm_w, kb * KB, (int)(first / mt) * BN + (int)rank * 128);
     }
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
         uint8_t *out = sm + OUT + warp * 4096;
         int as = 0, cs = 0;
         uint32_t ph = 0, cph = 0;
-        for (unsigned tile = pair; tile < tiles; tile += npairs) {
+        for (unsigned tile = first; tile < tiles; tile += npairs) {
             uint64_t acc[JC / 2];  // pairs of fp32
 #pragma unroll
             for (int j = 0; j < JC / 2; ++j) acc[j] = 0;
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
         if (warp == JW) {
             int st = 0;
             uint32_t ph = 1;  // the ring starts out free
-            for (unsigned tile = pair; tile < tiles; tile += npairs) {
+            for (unsigned tile = first; tile < tiles; tile += npairs) {
                 const int row_a = (int)(tile % mt) * BM + (int)rank * 128;
                 const int row_w = (int)(tile / mt) * BN + (int)rank * 128;
                 for (int kb = kb0; kb < kb1; ++kb) {
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                 int st = 0, as = 0;
                 uint32_t ph = 0, aph = 1;  // the accumulators start out free
                 const uint64_t a0 = sdesc_sw128(sbase, 16, 1024), b0 = sdesc_sw128(sbase + A_BYTES, 16, 1024);
-                for (unsigned tile = pair; tile < tiles; tile += npairs) {
+                for (unsigned tile = first; tile < tiles; tile += npairs) {
                     for (int kb = kb0; kb < kb1; ++kb) {
                         const uint64_t a = a0 + (uint64_t)(st * (STAGE / 16)), b = b0 + (uint64_t)(st * (STAGE / 16));
                         ok = wait_more(full + st, ph, ok);
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
             const int nblk = (N + 127) / 128, w2 = (warp - JW - 2) * 2;
             int cs = 0;
             uint32_t cph = 1;
-            for (unsigned tile = pair; tile < tiles; tile += npairs) {
+            for (unsigned tile = first; tile < tiles; tile += npairs) {
                 const int m0 = (int)(tile % mt) * BM + (int)rank * 128 + lane, nb = (int)(tile / mt) * 2;
                 const float *w0 = sw + (int64_t)nb * nkb, *w1 = nb + 1 < nblk ? w0 + nkb : w0;
                 for (int k0 = kb0; k0 < kb1; k0 += CK) {
@@ -838,32 +839,38 @@ template <typename TO, bool SPLIT> static int resident_clusters(int S) {
     return n;
 }
 
-// The estimated time of the CTA-pair kernel in ns and the pairs of a cluster (a split of K in S) that
-// give it: 370 ns a K block, 1 us a tile and 3.5 us a launch; a split takes one tile per cluster and 3 or
-// 5.5 us (2 or 4 pairs) for the meeting of the partial sums, and pays where the tiles leave most pairs idle
-// and K is long. (512 x 4096 x 12288: 26 us at S = 2, 35.5 at 1; 240 x 3800 x 12288: 19 at 4, 35 at 1.)
-template <typename TO> static int64_t many_estimate(int64_t M, int N, int nkb, int *best) {
-    const int64_t tiles = ((M + many::BM - 1) / many::BM) * (((int64_t)N + many::BN - 1) / many::BN);
+// How the CTA pairs take a product's tiles: `whole` of them in turn, one pair each, then the rest one per
+// cluster with its K blocks split over S pairs.
+struct ManyPlan {
+    int64_t whole, tiles;
+    int S;
+    int64_t ns;  // estimated time
+};
+
+// 370 ns a K block, 1 us a tile and 3.5 us a launch; a split takes 3 or 5.5 us (2 or 4 pairs) for the meeting
+// of the partial sums, and pays for tiles that would leave most pairs idle, be it all of them or a last
+// wave's, when K is long. (512 x 4096 x 12288, 32 tiles: 25 us at S = 2, 35.5 whole; 240 x 3800 x 12288, 15
+// tiles: 19 us at 4, 35 whole.)
+template <typename TO> static ManyPlan many_plan(int64_t M, int N, int nkb) {
+    ManyPlan p{0, 0, 1, INT64_MAX};
+    p.tiles = ((M + many::BM - 1) / many::BM) * (((int64_t)N + many::BN - 1) / many::BN);
     const int pairs = resident_clusters<TO, false>(1);
-    *best = 0;
-    if (pairs < 1) return INT64_MAX;
-    int64_t ns = ((tiles + pairs - 1) / pairs) * ((int64_t)nkb * 370 + 1000) + 3500;
-    *best = 1;
-    for (int S = 2; S <= 4 && S <= nkb && tiles * S <= pairs; S *= 2) {
-        const int64_t t = (int64_t)((nkb + S - 1) / S) * 370 + 1000 + 3500 + (S == 2 ? 3000 : 5500);
-        if (t < ns && tiles <= resident_clusters<TO, true>(S)) {
-            ns = t;
-            *best = S;
-        }
+    if (pairs < 1) return p;
+    const int64_t wave = (int64_t)nkb * 370 + 1000, full = p.tiles / pairs, rest = p.tiles % pairs;
+    p.whole = p.tiles;
+    p.ns = (full + (rest ? 1 : 0)) * wave + 3500;
+    for (int S = 2; S <= 4 && S <= nkb && rest && rest * S <= pairs; S *= 2) {
+        const int64_t t = full * wave + (full ? 3500 : 0) + (int64_t)((nkb + S - 1) / S) * 370 + 4500 +
+                          (S == 2 ? 3000 : 5500);
+        if (t < p.ns && rest <= resident_clusters<TO, true>(S)) p = ManyPlan{p.tiles - rest, p.tiles, S, t};
     }
-    return ns;
+    return p;
 }
 
 template <typename TO>
 static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, const float *sa, const float *sw, void *y,
-                              int64_t M, int N, int K, int64_t ldy, int S, unsigned *err, cudaStream_t s) {
-    const int64_t mt = (M + many::BM - 1) / many::BM, tiles = mt * (((int64_t)N + many::BN - 1) / many::BN);
-    if (tiles > 0x7fffffffLL) return invalid("M*N too large for one launch");
+                              int64_t M, int N, int K, int64_t ldy, const ManyPlan &p, unsigned *err, cudaStream_t s) {
+    if (p.tiles > 0x7fffffffLL) return invalid("M*N too large for one launch");
     // y's rows suit a tensor map where their stride is a multiple of 16 bytes
     const int by_tma = (ldy * sizeof(TO)) % 16 == 0 && ldy < (1LL << 36);
     CUtensorMap ty;
@@ -871,16 +878,16 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
     if (by_tma && !row_map(&ty, y, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                            (uint64_t)N, (uint64_t)M, (uint64_t)ldy * sizeof(TO), 128 / sizeof(TO), 32))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    const int64_t most = S > 1 ? tiles : resident_clusters<TO, false>(1);
+    const unsigned mt = (unsigned)((M + many::BM - 1) / many::BM);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
-    many_config(cfg, at, (unsigned)(tiles < most ? tiles : most), S, s);
-    auto go = [&](auto kern) {
-        cudaLaunchKernelEx(&cfg, kern, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy,
-                           (unsigned)mt, (unsigned)tiles, by_tma, S, err);  // an error is left for check_launch
+    auto go = [&](auto kern, int64_t tile0, int64_t tiles, int64_t most, int S) {
+        many_config(cfg, at, (unsigned)(tiles - tile0 < most ? tiles - tile0 : most), S, s);
+        cudaLaunchKernelEx(&cfg, kern, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy, mt,
+                           (unsigned)tile0, (unsigned)tiles, by_tma, S, err);  // an error is left for check_launch
     };
-    if (S > 1) go(linear_many_kernel<TO, true>);
-    else go(linear_many_kernel<TO, false>);
+    if (p.whole > 0) go(linear_many_kernel<TO, false>, 0, p.whole, resident_clusters<TO, false>(1), 1);
+    if (p.whole < p.tiles) go(linear_many_kernel<TO, true>, p.whole, p.tiles, p.tiles - p.whole, p.S);
     return check_launch("linear_many_kernel");
 }
 
@@ -891,19 +898,20 @@ static kda_status run_linear(const void *a, const float *sa, const void *w, cons
     // more, whichever is estimated faster.
     const int sms = current_sms();
     if (sms < 2) return fail(KDA_ERR_CUDA, "the device's SM count is unavailable");
-    int S = 0;
+    ManyPlan plan{};
+    bool many_tokens = false;
     if (M > 64) {
         const int nkb = (K + KB - 1) / KB;
-        const int64_t units = ((M + 63) / 64) * (((int64_t)N + 127) / 128), many_ns = many_estimate<TO>(M, N, nkb, &S);
         int64_t few_ns = 0;
-        few_split(units, nkb, 2 * sms, &few_ns);
-        if (few_ns <= many_ns) S = 0;
+        few_split(((M + 63) / 64) * (((int64_t)N + 127) / 128), nkb, 2 * sms, &few_ns);
+        plan = many_plan<TO>(M, N, nkb);
+        many_tokens = plan.ns < few_ns;
     }
-    if (S > 0) {
+    if (many_tokens) {
         CUtensorMap ta, tw;
         if (!byte_map(&ta, a, K, M, lda, 128) || !byte_map(&tw, w, K, N, ldw, 128))
             return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-        return launch_many<TO>(ta, tw, sa, sw, y, M, N, K, ldy, S, err, s);
+        return launch_many<TO>(ta, tw, sa, sw, y, M, N, K, ldy, plan, err, s);
     }
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     CUtensorMap tw, ta;
