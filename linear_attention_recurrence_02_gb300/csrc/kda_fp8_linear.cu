@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constan
         return;
     }
     // Partial sums [token][feature] in the ring's place; each CTA adds up `per` tokens over the cluster, in
-    // the CTAs' order, all of a token's loads on their way at once.
+    // the CTAs' order, four tokens' loads on their way at once.
     const int per = (NT + S - 1) / S, f = tid & 127;
     float *part = reinterpret_cast<float *>(sm);
     if (warp < 4) {
@@ -345,62 +345,109 @@ __global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constan
         for (int j = 0; j < NT; ++j) part[j * 128 + tid] = ok ? acc[j] : __uint_as_float(0x7fffffffu);
     }
     cluster_sync();
-    for (int j = r * per + (tid >> 7); j < (r + 1) * per && j < NT && m0 + j < M; j += 2) {
-        float v[8];
+    const int j1 = min(min((r + 1) * per, NT), M - m0);
+    for (int j0 = r * per + (tid >> 7); j0 < j1; j0 += 8) {
+        float v[4][8];
 #pragma unroll
-        for (int p = 0; p < 8; ++p) v[p] = p < S ? peer_load(part + j * 128 + f, (uint32_t)p) : 0.f;
-        float sum = v[0];
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int p = 1; p < 8; ++p) sum += v[p];
-        if (n0 + f < N) Elem<TO>::store(y + (int64_t)(m0 + j) * ldy + n0 + f, sum);
+            for (int p = 0; p < 8; ++p)
+                v[i][p] = p < S && j0 + 2 * i < j1 ? peer_load(part + (j0 + 2 * i) * 128 + f, (uint32_t)p) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float sum = v[i][0];
+#pragma unroll
+            for (int p = 1; p < 8; ++p) sum += v[i][p];
+            if (j0 + 2 * i < j1 && n0 + f < N)
+                Elem<TO>::store(y + (int64_t)(m0 + j0 + 2 * i) * ldy + n0 + f, sum);
+        }
     }
     cluster_sync();  // no CTA leaves while another still reads its sums
 }
 
-// CTAs of a cluster (a split of K) for `units` tiles of nkb K blocks on `slots` CTA slots (two
-// per SM), and the time in ns that this takes where the weights' bytes are not what bounds it.
-// Measured: 410 ns a K block with both slots of an SM busy, 3 us for a wave's start and end,
-// 2 us for the meeting of the partial sums. (1 x 12288 x 4096: 96 tiles, 10.6 us at S = 3, 11.5
-// at 1, 14.0 at 4; 64 x 4096 x 12288: 32 tiles, 13.1 us at 8, 30 at 1.)
-static int few_split(int64_t units, int nkb, int slots, int64_t *ns) {
-    int best = 1;
-    *ns = INT64_MAX;
+static void few_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], unsigned ctas, int smem, int S,
+                       cudaStream_t s) {
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)S;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+}
+
+// Clusters of S CTAs that run at once on the current device (0: none, or an error). Two CTAs fit an SM,
+// but clusters do not always fill the SMs that they have to share: 304 CTAs as clusters of 1 or 2, 296 of 4,
+// 276 of 6. The occupancy query counts one CTA per SM for any kernel that allocates TMEM, although two run
+// (13.8 of 16 warps active on average at 288 CTAs), so a stand-in of the same shape is asked.
+__global__ void __launch_bounds__(256, 2) few_stand_in() {}
+static int few_resident(int S) {
+    static std::atomic<int> known[9][64];  // value + 1
+    constexpr int SMEM = Few<16>::SMEM;    // the largest of the three
+    static_assert(Few<32>::SMEM <= SMEM && Few<64>::SMEM <= SMEM, "two CTAs of each size fit an SM");
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return 0;
+    int n = known[S][dev].load(std::memory_order_acquire);
+    if (n > 0) return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    few_config(cfg, at, (unsigned)S, SMEM, S, nullptr);
+    cfg.numAttrs = 1;
+    if (smem_attr_once<few_stand_in>(SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, few_stand_in, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[S][dev].store(n + 1, std::memory_order_release);
+    return n;
+}
+
+// CTAs of a cluster (a split of K) for M x N x K and the time in ns that this takes where the weights'
+// bytes are not what bounds it (S = 0: the kernel cannot run here). Measured: 200, 300 or 410 ns a K block
+// (16, 32 or 64 tokens), 3 us a launch, 4 us a further wave, and the meeting of the partial sums.
+// (1 x 12288 x 4096, 96 tiles: 10.2 us at S = 3, 11.1 at 1, 14.3 at 4; 64 x 4096 x 12288, 32 tiles: 13.1 us
+// at 8, 30 at 1; 100 x 1000 x 1040, 16 tiles: 5.0 us at 4, 6.5 at 1 or 2.)
+struct FewPlan {
+    int64_t units;
+    int S;
+    int64_t ns;
+};
+template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
+    constexpr int64_t BLOCK_NS = NT == 16 ? 200 : NT == 32 ? 300 : 410;
+    constexpr int64_t MEET_NS[9] = {0, 0, 1650, 1200, 900, 1470, 1460, 1500, 1900};
+    FewPlan p{((M + NT - 1) / NT) * (((int64_t)N + 127) / 128), 0, INT64_MAX};
     for (int S = 1; S <= 8 && S <= nkb; ++S) {
-        const int64_t waves = (units * S + slots - 1) / slots;
-        const int64_t t = waves * ((int64_t)((nkb + S - 1) / S) * 410 + 3000) + (S > 1 ? 2000 : 0) + 1000;
-        if (t < *ns) {
-            *ns = t;
-            best = S;
+        const int at_once = few_resident(S);
+        if (at_once < 1) continue;
+        const int64_t waves = (p.units + at_once - 1) / at_once;
+        const int64_t t = waves * (int64_t)((nkb + S - 1) / S) * BLOCK_NS + (waves - 1) * 4000 + 3000 + MEET_NS[S];
+        if (t < p.ns) {
+            p.ns = t;
+            p.S = S;
         }
     }
-    return best;
+    return p;
 }
 
 template <int NT, typename TO>
 static kda_status launch_few(const CUtensorMap &tw, const CUtensorMap &ta, const float *sa, const float *sw, void *y,
-                             int64_t M, int N, int K, int64_t ldy, int sms, unsigned *err, cudaStream_t s) {
-    using F = Few<NT>;
-    if (smem_attr_once<linear_few_kernel<NT, TO>>(F::SMEM) != cudaSuccess)
-        return check_launch("linear_few_kernel (shared memory attribute)");
-    const int64_t mt = (M + NT - 1) / NT, units = mt * (((int64_t)N + 127) / 128);
-    int64_t ns = 0;
-    const int nkb = (K + KB - 1) / KB, S = few_split(units, nkb, 2 * sms, &ns);
-    if (units * S > 0x7fffffffLL) return invalid("M*N too large for one launch");
+                             int64_t M, int N, int K, int64_t ldy, unsigned *err, cudaStream_t s) {
+    const int nkb = (K + KB - 1) / KB;
+    const FewPlan p = few_plan<NT>(M, N, nkb);
+    if (p.S < 1 || smem_attr_once<linear_few_kernel<NT, TO>>(Few<NT>::SMEM) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(KDA_ERR_CUDA, "linear_few_kernel does not fit the device");
+    }
+    if (p.units * p.S > 0x7fffffffLL) return invalid("M*N too large for one launch");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * S));
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = F::SMEM;
-    cfg.stream = s;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)S;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
+    few_config(cfg, at, (unsigned)(p.units * p.S), Few<NT>::SMEM, p.S, s);
     cudaLaunchKernelEx(&cfg, linear_few_kernel<NT, TO>, tw, ta, sa, sw, static_cast<TO *>(y), (int)M, N, nkb, ldy,
-                       (int)mt, S, err);  // an error is left for check_launch
+                       (int)((M + NT - 1) / NT), p.S, err);  // an error is left for check_launch
     return check_launch("linear_few_kernel");
 }
 
@@ -847,7 +894,7 @@ struct ManyPlan {
     int64_t ns;  // estimated time
 };
 
-// 370 ns a K block, 1 us a tile and 3.5 us a launch; a split takes 3 or 5.5 us (2 or 4 pairs) for the meeting
+// 350 ns a K block (330 with half the SMs idle, 370 with none), 1 us a tile and 3.5 us a launch; a split takes 3 or 5.5 us (2 or 4 pairs) for the meeting
 // of the partial sums, and pays for tiles that would leave most pairs idle, be it all of them or a last
 // wave's, when K is long. (512 x 4096 x 12288, 32 tiles: 25 us at S = 2, 35.5 whole; 240 x 3800 x 12288, 15
 // tiles: 19 us at 4, 35 whole.)
@@ -856,11 +903,11 @@ template <typename TO> static ManyPlan many_plan(int64_t M, int N, int nkb) {
     p.tiles = ((M + many::BM - 1) / many::BM) * (((int64_t)N + many::BN - 1) / many::BN);
     const int pairs = resident_clusters<TO, false>(1);
     if (pairs < 1) return p;
-    const int64_t wave = (int64_t)nkb * 370 + 1000, full = p.tiles / pairs, rest = p.tiles % pairs;
+    const int64_t wave = (int64_t)nkb * 350 + 1000, full = p.tiles / pairs, rest = p.tiles % pairs;
     p.whole = p.tiles;
     p.ns = (full + (rest ? 1 : 0)) * wave + 3500;
     for (int S = 2; S <= 4 && S <= nkb && rest && rest * S <= pairs; S *= 2) {
-        const int64_t t = full * wave + (full ? 3500 : 0) + (int64_t)((nkb + S - 1) / S) * 370 + 4500 +
+        const int64_t t = full * wave + (full ? 3500 : 0) + (int64_t)((nkb + S - 1) / S) * 350 + 4500 +
                           (S == 2 ? 3000 : 5500);
         if (t < p.ns && rest <= resident_clusters<TO, true>(S)) p = ManyPlan{p.tiles - rest, p.tiles, S, t};
     }
@@ -896,16 +943,12 @@ static kda_status run_linear(const void *a, const float *sa, const void *w, cons
                              int N, int K, int64_t lda, int64_t ldw, int64_t ldy, unsigned *err, cudaStream_t s) {
     // Up to 64 tokens a weight tile is read once and its bytes bound the call: the few-token kernel. With
     // more, whichever is estimated faster.
-    const int sms = current_sms();
-    if (sms < 2) return fail(KDA_ERR_CUDA, "the device's SM count is unavailable");
     ManyPlan plan{};
     bool many_tokens = false;
     if (M > 64) {
         const int nkb = (K + KB - 1) / KB;
-        int64_t few_ns = 0;
-        few_split(((M + 63) / 64) * (((int64_t)N + 127) / 128), nkb, 2 * sms, &few_ns);
         plan = many_plan<TO>(M, N, nkb);
-        many_tokens = plan.ns < few_ns;
+        many_tokens = plan.ns < few_plan<64>(M, N, nkb).ns;
     }
     if (many_tokens) {
         CUtensorMap ta, tw;
@@ -918,9 +961,9 @@ static kda_status run_linear(const void *a, const float *sa, const void *w, cons
     if (!byte_map(&tw, w, K, N, ldw, 128) || !byte_map(&ta, a, K, M, lda, nt))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     switch (nt) {
-    case 16: return launch_few<16, TO>(tw, ta, sa, sw, y, M, N, K, ldy, sms, err, s);
-    case 32: return launch_few<32, TO>(tw, ta, sa, sw, y, M, N, K, ldy, sms, err, s);
-    default: return launch_few<64, TO>(tw, ta, sa, sw, y, M, N, K, ldy, sms, err, s);
+    case 16: return launch_few<16, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
+    case 32: return launch_few<32, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
+    default: return launch_few<64, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
     }
 }
 
