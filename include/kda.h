@@ -302,7 +302,8 @@ kda_status kda_gated_rmsnorm_fp8(const void *o, const void *gate, const float *w
  *   a [M,K] e4m3, row stride lda; a_scales [ceil(K/128),M] fp32
  *   w [N,K] e4m3, row stride ldw; w_scales [ceil(N/128),ceil(K/128)] fp32
  *   y [M,N] out_dtype, row stride ldy (strides in elements); elements between
- *     N and ldy keep their values. y may not alias another argument.
+ *     N and ldy keep their values. y may not alias another argument. With many
+ *     tokens, rows a multiple of 16 bytes apart are written fastest.
  * e4m3 products are exact and are summed in fp32; the sums of the K blocks are
  * scaled and joined in fp32, in an order that depends on the sizes alone: the
  * same inputs give the same bits.

@@ -532,6 +532,50 @@ __device__ __forceinline__ void add2(uint64_t &a, float x, float y) {
     asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(d));
 }
 
+__device__ __forceinline__ void store_if(bool yes, void *to, uint32_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}"
+                 :: "r"((uint32_t)yes), "l"(to), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void store_if(bool yes, void *to, uint16_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.b16 [%1], %2;\n\t}"
+                 :: "r"((uint32_t)yes), "l"(to), "h"(v) : "memory");
+}
+
+// A warp stores `rows` rows of `cols` elements from its staged 128-byte rows (16-byte pieces swizzled by the
+// row) to rows of any alignment: 4 bytes a lane, sixteen rows' reads in flight, predicated stores. Where a
+// row of 2-byte elements starts between two words, each lane's word is joined from two neighbours' halves and
+// the elements at the ends go by themselves. (3000 x 20001 x 464: bf16 78 us, 131 with an element a lane and
+// a branch, 80 at eight rows, 84 at four; f32 86, 88, 88 and 93. Rows of 20000 elements, which a tensor copy
+// stores: 47 and 61. Rows that start inside a 32-byte sector also write that sector in two parts.)
+template <typename TO>
+__device__ __forceinline__ void store_rows(TO *to, int64_t ld, const uint8_t *from, int rows, int cols) {
+    constexpr int B = 16;
+    const int lane = threadIdx.x & 31;
+    for (int i0 = 0; i0 < rows; i0 += B) {
+        uint32_t w[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            w[j] = *reinterpret_cast<const uint32_t *>(from + (i0 + j) * 128 + (((lane >> 2) ^ (j & 7)) << 4) +
+                                                       (lane & 3) * 4);
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            if (i0 + j >= rows) break;
+            TO *row = to + (i0 + j) * ld;
+            if constexpr (sizeof(TO) == 4) {
+                store_if(lane < cols, row + lane, w[j]);
+            } else {
+                const int odd = (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 1, c = 2 * lane + odd;
+                const uint32_t up = __shfl_down_sync(0xffffffffu, w[j], 1);
+                const uint32_t pair = odd ? __funnelshift_r(w[j], up, 16) : w[j];
+                store_if(c + 1 < cols, row + c, pair);
+                store_if(c + 1 == cols, row + c, (uint16_t)pair);
+                store_if(odd && lane == 0, row, (uint16_t)w[j]);
+            }
+        }
+    }
+}
+
 template <typename TO, bool SPLIT>
 __global__ void __launch_bounds__(many::NTHREADS, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
@@ -705,11 +749,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                             bulk_commit();
                         }
                     } else {
-                        const int rows = M - mw < 32 ? M - mw : 32;
-                        for (int i = 0; i < rows; ++i)
-                            for (int c = lane; c < JR && n + c < N; c += 32)
-                                y[(mw + i) * ldy + n + c] = *reinterpret_cast<const TO *>(
-                                    out + i * 128 + (((c / V) ^ (i & 7)) << 4) + (c % V) * (int)sizeof(TO));
+                        store_rows(y + mw * ldy + n, ldy, out, M - mw < 32 ? M - mw : 32, N - n < JR ? N - n : JR);
                     }
                 }
             }

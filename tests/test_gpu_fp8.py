@@ -493,3 +493,20 @@ def test_linear_pairs_that_share_a_tile(env, M, N, K, out):
     for _ in range(3):
         kda.kda_fp8_linear(a, sa, w, sw, again)
         assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("N,off,ld", [(1001, 0, 1001), (1002, 0, 1002), (1000, 8, 1031), (1003, 8, 1040), (260, 0, 263),
+                                      (961, 0, 963)])
+def test_linear_many_tokens_unaligned_rows(env, N, off, ld, out):
+    """Rows of the result at every alignment that the element size allows, whole and partial tiles: each
+    element, and what lies beside it."""
+    torch, kda = env
+    M, K = 700, 256
+    a, sa, w, sw = _lin_case(torch, 150 + N, M, N, K)
+    big = torch.full((M + 2, ld), -9.0, dtype=_dt(torch, out), device="cuda")
+    y = big[:M, off:off + N]
+    kda.kda_fp8_linear(a, sa, w, sw, y)
+    _lin_check(torch, y, a, sa, w, sw, f"{N} {off} {ld}")
+    assert bool((big[:M, :off] == -9.0).all()) and bool((big[:M, off + N:] == -9.0).all())
+    assert bool((big[M:] == -9.0).all())
