@@ -471,7 +471,7 @@ namespace many {
 constexpr int BM = 256, BN = 256;                 // tile of a pair
 constexpr int A_BYTES = 128 * KB, W_BYTES = 128 * KB;
 constexpr int STAGE = A_BYTES + W_BYTES;          // bytes per CTA: tokens, then weights
-constexpr int ST = 5, AS = 2;
+constexpr int ST = 5, AS = 2;                      // stages of operands at most, accumulators
 constexpr int JW = 8, JC = 128;                   // joining warps, features of each
 constexpr int NTHREADS = 32 * (JW + 4);
 // Registers a thread: launched with REGS, split so that the joining warps hold their sums and neither
@@ -480,8 +480,12 @@ constexpr int REGS = 168, REGS_JOIN = 216, REGS_ISSUE = 72;
 static_assert(JW * REGS_JOIN + 4 * REGS_ISSUE == (JW + 4) * REGS, "the split draws on the launch's registers");
 constexpr int CK = 4, CS = 4;                     // K blocks of scales per chunk, chunks in flight
 constexpr int CHUNK = CK * 256 * 4;               // [CK][feature half][token] products of the two scales
-constexpr int OUT = ST * STAGE;                   // results on their way out: per joining warp 32 rows of 128 B
-constexpr int SCALES = OUT + JW * 4096;
+// Behind the stages the results on their way out: per joining warp one piece of 32 rows of 128 B beside five
+// stages, or two beside four (many_stages).
+constexpr int PIECE = 4096;
+constexpr int SCALES = ST * STAGE + JW * PIECE;
+static_assert((ST - 1) * STAGE + JW * 2 * PIECE == SCALES, "a stage is a piece per joining warp");
+static_assert(3 * 32768 <= (ST - 1) * STAGE, "a split's partial sums, of 2 or 4 pairs, take the ring's place");
 constexpr int BARS = SCALES + CS * CHUNK;
 constexpr int SMEM = BARS + (2 * ST + 2 * AS + 2 * CS) * 8 + 16 + 1024;
 }  // namespace many
@@ -530,6 +534,11 @@ __device__ __forceinline__ void add2(uint64_t &a, float x, float y) {
     uint64_t d;
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
     asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(d));
+}
+
+// until at most N of this thread's committed bulk stores have still to read their shared memory
+template <int N> __device__ __forceinline__ void bulk_wait_read_but() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void store_if(bool yes, void *to, uint32_t v) {
@@ -581,7 +590,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_y, const float *__restrict__ sa,
                        const float *__restrict__ sw, TO *__restrict__ y, int M, int N, int nkb, int64_t ldy,
-                       unsigned mt, unsigned tile0, unsigned tiles, int by_tma, int S,
+                       unsigned mt, unsigned tile0, unsigned tiles, int by_tma, int S, int stages,
                        unsigned *err) {
     using namespace tc;
     using namespace many;
@@ -600,7 +609,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
     // K blocks of this pair
     const int kb0 = SPLIT ? (int)((int64_t)nkb * sp / S) : 0, kb1 = SPLIT ? (int)((int64_t)nkb * (sp + 1) / S) : nkb;
     if (tid == 0) {
-        for (int i = 0; i < ST; ++i) {
+        for (int i = 0; i < stages; ++i) {
             mbar_init(full + i, 1);  // the even CTA's own arrival; both CTAs' bytes
             mbar_init(empty + i, 1);
         }
@@ -624,7 +633,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
     if (warp == JW && elect_one()) {
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_w);
-        for (int kb = kb0; kb < kb0 + ST && kb < kb1; ++kb)
+        for (int kb = kb0; kb < kb0 + stages && kb < kb1; ++kb)
             tma_prefetch_l2_2d(&tm_w, kb * KB, (int)(first / mt) * BN + (int)rank * 128);
     }
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
@@ -643,7 +652,9 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
         const uint32_t rel0 = peer_addr(aempty, lead), rel1 = peer_addr(aempty + 1, lead);
         const int mrow = (int)rank * 128 + 32 * (warp & 3) + lane;
         const float *mine = reinterpret_cast<const float *>(sm + SCALES) + half * 128 + 32 * (warp & 3) + lane;
-        uint8_t *out = sm + OUT + warp * 4096;
+        const bool two = stages < ST;  // pieces
+        uint8_t *out = sm + stages * STAGE + warp * (two ? 2 * PIECE : PIECE);
+        int flip = 0;
         int as = 0, cs = 0;
         uint32_t ph = 0, cph = 0;
         for (unsigned tile = first; tile < tiles; tile += npairs) {
@@ -731,7 +742,12 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                     const int n = n0 + r * JR;
                     if (n >= N) break;
                     if (SPLIT && (2 * half + r * JR / 64) / (4 / S) != sp) continue;  // another pair's
-                    if (lane == 0) bulk_wait_read();  // the buffer's last copy has read it
+                    uint8_t *piece = out + flip;
+                    if (two) flip ^= PIECE;
+                    if (lane == 0) {  // the piece's last copy has read it
+                        if (two) bulk_wait_read_but<1>();
+                        else bulk_wait_read();
+                    }
                     __syncwarp();
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
@@ -739,17 +755,17 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                         TO *e = reinterpret_cast<TO *>(&raw);
 #pragma unroll
                         for (int i = 0; i < V; ++i) Elem<TO>::store(e + i, at(r * JR + q * V + i));
-                        *reinterpret_cast<uint4 *>(out + lane * 128 + ((q ^ (lane & 7)) << 4)) = raw;
+                        *reinterpret_cast<uint4 *>(piece + lane * 128 + ((q ^ (lane & 7)) << 4)) = raw;
                     }
                     fence_async_smem();
                     __syncwarp();
                     if (by_tma) {
                         if (lane == 0) {
-                            tma_store_2d(&tm_y, out, n, mw);
+                            tma_store_2d(&tm_y, piece, n, mw);
                             bulk_commit();
                         }
                     } else {
-                        store_rows(y + mw * ldy + n, ldy, out, M - mw < 32 ? M - mw : 32, N - n < JR ? N - n : JR);
+                        store_rows(y + mw * ldy + n, ldy, piece, M - mw < 32 ? M - mw : 32, N - n < JR ? N - n : JR);
                     }
                 }
             }
@@ -773,7 +789,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                         tma_load_pair(d, &tm_a, bar, kb * KB, row_a);
                         tma_load_pair(d + A_BYTES, &tm_w, bar, kb * KB, row_w);
                     }
-                    if (++st == ST) {
+                    if (++st == stages) {
                         st = 0;
                         ph ^= 1;
                     }
@@ -782,9 +798,9 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
             // Every copy of both CTAs lands before shared memory goes away (the even CTA's barriers count
             // them): the ring's next phase of each stage is the one that the last copies complete.
             if (rank == 0)
-                for (int i = 0; i < ST; ++i) {
+                for (int i = 0; i < stages; ++i) {
                     if (--st < 0) {
-                        st = ST - 1;
+                        st = stages - 1;
                         ph ^= 1;
                     }
                     if (!tc::mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
@@ -810,7 +826,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                         }
                         as ^= 1;
                         aph ^= as == 0;
-                        if (++st == ST) {
+                        if (++st == stages) {
                             st = 0;
                             ph ^= 1;
                         }
@@ -954,6 +970,12 @@ template <typename TO> static ManyPlan many_plan(int64_t M, int N, int nkb) {
     return p;
 }
 
+// Four stages and two pieces where a pair has tiles after its first and short ones: results leave beside the next
+// tile's K blocks (4864 x 4096 x 512: 14.6 us, 15.7 with one piece; x 2048: 32.2 and 33.0; 3000 x 20000 x 464:
+// 44.6 and 47.8). Else five and one, for weights that come from memory (128 x 12288 x 4096: 16.5 us, 17.6 with
+// four; 182 x 10432 x 11312: 38.6 and 41.6; 4096 x 4096 x 12288 the same).
+static int many_stages(bool more_tiles, int nkb) { return more_tiles && nkb <= 16 ? many::ST - 1 : many::ST; }
+
 template <typename TO>
 static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, const float *sa, const float *sw, void *y,
                               int64_t M, int N, int K, int64_t ldy, const ManyPlan &p, unsigned *err, cudaStream_t s) {
@@ -966,12 +988,13 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
                            (uint64_t)N, (uint64_t)M, (uint64_t)ldy * sizeof(TO), 128 / sizeof(TO), 32))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     const unsigned mt = (unsigned)((M + many::BM - 1) / many::BM);
+    const int nkb = (K + KB - 1) / KB;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     auto go = [&](auto kern, int64_t tile0, int64_t tiles, int64_t most, int S) {
         many_config(cfg, at, (unsigned)(tiles - tile0 < most ? tiles - tile0 : most), S, s);
-        cudaLaunchKernelEx(&cfg, kern, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N, (K + KB - 1) / KB, ldy, mt,
-                           (unsigned)tile0, (unsigned)tiles, by_tma, S, err);  // an error is left for check_launch
+        cudaLaunchKernelEx(&cfg, kern, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N, nkb, ldy, mt,
+                           (unsigned)tile0, (unsigned)tiles, by_tma, S, many_stages(tiles - tile0 > most, nkb), err);  // an error is left for check_launch
     };
     if (p.whole > 0) go(linear_many_kernel<TO, false>, 0, p.whole, resident_clusters<TO, false>(1), 1);
     if (p.whole < p.tiles) go(linear_many_kernel<TO, true>, p.whole, p.tiles, p.tiles - p.whole, p.S);
