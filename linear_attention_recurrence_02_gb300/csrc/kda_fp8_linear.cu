@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                     }
                     fence_async_smem();
                     __syncwarp();
-                    if (by_tma) {
+                    if (by_tma && (N % V == 0 || n + JR <= N)) {  // the copy would write all of a 16-byte piece
                         if (lane == 0) {
                             tma_store_2d(&tm_y, piece, n, mw);
                             bulk_commit();

@@ -496,13 +496,16 @@ def test_linear_pairs_that_share_a_tile(env, M, N, K, out):
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-@pytest.mark.parametrize("N,off,ld", [(1001, 0, 1001), (1002, 0, 1002), (1000, 8, 1031), (1003, 8, 1040), (260, 0, 263),
-                                      (961, 0, 963)])
-def test_linear_many_tokens_unaligned_rows(env, N, off, ld, out):
+@pytest.mark.parametrize("M,N,off,ld", [(700, 1001, 0, 1001), (700, 1002, 0, 1002), (700, 1000, 8, 1031),
+                                        (700, 1003, 8, 1040), (700, 260, 0, 263), (700, 961, 0, 963),
+                                        (1500, 2001, 0, 2001), (1500, 2002, 0, 2002), (1530, 2000, 8, 2031),
+                                        (1509, 2003, 8, 2040), (1500, 1985, 8, 1994), (1500, 2047, 0, 2048),
+                                        (2600, 2603, 0, 2608)])
+def test_linear_rows_of_any_alignment(env, M, N, off, ld, out):
     """Rows of the result at every alignment that the element size allows, whole and partial tiles: each
     element, and what lies beside it."""
     torch, kda = env
-    M, K = 700, 256
+    K = 256
     a, sa, w, sw = _lin_case(torch, 150 + N, M, N, K)
     big = torch.full((M + 2, ld), -9.0, dtype=_dt(torch, out), device="cuda")
     y = big[:M, off:off + N]
@@ -510,3 +513,20 @@ def test_linear_many_tokens_unaligned_rows(env, N, off, ld, out):
     _lin_check(torch, y, a, sa, w, sw, f"{N} {off} {ld}")
     assert bool((big[:M, :off] == -9.0).all()) and bool((big[:M, off + N:] == -9.0).all())
     assert bool((big[M:] == -9.0).all())
+
+
+@pytest.mark.parametrize("K", [2048, 2064])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_several_tiles_a_pair(env, K, out):
+    """More tiles than CTA pairs at 16 and 17 K blocks: results that leave beside the next tile, and ahead of it."""
+    torch, kda = env
+    M, N = 2600, 2312
+    a, sa, w, sw = _lin_case(torch, 160 + K, M, N, K)
+    y = torch.full((M, N), float("nan"), dtype=_dt(torch, out), device="cuda")
+    kda.kda_fp8_linear(a, sa, w, sw, y)
+    assert bool(torch.isfinite(y).all())
+    rows = torch.arange(0, M, 13, device="cuda")
+    _lin_check(torch, y[rows], a.view(torch.uint8)[rows].view(a.dtype), sa[:, rows], w, sw, f"{M}x{N}x{K}")
+    again = torch.empty_like(y)
+    kda.kda_fp8_linear(a, sa, w, sw, again)
+    assert torch.equal(y, again)
