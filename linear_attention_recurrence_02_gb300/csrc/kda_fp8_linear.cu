@@ -123,17 +123,22 @@ __device__ __forceinline__ void tma_load_once(void *dst, const CUtensorMap *map,
 }
 
 // ---------------------------------------------------------------- few tokens
-// A CTA owns 128 weight rows (the MMA's M axis: TMEM lane = output feature),
-// NT tokens (its N axis) and, as one of the S CTAs of a cluster, a run of K
-// blocks, so that a step with few tokens still feeds whole 128-row tiles from
-// every SM: the weights, read once, are what bounds it. Warps 0-3 join the
-// block sums (a thread holds its feature's NT fp32 sums; the products of the
-// token scales with the weight block's come from shared memory), warp 4
-// streams the weight and token tiles through a ring of ST stages, warp 5 issues
-// a block's four MMAs into one of AS accumulators, warps 6 and 7 form the
+// A unit is 128 weight rows (the MMA's M axis: TMEM lane = output feature) and
+// NT tokens (its N axis). The weights, read once, are what bounds it: a step
+// with few tokens still feeds whole 128-row tiles from every SM, as S CTAs of a
+// cluster with a run of the K blocks each (SPLIT), or as CTAs that walk several
+// units, so that one's first blocks arrive while the one before is stored (128 x
+// 36864 x 4096: 29.5 us, 33.3 with a CTA per unit). JW warps join the block
+// sums (a thread holds its feature's sums for TPW tokens; the products of the
+// token scales with the weight block's come from shared memory), the next
+// streams the weight and token tiles through a ring of ST stages, the next issues
+// a block's four MMAs into one of AS accumulators, the last two form the
 // scales' products of CK blocks at a time. The cluster's partial sums meet in
 // shared memory: each CTA adds up its share of the tokens over the S CTAs in
-// their order. Two CTAs fit an SM.
+// their order. Two CTAs fit an SM, of 128 tokens one.
+// Why 128 tokens: the weight tile is read once where 64 would read it twice, and
+// a tile of 256 x 256 would be half empty (100 x 12288 x 8192: 23.8 us, 31.8 at
+// 64, 27.4 in the many-token kernel; 80 x 2912 x 4096: 7.9, 8.5 and 11.8).
 // A weight tile that one CTA alone reads is marked first to leave L2 (64 x
 // 36864 x 4096: 27.1 us, 28.5 without), where the state, the activations and
 // the next call's tokens stay.
@@ -141,10 +146,13 @@ __device__ __forceinline__ void tma_load_once(void *dst, const CUtensorMap *map,
 // has completed it only prefetches weight tiles into L2, which cannot serve a
 // stale value; every read and write comes after griddepcontrol.wait.
 template <int NT> struct Few {
+    static constexpr int JW = NT == 128 ? 8 : 4;      // joining warps: 4 for up to 64 tokens each
+    static constexpr int TPW = NT / (JW / 4);         // tokens of a joining warp
+    static constexpr int NTHREADS = 32 * (JW + 4), PER_SM = NT == 128 ? 1 : 2;  // CTAs an SM
     static constexpr int STAGE = 128 * KB + NT * KB;  // bytes: weights, then tokens
-    static constexpr int ST = NT == 16 ? 6 : NT == 32 ? 5 : 4;
+    static constexpr int ST = NT == 16 || NT == 128 ? 6 : NT == 32 ? 5 : 4;
     static constexpr int AS = 4;                      // accumulators
-    static constexpr int COLS = NT * AS;              // TMEM columns (64, 128 or 256)
+    static constexpr int COLS = NT * AS;              // TMEM columns (64 to 512)
     static constexpr int CK = 4, CS = 2;              // K blocks of scales per chunk, chunks in flight
     static constexpr int SCALES = ST * STAGE;
     static constexpr int BARS = SCALES + CS * CK * NT * 4;
@@ -152,12 +160,35 @@ template <int NT> struct Few {
     static_assert(NT * 128 * 4 <= ST * STAGE, "the partial sums take the ring's place");
 };
 
-template <int NT, typename TO>
-__global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constant__ CUtensorMap tm_w,
-                                                         const __grid_constant__ CUtensorMap tm_a,
-                                                         const float *__restrict__ sa, const float *__restrict__ sw,
-                                                         TO *__restrict__ y, int M, int N, int nkb, int64_t ldy, int mt,
-                                                         int S, unsigned *err) {
+// Tokens j0, j0 + G, ... below j1 of a feature: the sum of the S CTAs' partial sums (at most P) in the CTAs'
+// order, 32 loads on their way at once.
+template <int P, int G, typename TO>
+__device__ __forceinline__ void add_parts(const float *part, int j0, int j1, int S, bool live, TO *y, int64_t ldy) {
+    constexpr int R = 32 / P;
+    for (; j0 < j1; j0 += R * G) {
+        float v[R][P];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                v[i][p] = p < S && j0 + G * i < j1 ? peer_load(part + (j0 + G * i) * 128, (uint32_t)p) : 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float sum = v[i][0];
+#pragma unroll
+            for (int p = 1; p < P; ++p) sum += v[i][p];
+            if (j0 + G * i < j1 && live) Elem<TO>::store(y + (int64_t)(j0 + G * i) * ldy, sum);
+        }
+    }
+}
+
+template <int NT, typename TO, bool SPLIT>
+__global__ void __launch_bounds__(Few<NT>::NTHREADS, Few<NT>::PER_SM)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_a,
+                      const float *__restrict__ sa, const float *__restrict__ sw,
+                      TO *__restrict__ y, int M, int N, int nkb, int64_t ldy, int mt,
+                      int S, unsigned units, unsigned *err) {
     using namespace tc;
     using F = Few<NT>;
     extern __shared__ uint8_t smem_raw[];
@@ -167,9 +198,14 @@ __global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constan
     uint32_t *s_taddr = reinterpret_cast<uint32_t *>(sempty + F::CS);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
-    const int r = (int)(blockIdx.x % (unsigned)S), unit = (int)(blockIdx.x / (unsigned)S);
-    const int nt = unit / mt, n0 = nt * 128, m0 = (unit - nt * mt) * NT;
-    const int k0 = (int)((int64_t)nkb * r / S), k1 = (int)((int64_t)nkb * (r + 1) / S);  // K blocks of this CTA
+    // SPLIT: one of the S CTAs of a cluster, which share a unit's K blocks; else a CTA walks units (128 features x
+    // NT tokens, the token tiles of a weight tile together)
+    const unsigned first = SPLIT ? blockIdx.x / (unsigned)S : blockIdx.x;
+    const int r = SPLIT ? (int)(blockIdx.x - first * (unsigned)S) : 0;
+    auto feature = [&](unsigned u) { return (int)(u / (unsigned)mt) * 128; };
+    auto token = [&](unsigned u) { return (int)(u % (unsigned)mt) * NT; };
+    // K blocks of this CTA
+    const int k0 = SPLIT ? (int)((int64_t)nkb * r / S) : 0, k1 = SPLIT ? (int)((int64_t)nkb * (r + 1) / S) : nkb;
     if (tid == 0) {
         for (int i = 0; i < F::ST; ++i) {
             mbar_init(full + i, 1);
@@ -177,20 +213,20 @@ __global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constan
         }
         for (int i = 0; i < F::AS; ++i) {
             mbar_init(afull + i, 1);
-            mbar_init(aempty + i, 4);
+            mbar_init(aempty + i, F::JW);
         }
         for (int i = 0; i < F::CS; ++i) {
             mbar_init(sfull + i, 2);
-            mbar_init(sempty + i, 4);
+            mbar_init(sempty + i, F::JW);
         }
         fence_mbar_init();
     }
-    if (warp == 4 && elect_one()) {
+    if (warp == F::JW && elect_one()) {
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_a);
-        for (int i = 0; i < F::ST && k0 + i < k1; ++i) tma_prefetch_l2_2d(&tm_w, (k0 + i) * KB, n0);
+        for (int i = 0; i < F::ST && k0 + i < k1; ++i) tma_prefetch_l2_2d(&tm_w, (k0 + i) * KB, feature(first));
     }
-    if (warp == 5) {
+    if (warp == F::JW + 1) {
         tmem_alloc(s_taddr, F::COLS);
         tmem_relinquish();
     }
@@ -199,70 +235,84 @@ __global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constan
     sync_tc();
     const uint32_t tbase = *s_taddr, sbase = smem_u32(sm);
     bool ok = true;
-    float acc[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j] = 0.f;
-    if (warp < 4) {
-        const uint32_t trow = tbase + ((uint32_t)(32 * warp) << 16);
-        const float *chunks = reinterpret_cast<const float *>(sm + F::SCALES);
+    const int j0w = (warp >> 2) * F::TPW, f = tid & 127;  // a joining thread's first token, its feature
+    float acc[F::TPW];
+    if (warp < F::JW) {
+        const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + j0w;
+        const float *chunks = reinterpret_cast<const float *>(sm + F::SCALES) + j0w;
         int as = 0, cs = 0;
         uint32_t ph = 0, cph = 0;
-        for (int kb = k0; kb < k1; ++kb) {
-            const int ck = (kb - k0) % F::CK;
-            if (ck == 0) ok = wait_more(sfull + cs, cph, ok);
-            const float *sr = chunks + (cs * F::CK + ck) * NT;
-            ok = wait_more(afull + as, ph, ok);
-            __syncwarp();
-            tc_fence_after();
+        for (unsigned u = first; u < units; u += gridDim.x) {
+            const int n0 = feature(u), m0 = token(u);
 #pragma unroll
-            for (int c = 0; c < NT; c += 16) {
-                uint32_t d[16];
-                tmem_ld16(trow + as * NT + c, d);
-                tmem_ld_wait_for(d);
-                if (c == NT - 16) {  // the accumulator is read: the MMAs may write it again
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(aempty + as);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 s = *reinterpret_cast<const float4 *>(sr + c + 4 * q);
-                    acc[c + 4 * q] = fmaf(__uint_as_float(d[4 * q]), s.x, acc[c + 4 * q]);
-                    acc[c + 4 * q + 1] = fmaf(__uint_as_float(d[4 * q + 1]), s.y, acc[c + 4 * q + 1]);
-                    acc[c + 4 * q + 2] = fmaf(__uint_as_float(d[4 * q + 2]), s.z, acc[c + 4 * q + 2]);
-                    acc[c + 4 * q + 3] = fmaf(__uint_as_float(d[4 * q + 3]), s.w, acc[c + 4 * q + 3]);
-                }
-            }
-            if (++as == F::AS) {
-                as = 0;
-                ph ^= 1;
-            }
-            if (ck == F::CK - 1 || kb == k1 - 1) {  // the chunk's last: its slot may be filled again
+            for (int j = 0; j < F::TPW; ++j) acc[j] = 0.f;
+            for (int kb = k0; kb < k1; ++kb) {
+                const int ck = (kb - k0) % F::CK;
+                if (ck == 0) ok = wait_more(sfull + cs, cph, ok);
+                const float *sr = chunks + (cs * F::CK + ck) * NT;
+                ok = wait_more(afull + as, ph, ok);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sempty + cs);
-                if (++cs == F::CS) {
-                    cs = 0;
-                    cph ^= 1;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < F::TPW; c += 16) {
+                    uint32_t d[16];
+                    tmem_ld16(trow + as * NT + c, d);
+                    tmem_ld_wait_for(d);
+                    if (c == F::TPW - 16) {  // the accumulator is read: the MMAs may write it again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(aempty + as);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 s = *reinterpret_cast<const float4 *>(sr + c + 4 * q);
+                        acc[c + 4 * q] = fmaf(__uint_as_float(d[4 * q]), s.x, acc[c + 4 * q]);
+                        acc[c + 4 * q + 1] = fmaf(__uint_as_float(d[4 * q + 1]), s.y, acc[c + 4 * q + 1]);
+                        acc[c + 4 * q + 2] = fmaf(__uint_as_float(d[4 * q + 2]), s.z, acc[c + 4 * q + 2]);
+                        acc[c + 4 * q + 3] = fmaf(__uint_as_float(d[4 * q + 3]), s.w, acc[c + 4 * q + 3]);
+                    }
+                }
+                if (++as == F::AS) {
+                    as = 0;
+                    ph ^= 1;
+                }
+                if (ck == F::CK - 1 || kb == k1 - 1) {  // the chunk's last: its slot may be filled again
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sempty + cs);
+                    if (++cs == F::CS) {
+                        cs = 0;
+                        cph ^= 1;
+                    }
                 }
             }
+            if (!SPLIT && ok && n0 + f < N) {
+#pragma unroll
+                for (int j = 0; j < F::TPW; ++j)
+                    if (m0 + j0w + j < M) Elem<TO>::store(y + (int64_t)(m0 + j0w + j) * ldy + n0 + f, acc[j]);
+            }
+            if (SPLIT) break;
         }
-    } else if (warp == 4) {
+    } else if (warp == F::JW) {
         int st = 0;
         uint32_t ph = 1;  // the ring starts out free
-        for (int kb = k0; kb < k1; ++kb) {
-            ok = wait_more(empty + st, ph, ok);
-            __syncwarp();
-            if (elect_one()) {
-                uint8_t *d = sm + st * F::STAGE;
-                mbar_arrive_expect_tx(full + st, F::STAGE);
-                if (mt == 1) tma_load_once(d, &tm_w, full + st, kb * KB, n0);
-                else tma_load_2d(d, &tm_w, full + st, kb * KB, n0);
-                tma_load_2d(d + 128 * KB, &tm_a, full + st, kb * KB, m0);
+        for (unsigned u = first; u < units; u += gridDim.x) {
+            const int n0 = feature(u), m0 = token(u);
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = wait_more(empty + st, ph, ok);
+                __syncwarp();
+                if (elect_one()) {
+                    uint8_t *d = sm + st * F::STAGE;
+                    mbar_arrive_expect_tx(full + st, F::STAGE);
+                    if (mt == 1) tma_load_once(d, &tm_w, full + st, kb * KB, n0);
+                    else tma_load_2d(d, &tm_w, full + st, kb * KB, n0);
+                    tma_load_2d(d + 128 * KB, &tm_a, full + st, kb * KB, m0);
+                }
+                if (++st == F::ST) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
-            if (++st == F::ST) {
-                st = 0;
-                ph ^= 1;
-            }
+            if (SPLIT) break;
         }
         // every copy lands before shared memory is used otherwise or goes away
         for (int i = 0; i < F::ST; ++i) {
@@ -272,103 +322,92 @@ __global__ void __launch_bounds__(256, 2) linear_few_kernel(const __grid_constan
             }
             if (!mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
         }
-    } else if (warp == 5) {
+    } else if (warp == F::JW + 1) {
         int st = 0, as = 0;
         uint32_t ph = 0, aph = 1;  // the accumulators start out free
         const uint64_t a0 = sdesc_sw128(sbase, 16, 1024), b0 = sdesc_sw128(sbase + 128 * KB, 16, 1024);
-        for (int kb = k0; kb < k1; ++kb) {
-            const uint64_t a = a0 + (uint64_t)(st * (F::STAGE / 16)), b = b0 + (uint64_t)(st * (F::STAGE / 16));
-            ok = wait_more(full + st, ph, ok);
-            ok = wait_more(aempty + as, aph, ok);
-            __syncwarp();
-            tc_fence_after();
-            if (elect_one()) {
+        for (unsigned u = first; u < units; u += gridDim.x) {
+            const int n0 = feature(u), m0 = token(u);
+            for (int kb = k0; kb < k1; ++kb) {
+                const uint64_t a = a0 + (uint64_t)(st * (F::STAGE / 16)), b = b0 + (uint64_t)(st * (F::STAGE / 16));
+                ok = wait_more(full + st, ph, ok);
+                ok = wait_more(aempty + as, aph, ok);
+                __syncwarp();
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f8(tbase + as * NT, a + 2 * ks, b + 2 * ks, idesc_f8(128, NT), ks > 0);
-                mma_commit(empty + st);
-                mma_commit(afull + as);
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f8(tbase + as * NT, a + 2 * ks, b + 2 * ks, idesc_f8(128, NT), ks > 0);
+                    mma_commit(empty + st);
+                    mma_commit(afull + as);
+                }
+                if (++as == F::AS) {
+                    as = 0;
+                    aph ^= 1;
+                }
+                if (++st == F::ST) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
-            if (++as == F::AS) {
-                as = 0;
-                aph ^= 1;
-            }
-            if (++st == F::ST) {
-                st = 0;
-                ph ^= 1;
-            }
+            if (SPLIT) break;
         }
     } else {
         // the scales' products (tokens past the end take the last one's and are not stored)
-        const float *swp = sw + (int64_t)nt * nkb;
         float *chunks = reinterpret_cast<float *>(sm + F::SCALES);
+        const int t2 = tid - 32 * (F::JW + 2);
         int cs = 0;
         uint32_t cph = 1;
         constexpr int PER = F::CK * NT / 64;  // products of a chunk per lane
-        for (int kc = k0; kc < k1; kc += F::CK) {
-            float av[PER], wv[PER];
+        for (unsigned u = first; u < units; u += gridDim.x) {
+            const int n0 = feature(u), m0 = token(u);
+            const float *swp = sw + (int64_t)(n0 >> 7) * nkb;
+            for (int kc = k0; kc < k1; kc += F::CK) {
+                float av[PER], wv[PER];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = tid - 192 + 64 * i, j = e % NT, kb = kc + e / NT < k1 ? kc + e / NT : k1 - 1;
-                av[i] = __ldg(sa + (int64_t)kb * M + (m0 + j < M ? m0 + j : M - 1));
-                wv[i] = __ldg(swp + kb);
-            }
-            ok = wait_more(sempty + cs, cph, ok);
+                for (int i = 0; i < PER; ++i) {
+                    const int e = t2 + 64 * i, j = e % NT, kb = kc + e / NT < k1 ? kc + e / NT : k1 - 1;
+                    av[i] = __ldg(sa + (int64_t)kb * M + (m0 + j < M ? m0 + j : M - 1));
+                    wv[i] = __ldg(swp + kb);
+                }
+                ok = wait_more(sempty + cs, cph, ok);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) chunks[cs * F::CK * NT + tid - 192 + 64 * i] = av[i] * wv[i];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sfull + cs);
-            if (++cs == F::CS) {
-                cs = 0;
-                cph ^= 1;
+                for (int i = 0; i < PER; ++i) chunks[cs * F::CK * NT + t2 + 64 * i] = av[i] * wv[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull + cs);
+                if (++cs == F::CS) {
+                    cs = 0;
+                    cph ^= 1;
+                }
             }
+            if (SPLIT) break;
         }
     }
     if (!ok) atomicOr(err, DEVERR_TIMEOUT);
     sync_tc();
-    if (warp == 5) tmem_dealloc(tbase, F::COLS);
-    const int n = n0 + tid;
-    if (S == 1) {
-        if (warp < 4 && ok && n < N) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (m0 + j < M) Elem<TO>::store(y + (int64_t)(m0 + j) * ldy + n, acc[j]);
-        }
-        return;
-    }
-    // Partial sums [token][feature] in the ring's place; each CTA adds up `per` tokens over the cluster, in
-    // the CTAs' order, four tokens' loads on their way at once.
-    const int per = (NT + S - 1) / S, f = tid & 127;
+    if (warp == F::JW + 1) tmem_dealloc(tbase, F::COLS);
+    if (!SPLIT) return;
+    // Partial sums [token][feature] in the ring's place; each CTA adds up `per` tokens over the cluster.
+    const int n0 = feature(first), m0 = token(first), per = (NT + S - 1) / S;
     float *part = reinterpret_cast<float *>(sm);
-    if (warp < 4) {
+    if (warp < F::JW) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) part[j * 128 + tid] = ok ? acc[j] : __uint_as_float(0x7fffffffu);
+        for (int j = 0; j < F::TPW; ++j) part[(j0w + j) * 128 + f] = ok ? acc[j] : __uint_as_float(0x7fffffffu);
     }
     cluster_sync();
-    const int j1 = min(min((r + 1) * per, NT), M - m0);
-    for (int j0 = r * per + (tid >> 7); j0 < j1; j0 += 8) {
-        float v[4][8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-                v[i][p] = p < S && j0 + 2 * i < j1 ? peer_load(part + (j0 + 2 * i) * 128 + f, (uint32_t)p) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float sum = v[i][0];
-#pragma unroll
-            for (int p = 1; p < 8; ++p) sum += v[i][p];
-            if (j0 + 2 * i < j1 && n0 + f < N)
-                Elem<TO>::store(y + (int64_t)(m0 + j0 + 2 * i) * ldy + n0 + f, sum);
-        }
-    }
+    constexpr int G = F::NTHREADS / 128;
+    const int j0 = r * per + (tid >> 7), j1 = min(min((r + 1) * per, NT), M - m0);
+    TO *to = y + (int64_t)m0 * ldy + n0 + f;
+    if (S == 2) add_parts<2, G>(part + f, j0, j1, S, n0 + f < N, to, ldy);
+    else if (S <= 4) add_parts<4, G>(part + f, j0, j1, S, n0 + f < N, to, ldy);
+    else add_parts<8, G>(part + f, j0, j1, S, n0 + f < N, to, ldy);
     cluster_sync();  // no CTA leaves while another still reads its sums
 }
 
-static void few_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], unsigned ctas, int smem, int S,
-                       cudaStream_t s) {
+static void few_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], unsigned ctas, int threads, int smem,
+                       int S, cudaStream_t s) {
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -384,21 +423,22 @@ static void few_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], un
 // but clusters do not always fill the SMs that they have to share: 304 CTAs as clusters of 1 or 2, 296 of 4,
 // 276 of 6. The occupancy query counts one CTA per SM for any kernel that allocates TMEM, although two run
 // (13.8 of 16 warps active on average at 288 CTAs), so a stand-in of the same shape is asked.
-__global__ void __launch_bounds__(256, 2) few_stand_in() {}
-static int few_resident(int S) {
+template <int NTHREADS, int PER_SM> __global__ void __launch_bounds__(NTHREADS, PER_SM) few_stand_in() {}
+template <int NT> static int few_resident(int S) {
+    using F = Few<NT == 128 ? 128 : 16>;  // of the smaller three, the one with the most shared memory
+    static_assert(Few<32>::SMEM <= Few<16>::SMEM && Few<64>::SMEM <= Few<16>::SMEM, "two CTAs of each size fit an SM");
+    constexpr auto stand_in = few_stand_in<F::NTHREADS, F::PER_SM>;
     static std::atomic<int> known[9][64];  // value + 1
-    constexpr int SMEM = Few<16>::SMEM;    // the largest of the three
-    static_assert(Few<32>::SMEM <= SMEM && Few<64>::SMEM <= SMEM, "two CTAs of each size fit an SM");
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return 0;
     int n = known[S][dev].load(std::memory_order_acquire);
     if (n > 0) return n - 1;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
-    few_config(cfg, at, (unsigned)S, SMEM, S, nullptr);
+    few_config(cfg, at, (unsigned)S, F::NTHREADS, F::SMEM, S, nullptr);
     cfg.numAttrs = 1;
-    if (smem_attr_once<few_stand_in>(SMEM) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, few_stand_in, &cfg) != cudaSuccess) {
+    if (smem_attr_once<stand_in>(F::SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, stand_in, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
@@ -406,28 +446,44 @@ static int few_resident(int S) {
     return n;
 }
 
-// CTAs of a cluster (a split of K) for M x N x K and the time in ns that this takes where the weights'
-// bytes are not what bounds it (S = 0: the kernel cannot run here). Measured: 200, 300 or 410 ns a K block
-// (16, 32 or 64 tokens), 3 us a launch, 4 us a further wave, and the meeting of the partial sums.
-// (1 x 12288 x 4096, 96 tiles: 10.2 us at S = 3, 11.1 at 1, 14.3 at 4; 64 x 4096 x 12288, 32 tiles: 13.1 us
-// at 8, 30 at 1; 100 x 1000 x 1040, 16 tiles: 5.0 us at 4, 6.5 at 1 or 2.)
+// Estimated times in ns choose between kernels and splits of K; their constants are fitted to measurements at
+// 8 to 224 weight tiles of 4 to 64 K blocks, which they meet within a tenth. A call's CTAs take `ctas` and the
+// weights' bytes 2.5 ns per 16 KB tile: the longer of the two and some of the shorter.
+static int64_t with_weights(int64_t ctas, int N, int nkb) {
+    const int64_t bytes = ((int64_t)N + 127) / 128 * nkb * 5 / 2;
+    return ctas > bytes ? ctas + bytes * 3 / 20 : bytes + ctas * 3 / 20;
+}
+
+// CTAs of a cluster (a split of K) for M x N x K and the time that this takes (S = 0: the kernel cannot run
+// here). A call takes FIX and a K block BLOCK, 1.4 times that where two CTAs share an SM; the meeting of the
+// partial sums MEET (NT = 128: 600 more); CTAs that fill the GPU 1.2 us more than a few (the next call's cannot set
+// up beside them); and a further wave of clusters a call's time, of units that a CTA walks 1.6 us.
+// (1 x 12288 x 4096, 96 tiles: 10.2 us at S = 3, 11.1 at 1, 14.3 at 4; 64 x 12288 x 4096: 12.9 us at 3, 14.6 at
+// 1, 18.3 at 4; 64 x 4096 x 8192, 32 tiles: 10.7 us at 4, 20.9 at 1.)
 struct FewPlan {
     int64_t units;
-    int S;
+    int S, at_once;  // clusters that run at once
     int64_t ns;
 };
 template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
-    constexpr int64_t BLOCK_NS = NT == 16 ? 200 : NT == 32 ? 300 : 410;
-    constexpr int64_t MEET_NS[9] = {0, 0, 1650, 1200, 900, 1470, 1460, 1500, 1900};
-    FewPlan p{((M + NT - 1) / NT) * (((int64_t)N + 127) / 128), 0, INT64_MAX};
+    constexpr int64_t FIX = NT == 16 ? 2150 : NT == 32 ? 2630 : NT == 64 ? 3560 : 3940;
+    constexpr int64_t BLOCK = NT == 16 ? 194 : NT == 32 ? 208 : NT == 64 ? 263 : 283;
+    constexpr int64_t MEET[9] = {0, 0, 500, 1000, 500, 1300, 1300, 1400, 1400};
+    FewPlan p{((M + NT - 1) / NT) * (((int64_t)N + 127) / 128), 0, 0, INT64_MAX};
+    const int sms = current_sms();
     for (int S = 1; S <= 8 && S <= nkb; ++S) {
-        const int at_once = few_resident(S);
+        const int at_once = few_resident<NT>(S);
         if (at_once < 1) continue;
-        const int64_t waves = (p.units + at_once - 1) / at_once;
-        const int64_t t = waves * (int64_t)((nkb + S - 1) / S) * BLOCK_NS + (waves - 1) * 4000 + 3000 + MEET_NS[S];
+        const int64_t waves = (p.units + at_once - 1) / at_once, resident = p.units < at_once ? p.units : at_once;
+        const int64_t meet = S > 1 ? MEET[S] + (NT == 128 ? 600 : 0) : 0;
+        const int64_t block = resident * S > sms ? BLOCK * 14 / 10 : BLOCK;
+        const int64_t ctas = waves * ((nkb + S - 1) / S) * block + meet + 1200 * resident / at_once +
+                             (waves - 1) * (S > 1 ? FIX + meet + 1200 : 1600);
+        const int64_t t = FIX + with_weights(ctas, N, nkb);
         if (t < p.ns) {
             p.ns = t;
             p.S = S;
+            p.at_once = at_once;
         }
     }
     return p;
@@ -438,16 +494,19 @@ static kda_status launch_few(const CUtensorMap &tw, const CUtensorMap &ta, const
                              int64_t M, int N, int K, int64_t ldy, unsigned *err, cudaStream_t s) {
     const int nkb = (K + KB - 1) / KB;
     const FewPlan p = few_plan<NT>(M, N, nkb);
-    if (p.S < 1 || smem_attr_once<linear_few_kernel<NT, TO>>(Few<NT>::SMEM) != cudaSuccess) {
+    if (p.S < 1 || smem_attr_once<linear_few_kernel<NT, TO, false>>(Few<NT>::SMEM) != cudaSuccess ||
+        smem_attr_once<linear_few_kernel<NT, TO, true>>(Few<NT>::SMEM) != cudaSuccess) {
         cudaGetLastError();
         return fail(KDA_ERR_CUDA, "linear_few_kernel does not fit the device");
     }
     if (p.units * p.S > 0x7fffffffLL) return invalid("M*N too large for one launch");
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
-    few_config(cfg, at, (unsigned)(p.units * p.S), Few<NT>::SMEM, p.S, s);
-    cudaLaunchKernelEx(&cfg, linear_few_kernel<NT, TO>, tw, ta, sa, sw, static_cast<TO *>(y), (int)M, N, nkb, ldy,
-                       (int)((M + NT - 1) / NT), p.S, err);  // an error is left for check_launch
+    const int64_t ctas = p.S > 1 ? p.units * p.S : p.units < p.at_once ? p.units : p.at_once;
+    few_config(cfg, at, (unsigned)ctas, Few<NT>::NTHREADS, Few<NT>::SMEM, p.S, s);
+    cudaLaunchKernelEx(&cfg, p.S > 1 ? linear_few_kernel<NT, TO, true> : linear_few_kernel<NT, TO, false>, tw, ta, sa, sw,
+                       static_cast<TO *>(y), (int)M, N, nkb, ldy, (int)((M + NT - 1) / NT), p.S, (unsigned)p.units,
+                       err);  // an error is left for check_launch
     return check_launch("linear_few_kernel");
 }
 
@@ -950,10 +1009,10 @@ struct ManyPlan {
     int64_t ns;  // estimated time
 };
 
-// 350 ns a K block (330 with half the SMs idle, 370 with none), 1 us a tile and 3.5 us a launch; a split takes 3 or 5.5 us (2 or 4 pairs) for the meeting
-// of the partial sums, and pays for tiles that would leave most pairs idle, be it all of them or a last
-// wave's, when K is long. (512 x 4096 x 12288, 32 tiles: 25 us at S = 2, 35.5 whole; 240 x 3800 x 12288, 15
-// tiles: 19 us at 4, 35 whole.)
+// 350 ns a K block, 1 us a tile, 3.5 us a launch and 1.2 us more for one that fills the GPU; a split takes 3 or
+// 5.5 us (2 or 4 pairs) for the meeting of the partial sums, and pays for tiles that would leave most pairs idle,
+// be it all of them or a last wave's, when K is long. (512 x 4096 x 12288, 32 tiles: 25 us at S = 2, 35.5 whole;
+// 240 x 3800 x 12288, 15 tiles: 19 us at 4, 35 whole.)
 template <typename TO> static ManyPlan many_plan(int64_t M, int N, int nkb) {
     ManyPlan p{0, 0, 1, INT64_MAX};
     p.tiles = ((M + many::BM - 1) / many::BM) * (((int64_t)N + many::BN - 1) / many::BN);
@@ -961,10 +1020,10 @@ template <typename TO> static ManyPlan many_plan(int64_t M, int N, int nkb) {
     if (pairs < 1) return p;
     const int64_t wave = (int64_t)nkb * 350 + 1000, full = p.tiles / pairs, rest = p.tiles % pairs;
     p.whole = p.tiles;
-    p.ns = (full + (rest ? 1 : 0)) * wave + 3500;
+    p.ns = with_weights((full + (rest ? 1 : 0)) * wave, N, nkb) + 3500 + (full ? 1200 : 1200 * rest / pairs);
     for (int S = 2; S <= 4 && S <= nkb && rest && rest * S <= pairs; S *= 2) {
-        const int64_t t = full * wave + (full ? 3500 : 0) + (int64_t)((nkb + S - 1) / S) * 350 + 4500 +
-                          (S == 2 ? 3000 : 5500);
+        const int64_t t = with_weights(full * wave + (int64_t)((nkb + S - 1) / S) * 350, N, nkb) +
+                          (full ? 4700 : 1200 * rest * S / pairs) + 4500 + (S == 2 ? 3000 : 5500);
         if (t < p.ns && rest <= resident_clusters<TO, true>(S)) p = ManyPlan{p.tiles - rest, p.tiles, S, t};
     }
     return p;
@@ -1005,28 +1064,28 @@ template <typename TO>
 static kda_status run_linear(const void *a, const float *sa, const void *w, const float *sw, void *y, int64_t M,
                              int N, int K, int64_t lda, int64_t ldw, int64_t ldy, unsigned *err, cudaStream_t s) {
     // Up to 64 tokens a weight tile is read once and its bytes bound the call: the few-token kernel. With
-    // more, whichever is estimated faster.
-    ManyPlan plan{};
-    bool many_tokens = false;
+    // more, whichever is estimated fastest: that kernel, 64 or 128 tokens at a time, or the many-token one.
+    int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     if (M > 64) {
         const int nkb = (K + KB - 1) / KB;
-        plan = many_plan<TO>(M, N, nkb);
-        many_tokens = plan.ns < few_plan<64>(M, N, nkb).ns;
+        const ManyPlan plan = many_plan<TO>(M, N, nkb);
+        const int64_t ns64 = few_plan<64>(M, N, nkb).ns, ns128 = few_plan<128>(M, N, nkb).ns;
+        if (ns128 < ns64) nt = 128;
+        if (plan.ns < ns64 && plan.ns < ns128) {
+            CUtensorMap ta, tw;
+            if (!byte_map(&ta, a, K, M, lda, 128) || !byte_map(&tw, w, K, N, ldw, 128))
+                return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+            return launch_many<TO>(ta, tw, sa, sw, y, M, N, K, ldy, plan, err, s);
+        }
     }
-    if (many_tokens) {
-        CUtensorMap ta, tw;
-        if (!byte_map(&ta, a, K, M, lda, 128) || !byte_map(&tw, w, K, N, ldw, 128))
-            return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-        return launch_many<TO>(ta, tw, sa, sw, y, M, N, K, ldy, plan, err, s);
-    }
-    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     CUtensorMap tw, ta;
     if (!byte_map(&tw, w, K, N, ldw, 128) || !byte_map(&ta, a, K, M, lda, nt))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     switch (nt) {
     case 16: return launch_few<16, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
     case 32: return launch_few<32, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
-    default: return launch_few<64, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
+    case 64: return launch_few<64, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
+    default: return launch_few<128, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
     }
 }
 

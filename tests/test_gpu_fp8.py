@@ -530,3 +530,29 @@ def test_linear_several_tiles_a_pair(env, K, out):
     again = torch.empty_like(y)
     kda.kda_fp8_linear(a, sa, w, sw, again)
     assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("M,N,K", [(66, 28677, 528), (100, 40000, 144), (128, 20000, 1040), (128, 1000, 4112), (101, 4001, 8208),
+                                   (127, 12288, 272), (250, 4100, 4112), (1000, 330, 4880), (48, 40010, 272),
+                                   (9, 41000, 144)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_some_tokens(env, M, N, K, out):
+    """64 and 128 tokens at a time, split and unsplit, CTAs that walk several units: a sample of columns, what
+    lies beside the result, and the same bits twice."""
+    torch, kda = env
+    a, sa, w, sw = _lin_case(torch, 180 + M, M, N, K)
+    big = torch.full((M + 1, N + 3), -9.0, dtype=_dt(torch, out), device="cuda")
+    y = big[:M, :N]
+    kda.kda_fp8_linear(a, sa, w, sw, y)
+    kda.kda_sync_status()
+    assert bool((big[:M, N:] == -9.0).all()) and bool((big[M:] == -9.0).all())
+    assert bool(torch.isfinite(y).all())
+    # whole blocks of 128 features from the start, the middle and the end
+    nb = _fp8.nblocks(N)
+    blocks = sorted({0, 1 % nb, nb // 2, nb - 2 if nb > 1 else 0, nb - 1})
+    for b in blocks:
+        n0, n1 = 128 * b, min(128 * b + 128, N)
+        _lin_check(torch, y[:, n0:n1], a, sa, w.view(torch.uint8)[n0:n1].view(w.dtype), sw[b:b + 1], f"{M}x{N}x{K} at {n0}")
+    again = torch.empty_like(y)
+    kda.kda_fp8_linear(a, sa, w, sw, again)
+    assert torch.equal(y, again)
