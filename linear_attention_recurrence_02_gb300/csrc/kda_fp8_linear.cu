@@ -419,31 +419,35 @@ static void few_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], un
     cfg.numAttrs = 2;
 }
 
-// Clusters of S CTAs that run at once on the current device (0: none, or an error). Two CTAs fit an SM,
+// Clusters of S = 1 to `most` CTAs that run at once on the current device (0: none, or an error). Two CTAs fit an SM,
 // but clusters do not always fill the SMs that they have to share: 304 CTAs as clusters of 1 or 2, 296 of 4,
 // 276 of 6. The occupancy query counts one CTA per SM for any kernel that allocates TMEM, although two run
 // (13.8 of 16 warps active on average at 288 CTAs), so a stand-in of the same shape is asked.
 template <int NTHREADS, int PER_SM> __global__ void __launch_bounds__(NTHREADS, PER_SM) few_stand_in() {}
-template <int NT> static int few_resident(int S) {
+template <int NT> static void few_resident(int (&at_once)[9], int most) {
     using F = Few<NT == 128 ? 128 : 16>;  // of the smaller three, the one with the most shared memory
     static_assert(Few<32>::SMEM <= Few<16>::SMEM && Few<64>::SMEM <= Few<16>::SMEM, "two CTAs of each size fit an SM");
     constexpr auto stand_in = few_stand_in<F::NTHREADS, F::PER_SM>;
     static std::atomic<int> known[9][64];  // value + 1
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return 0;
-    int n = known[S][dev].load(std::memory_order_acquire);
-    if (n > 0) return n - 1;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2];
-    few_config(cfg, at, (unsigned)S, F::NTHREADS, F::SMEM, S, nullptr);
-    cfg.numAttrs = 1;
-    if (smem_attr_once<stand_in>(F::SMEM) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, stand_in, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
+    const bool found = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+    for (int S = 1; S <= most; ++S) {
+        int n = found ? known[S][dev].load(std::memory_order_acquire) - 1 : 0;
+        if (n < 0) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute at[2];
+            few_config(cfg, at, (unsigned)S, F::NTHREADS, F::SMEM, S, nullptr);
+            cfg.numAttrs = 1;
+            if (smem_attr_once<stand_in>(F::SMEM) == cudaSuccess &&
+                cudaOccupancyMaxActiveClusters(&n, stand_in, &cfg) == cudaSuccess) {
+                known[S][dev].store(n + 1, std::memory_order_release);
+            } else {
+                cudaGetLastError();
+                n = 0;
+            }
+        }
+        at_once[S] = n;
     }
-    known[S][dev].store(n + 1, std::memory_order_release);
-    return n;
 }
 
 // Estimated times in ns choose between kernels and splits of K; their constants are fitted to measurements at
@@ -470,9 +474,12 @@ template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
     constexpr int64_t BLOCK = NT == 16 ? 194 : NT == 32 ? 208 : NT == 64 ? 263 : 283;
     constexpr int64_t MEET[9] = {0, 0, 500, 1000, 500, 1300, 1300, 1400, 1400};
     FewPlan p{((M + NT - 1) / NT) * (((int64_t)N + 127) / 128), 0, 0, INT64_MAX};
-    const int sms = current_sms();
-    for (int S = 1; S <= 8 && S <= nkb; ++S) {
-        const int at_once = few_resident<NT>(S);
+    int fit[9];
+    const int most = nkb < 8 ? nkb : 8;
+    few_resident<NT>(fit, most);
+    const int sms = fit[1] / Few<NT>::PER_SM;
+    for (int S = 1; S <= most; ++S) {
+        const int at_once = fit[S];
         if (at_once < 1) continue;
         const int64_t waves = (p.units + at_once - 1) / at_once, resident = p.units < at_once ? p.units : at_once;
         const int64_t meet = S > 1 ? MEET[S] + (NT == 128 ? 600 : 0) : 0;
@@ -491,9 +498,7 @@ template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
 
 template <int NT, typename TO>
 static kda_status launch_few(const CUtensorMap &tw, const CUtensorMap &ta, const float *sa, const float *sw, void *y,
-                             int64_t M, int N, int K, int64_t ldy, unsigned *err, cudaStream_t s) {
-    const int nkb = (K + KB - 1) / KB;
-    const FewPlan p = few_plan<NT>(M, N, nkb);
+                             int64_t M, int N, int nkb, int64_t ldy, const FewPlan &p, unsigned *err, cudaStream_t s) {
     if (p.S < 1 || smem_attr_once<linear_few_kernel<NT, TO, false>>(Few<NT>::SMEM) != cudaSuccess ||
         smem_attr_once<linear_few_kernel<NT, TO, true>>(Few<NT>::SMEM) != cudaSuccess) {
         cudaGetLastError();
@@ -1066,12 +1071,16 @@ static kda_status run_linear(const void *a, const float *sa, const void *w, cons
     // Up to 64 tokens a weight tile is read once and its bytes bound the call: the few-token kernel. With
     // more, whichever is estimated fastest: that kernel, 64 or 128 tokens at a time, or the many-token one.
     int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    const int nkb = (K + KB - 1) / KB;
+    FewPlan p = nt == 16 ? few_plan<16>(M, N, nkb) : nt == 32 ? few_plan<32>(M, N, nkb) : few_plan<64>(M, N, nkb);
     if (M > 64) {
-        const int nkb = (K + KB - 1) / KB;
+        const FewPlan p128 = few_plan<128>(M, N, nkb);
+        if (p128.ns < p.ns) {
+            p = p128;
+            nt = 128;
+        }
         const ManyPlan plan = many_plan<TO>(M, N, nkb);
-        const int64_t ns64 = few_plan<64>(M, N, nkb).ns, ns128 = few_plan<128>(M, N, nkb).ns;
-        if (ns128 < ns64) nt = 128;
-        if (plan.ns < ns64 && plan.ns < ns128) {
+        if (plan.ns < p.ns) {
             CUtensorMap ta, tw;
             if (!byte_map(&ta, a, K, M, lda, 128) || !byte_map(&tw, w, K, N, ldw, 128))
                 return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -1082,10 +1091,10 @@ static kda_status run_linear(const void *a, const float *sa, const void *w, cons
     if (!byte_map(&tw, w, K, N, ldw, 128) || !byte_map(&ta, a, K, M, lda, nt))
         return fail(KDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     switch (nt) {
-    case 16: return launch_few<16, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
-    case 32: return launch_few<32, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
-    case 64: return launch_few<64, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
-    default: return launch_few<128, TO>(tw, ta, sa, sw, y, M, N, K, ldy, err, s);
+    case 16: return launch_few<16, TO>(tw, ta, sa, sw, y, M, N, nkb, ldy, p, err, s);
+    case 32: return launch_few<32, TO>(tw, ta, sa, sw, y, M, N, nkb, ldy, p, err, s);
+    case 64: return launch_few<64, TO>(tw, ta, sa, sw, y, M, N, nkb, ldy, p, err, s);
+    default: return launch_few<128, TO>(tw, ta, sa, sw, y, M, N, nkb, ldy, p, err, s);
     }
 }
 
