@@ -459,9 +459,10 @@ static int64_t with_weights(int64_t ctas, int N, int nkb) {
 }
 
 // CTAs of a cluster (a split of K) for M x N x K and the time that this takes (S = 0: the kernel cannot run
-// here). A call takes FIX and a K block BLOCK, 1.4 times that where two CTAs share an SM; the meeting of the
-// partial sums MEET (NT = 128: 600 more); CTAs that fill the GPU 0.5 to 1.2 us more than a few (the next call's
-// cannot set up beside them); and a further wave of clusters a call's time, of units that a CTA walks 1.6 us.
+// here). A call takes FIX and a K block BLOCK, 1.4 times that where two CTAs of 64 tokens share an SM; the
+// meeting of the partial sums MEET (NT = 128: 600 more); CTAs that fill the GPU 0.6 to 1.2 us more than a few
+// (the next call's cannot set up beside them); and a further wave of clusters a call's time, of units that a CTA
+// walks 1.6 us.
 // (1 x 12288 x 4096, 96 tiles: 10.2 us at S = 3, 11.1 at 1, 14.3 at 4; 64 x 12288 x 4096: 12.9 us at 3, 14.6 at
 // 1, 18.3 at 4; 64 x 4096 x 8192, 32 tiles: 10.7 us at 4, 20.9 at 1.)
 struct FewPlan {
@@ -472,9 +473,9 @@ struct FewPlan {
 template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
     constexpr int64_t FIX = NT == 16 ? 2150 : NT == 32 ? 2630 : NT == 64 ? 3560 : 3940;
     constexpr int64_t BLOCK = NT == 16 ? 194 : NT == 32 ? 208 : NT == 64 ? 263 : 283;
-    constexpr int64_t MEET[2][9] = {{0, 0, 500, 1000, 550, 900, 900, 1000, 1000},
+    constexpr int64_t MEET[2][9] = {{0, 0, 500, 1000, 600, 900, 900, 1000, 1000},
                                     {0, 0, 500, 1000, 500, 1300, 1300, 1400, 1400}};
-    const int64_t crowd = M < 16 ? 400 + 52 * M : 1240;
+    const int64_t crowd = M < 16 ? 550 + 44 * M : 1240;
     FewPlan p{((M + NT - 1) / NT) * (((int64_t)N + 127) / 128), 0, 0, INT64_MAX};
     int fit[9];
     const int most = nkb < 8 ? nkb : 8;
@@ -485,7 +486,7 @@ template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
         if (at_once < 1) continue;
         const int64_t waves = (p.units + at_once - 1) / at_once, resident = p.units < at_once ? p.units : at_once;
         const int64_t meet = S > 1 ? MEET[NT > 32][S] + (NT == 128 ? 600 : 0) : 0;
-        const int64_t block = resident * S > sms ? BLOCK * 14 / 10 : BLOCK;
+        const int64_t block = NT >= 64 && resident * S > sms ? BLOCK * 14 / 10 : BLOCK;
         const int64_t ctas = waves * ((nkb + S - 1) / S) * block + meet + crowd * resident / at_once +
                              (waves - 1) * (S > 1 ? FIX + meet + 1240 : 1600);
         const int64_t t = FIX + with_weights(ctas, N, nkb);
