@@ -96,10 +96,17 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(e));
     return e != 0;
 }
-// fp32 value at the place of `p` in the shared memory of the cluster's CTA `rank`
-__device__ __forceinline__ float peer_load(const float *p, uint32_t rank) {
+// where `yes`, the fp32 value at the place of `p` in the shared memory of the cluster's CTA `rank`, else 0
+__device__ __forceinline__ float peer_load_if(bool yes, const float *p, uint32_t rank) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(p, rank)) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "mov.f32 %0, 0f00000000;\n\t"
+        "@q ld.shared::cluster.f32 %0, [%1];\n\t}"
+        : "=&f"(v)
+        : "r"(peer_addr(p, yes ? rank : 0u)), "r"((uint32_t)yes)
+        : "memory");
     return v;
 }
 // wait for the warp's TMEM loads; the loaded registers pass through it, so that no use moves ahead of it
@@ -109,6 +116,20 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
+}
+
+// Predicated stores: as branches, a run of them took about 56 cycles each (64 x 12288 x 512: 5.0 us, 3.7 now).
+__device__ __forceinline__ void store_raw(bool yes, void *to, uint32_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}"
+                 :: "r"((uint32_t)yes), "l"(to), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store_raw(bool yes, void *to, uint16_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.b16 [%1], %2;\n\t}"
+                 :: "r"((uint32_t)yes), "l"(to), "h"(v) : "memory");
+}
+__device__ __forceinline__ void store_if(bool yes, float *to, float v) { store_raw(yes, to, __float_as_uint(v)); }
+__device__ __forceinline__ void store_if(bool yes, __nv_bfloat16 *to, float v) {
+    store_raw(yes, to, __bfloat16_as_ushort(__float2bfloat16_rn(v)));
 }
 
 // copy of a tile that no other CTA reads: the first to leave L2
@@ -128,7 +149,8 @@ __device__ __forceinline__ void tma_load_once(void *dst, const CUtensorMap *map,
 // with few tokens still feeds whole 128-row tiles from every SM, as S CTAs of a
 // cluster with a run of the K blocks each (SPLIT), or as CTAs that walk several
 // units, so that one's first blocks arrive while the one before is stored (128 x
-// 36864 x 4096: 29.5 us, 33.3 with a CTA per unit). JW warps join the block
+// 36864 x 4096: 27.6 us; 29.5 and, with a CTA per unit, 33.3 before the results'
+// stores were predicated). JW warps join the block
 // sums (a thread holds its feature's sums for TPW tokens; the products of the
 // token scales with the weight block's come from shared memory), the next
 // streams the weight and token tiles through a ring of ST stages, the next issues
@@ -137,8 +159,8 @@ __device__ __forceinline__ void tma_load_once(void *dst, const CUtensorMap *map,
 // shared memory: each CTA adds up its share of the tokens over the S CTAs in
 // their order. Two CTAs fit an SM, of 128 tokens one.
 // Why 128 tokens: the weight tile is read once where 64 would read it twice, and
-// a tile of 256 x 256 would be half empty (100 x 12288 x 8192: 23.8 us, 31.8 at
-// 64, 27.4 in the many-token kernel; 80 x 2912 x 4096: 7.9, 8.5 and 11.8).
+// a tile of 256 x 256 would be half empty (100 x 12288 x 8192: 22.4 us, 28.3 at
+// 64, 27.4 in the many-token kernel; 80 x 2912 x 4096: 7.8, 8.2 and 12.2).
 // A weight tile that one CTA alone reads is marked first to leave L2 (64 x
 // 36864 x 4096: 27.1 us, 28.5 without), where the state, the activations and
 // the next call's tokens stay.
@@ -171,13 +193,13 @@ __device__ __forceinline__ void add_parts(const float *part, int j0, int j1, int
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                v[i][p] = p < S && j0 + G * i < j1 ? peer_load(part + (j0 + G * i) * 128, (uint32_t)p) : 0.f;
+                v[i][p] = peer_load_if(p < S && j0 + G * i < j1, part + (j0 + G * i) * 128, (uint32_t)p);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             float sum = v[i][0];
 #pragma unroll
             for (int p = 1; p < P; ++p) sum += v[i][p];
-            if (j0 + G * i < j1 && live) Elem<TO>::store(y + (int64_t)(j0 + G * i) * ldy, sum);
+            store_if(j0 + G * i < j1 && live, y + (int64_t)(j0 + G * i) * ldy, sum);
         }
     }
 }
@@ -285,10 +307,11 @@ __global__ void __launch_bounds__(Few<NT>::NTHREADS, Few<NT>::PER_SM)
                     }
                 }
             }
-            if (!SPLIT && ok && n0 + f < N) {
+            if (!SPLIT) {
+                const int live = ok && n0 + f < N ? M - m0 - j0w : 0;
+                TO *to = y + (int64_t)(m0 + j0w) * ldy + n0 + f;
 #pragma unroll
-                for (int j = 0; j < F::TPW; ++j)
-                    if (m0 + j0w + j < M) Elem<TO>::store(y + (int64_t)(m0 + j0w + j) * ldy + n0 + f, acc[j]);
+                for (int j = 0; j < F::TPW; ++j, to += ldy) store_if(j < live, to, acc[j]);
             }
             if (SPLIT) break;
         }
@@ -460,21 +483,23 @@ static int64_t with_weights(int64_t ctas, int N, int nkb) {
 
 // CTAs of a cluster (a split of K) for M x N x K and the time that this takes (S = 0: the kernel cannot run
 // here). A call takes FIX and a K block BLOCK, 1.4 times that where two CTAs of 64 tokens share an SM; the
-// meeting of the partial sums MEET (NT = 128: 600 more); CTAs that fill the GPU 0.6 to 1.2 us more than a few
-// (the next call's cannot set up beside them); and a further wave of clusters a call's time, of units that a CTA
-// walks 1.6 us.
-// (1 x 12288 x 4096, 96 tiles: 10.2 us at S = 3, 11.1 at 1, 14.3 at 4; 64 x 12288 x 4096: 12.9 us at 3, 14.6 at
-// 1, 18.3 at 4; 64 x 4096 x 8192, 32 tiles: 10.7 us at 4, 20.9 at 1.)
+// meeting of the partial sums MEET, 0.7 us more on shared SMs; CTAs that fill the GPU 0.6 to 1.2 us more than a
+// few (the next call's cannot set up beside them); and a further wave of clusters a call's time, of units that a
+// CTA walks 0.9 us. (1 x 12288 x 4096, 96 tiles: 10.3 us at S = 3, 11.1 at 1 or 2, 14.6 at 4; 64 x 12288 x
+// 4096: 12.8 us at 2 or 3, 13.3 at 1, 17.7 at 4; 64 x 4096 x 8192, 32 tiles: 10.5 us at 4, 19.6 at 1.)
 struct FewPlan {
     int64_t units;
     int S, at_once;  // clusters that run at once
     int64_t ns;
 };
 template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
-    constexpr int64_t FIX = NT == 16 ? 2150 : NT == 32 ? 2630 : NT == 64 ? 3560 : 3940;
-    constexpr int64_t BLOCK = NT == 16 ? 194 : NT == 32 ? 208 : NT == 64 ? 263 : 283;
-    constexpr int64_t MEET[2][9] = {{0, 0, 500, 1000, 600, 900, 900, 1000, 1000},
-                                    {0, 0, 500, 1000, 500, 1300, 1300, 1400, 1400}};
+    constexpr int C = NT == 16 ? 0 : NT == 32 ? 1 : NT == 64 ? 2 : 3;
+    constexpr int64_t FIX = C == 0 ? 1800 : C == 1 ? 2000 : C == 2 ? 2150 : 2460;
+    constexpr int64_t BLOCK = C == 0 ? 194 : C == 1 ? 208 : C == 2 ? 264 : 281;
+    constexpr int64_t MEET[4][9] = {{0, 0, 1100, 1450, 1100, 1500, 1500, 1800, 1800},
+                                    {0, 0, 1050, 1400, 1050, 1700, 1700, 2000, 2000},
+                                    {0, 0, 1150, 1950, 1300, 2200, 2200, 2300, 2300},
+                                    {0, 0, 2300, 2600, 2600, 2800, 2800, 3200, 3200}};
     const int64_t crowd = M < 16 ? 550 + 44 * M : 1240;
     FewPlan p{((M + NT - 1) / NT) * (((int64_t)N + 127) / 128), 0, 0, INT64_MAX};
     int fit[9];
@@ -485,10 +510,11 @@ template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
         const int at_once = fit[S];
         if (at_once < 1) continue;
         const int64_t waves = (p.units + at_once - 1) / at_once, resident = p.units < at_once ? p.units : at_once;
-        const int64_t meet = S > 1 ? MEET[NT > 32][S] + (NT == 128 ? 600 : 0) : 0;
-        const int64_t block = NT >= 64 && resident * S > sms ? BLOCK * 14 / 10 : BLOCK;
+        const bool shared = resident * S > sms;  // two CTAs on an SM
+        const int64_t meet = MEET[C][S] + (S > 1 && shared ? 700 : 0);
+        const int64_t block = NT >= 64 && shared ? BLOCK * 14 / 10 : BLOCK;
         const int64_t ctas = waves * ((nkb + S - 1) / S) * block + meet + crowd * resident / at_once +
-                             (waves - 1) * (S > 1 ? FIX + meet + 1240 : 1600);
+                             (waves - 1) * (S > 1 ? FIX + meet + 1240 : 900);
         const int64_t t = FIX + with_weights(ctas, N, nkb);
         if (t < p.ns) {
             p.ns = t;
@@ -608,16 +634,6 @@ template <int N> __device__ __forceinline__ void bulk_wait_read_but() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void store_if(bool yes, void *to, uint32_t v) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}"
-                 :: "r"((uint32_t)yes), "l"(to), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ void store_if(bool yes, void *to, uint16_t v) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.b16 [%1], %2;\n\t}"
-                 :: "r"((uint32_t)yes), "l"(to), "h"(v) : "memory");
-}
-
 // A warp stores `rows` rows of `cols` elements from its staged 128-byte rows (16-byte pieces swizzled by the
 // row) to rows of any alignment: 4 bytes a lane, sixteen rows' reads in flight, predicated stores. Where a
 // row of 2-byte elements starts between two words, each lane's word is joined from two neighbours' halves and
@@ -639,14 +655,14 @@ __device__ __forceinline__ void store_rows(TO *to, int64_t ld, const uint8_t *fr
             if (i0 + j >= rows) break;
             TO *row = to + (i0 + j) * ld;
             if constexpr (sizeof(TO) == 4) {
-                store_if(lane < cols, row + lane, w[j]);
+                store_raw(lane < cols, row + lane, w[j]);
             } else {
                 const int odd = (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 1, c = 2 * lane + odd;
                 const uint32_t up = __shfl_down_sync(0xffffffffu, w[j], 1);
                 const uint32_t pair = odd ? __funnelshift_r(w[j], up, 16) : w[j];
-                store_if(c + 1 < cols, row + c, pair);
-                store_if(c + 1 == cols, row + c, (uint16_t)pair);
-                store_if(odd && lane == 0, row, (uint16_t)w[j]);
+                store_raw(c + 1 < cols, row + c, pair);
+                store_raw(c + 1 == cols, row + c, (uint16_t)pair);
+                store_raw(odd && lane == 0, row, (uint16_t)w[j]);
             }
         }
     }
