@@ -637,9 +637,9 @@ template <int N> __device__ __forceinline__ void bulk_wait_read_but() {
 // A warp stores `rows` rows of `cols` elements from its staged 128-byte rows (16-byte pieces swizzled by the
 // row) to rows of any alignment: 4 bytes a lane, sixteen rows' reads in flight, predicated stores. Where a
 // row of 2-byte elements starts between two words, each lane's word is joined from two neighbours' halves and
-// the elements at the ends go by themselves. (3000 x 20001 x 464: bf16 78 us, 131 with an element a lane and
-// a branch, 80 at eight rows, 84 at four; f32 86, 88, 88 and 93. Rows of 20000 elements, which a tensor copy
-// stores: 47 and 61. Rows that start inside a 32-byte sector also write that sector in two parts.)
+// the elements at the ends go by themselves. (3000 x 20001 x 464: bf16 63 us, 78 with a branch a row, 131 with
+// an element a lane; f32 88. Rows of 20000 elements, which a tensor copy stores: 45 and 60. Rows that start inside
+// a 32-byte sector also write that sector in two parts.)
 template <typename TO>
 __device__ __forceinline__ void store_rows(TO *to, int64_t ld, const uint8_t *from, int rows, int cols) {
     constexpr int B = 16;
@@ -652,17 +652,17 @@ __device__ __forceinline__ void store_rows(TO *to, int64_t ld, const uint8_t *fr
                                                        (lane & 3) * 4);
 #pragma unroll
         for (int j = 0; j < B; ++j) {
-            if (i0 + j >= rows) break;
+            const bool live = i0 + j < rows;
             TO *row = to + (i0 + j) * ld;
             if constexpr (sizeof(TO) == 4) {
-                store_raw(lane < cols, row + lane, w[j]);
+                store_raw(live && lane < cols, row + lane, w[j]);
             } else {
                 const int odd = (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 1, c = 2 * lane + odd;
                 const uint32_t up = __shfl_down_sync(0xffffffffu, w[j], 1);
                 const uint32_t pair = odd ? __funnelshift_r(w[j], up, 16) : w[j];
-                store_raw(c + 1 < cols, row + c, pair);
-                store_raw(c + 1 == cols, row + c, (uint16_t)pair);
-                store_raw(odd && lane == 0, row, (uint16_t)w[j]);
+                store_raw(live && c + 1 < cols, row + c, pair);
+                store_raw(live && c + 1 == cols, row + c, (uint16_t)pair);
+                store_raw(live && odd && lane == 0, row, (uint16_t)w[j]);
             }
         }
     }
