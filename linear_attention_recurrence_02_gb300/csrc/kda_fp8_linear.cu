@@ -252,10 +252,9 @@ __global__ void __launch_bounds__(Few<NT>::NTHREADS, Few<NT>::PER_SM)
         tmem_alloc(s_taddr, F::COLS);
         tmem_relinquish();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     sync_tc();
     const uint32_t tbase = *s_taddr, sbase = smem_u32(sm);
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     bool ok = true;
     const int j0w = (warp >> 2) * F::TPW, f = tid & 127;  // a joining thread's first token, its feature
     float acc[F::TPW];
@@ -719,11 +718,11 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
         for (int kb = kb0; kb < kb0 + stages && kb < kb1; ++kb)
             tma_prefetch_l2_2d(&tm_w, kb * KB, (int)(first / mt) * BN + (int)rank * 128);
     }
-    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     static_assert(AS * BN == 512, "the whole TMEM: its first column is 0");
     constexpr uint32_t tbase = 0;
     const uint32_t sbase = smem_u32(sm);
