@@ -484,14 +484,16 @@ static int64_t with_weights(int64_t ctas, int N, int nkb) {
 // here). A call takes FIX and a K block BLOCK, 1.4 times that where two CTAs of 64 tokens share an SM; the
 // meeting of the partial sums MEET, 0.7 us more on shared SMs; CTAs that fill the GPU 0.6 to 1.2 us more than a
 // few (the next call's cannot set up beside them); and a further wave of clusters a call's time, of units that a
-// CTA walks 0.9 us. (1 x 12288 x 4096, 96 tiles: 10.3 us at S = 3, 11.1 at 1 or 2, 14.6 at 4; 64 x 12288 x
-// 4096: 12.8 us at 2 or 3, 13.3 at 1, 17.7 at 4; 64 x 4096 x 8192, 32 tiles: 10.5 us at 4, 19.6 at 1.)
+// CTA walks 1.1 us. With 64 tokens or more, rows that straddle 128-byte lines take half as long again where CTAs
+// walk units (300 x 30000 x 1040: 29 us, 22 in the many-token kernel).
+// (1 x 12288 x 4096, 96 tiles: 10.3 us at S = 3, 11.1 at 1 or 2, 14.6 at 4; 64 x 12288 x 4096: 12.8 us at 2 or 3,
+// 13.3 at 1, 17.7 at 4; 64 x 4096 x 8192, 32 tiles: 10.5 us at 4, 19.6 at 1.)
 struct FewPlan {
     int64_t units;
     int S, at_once;  // clusters that run at once
     int64_t ns;
 };
-template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
+template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb, bool straddle) {
     constexpr int C = NT == 16 ? 0 : NT == 32 ? 1 : NT == 64 ? 2 : 3;
     constexpr int64_t FIX = C == 0 ? 1800 : C == 1 ? 2000 : C == 2 ? 2150 : 2460;
     constexpr int64_t BLOCK = C == 0 ? 194 : C == 1 ? 208 : C == 2 ? 264 : 281;
@@ -511,9 +513,10 @@ template <int NT> static FewPlan few_plan(int64_t M, int N, int nkb) {
         const int64_t waves = (p.units + at_once - 1) / at_once, resident = p.units < at_once ? p.units : at_once;
         const bool shared = resident * S > sms;  // two CTAs on an SM
         const int64_t meet = MEET[C][S] + (S > 1 && shared ? 700 : 0);
-        const int64_t block = NT >= 64 && shared ? BLOCK * 14 / 10 : BLOCK;
+        int64_t block = NT >= 64 && shared ? BLOCK * 14 / 10 : BLOCK;
+        if (NT >= 64 && straddle && waves > 1) block += block / 2;
         const int64_t ctas = waves * ((nkb + S - 1) / S) * block + meet + crowd * resident / at_once +
-                             (waves - 1) * (S > 1 ? FIX + meet + 1240 : 900);
+                             (waves - 1) * (S > 1 ? FIX + meet + 1240 : 1100);
         const int64_t t = FIX + with_weights(ctas, N, nkb);
         if (t < p.ns) {
             p.ns = t;
@@ -1076,7 +1079,8 @@ static kda_status launch_many(const CUtensorMap &ta, const CUtensorMap &tw, cons
     auto go = [&](auto kern, int64_t tile0, int64_t tiles, int64_t most, int S) {
         many_config(cfg, at, (unsigned)(tiles - tile0 < most ? tiles - tile0 : most), S, s);
         cudaLaunchKernelEx(&cfg, kern, ta, tw, ty, sa, sw, static_cast<TO *>(y), (int)M, N, nkb, ldy, mt,
-                           (unsigned)tile0, (unsigned)tiles, by_tma, S, many_stages(tiles - tile0 > most, nkb), err);  // an error is left for check_launch
+                           (unsigned)tile0, (unsigned)tiles, by_tma, S, many_stages(tiles - tile0 > most, nkb),
+                           err);  // an error is left for check_launch
     };
     if (p.whole > 0) go(linear_many_kernel<TO, false>, 0, p.whole, resident_clusters<TO, false>(1), 1);
     if (p.whole < p.tiles) go(linear_many_kernel<TO, true>, p.whole, p.tiles, p.tiles - p.whole, p.S);
@@ -1090,9 +1094,12 @@ static kda_status run_linear(const void *a, const float *sa, const void *w, cons
     // more, whichever is estimated fastest: that kernel, 64 or 128 tokens at a time, or the many-token one.
     int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     const int nkb = (K + KB - 1) / KB;
-    FewPlan p = nt == 16 ? few_plan<16>(M, N, nkb) : nt == 32 ? few_plan<32>(M, N, nkb) : few_plan<64>(M, N, nkb);
+    const bool straddle = lda % 128 != 0 || ldw % 128 != 0;
+    FewPlan p = nt == 16   ? few_plan<16>(M, N, nkb, straddle)
+                : nt == 32 ? few_plan<32>(M, N, nkb, straddle)
+                           : few_plan<64>(M, N, nkb, straddle);
     if (M > 64) {
-        const FewPlan p128 = few_plan<128>(M, N, nkb);
+        const FewPlan p128 = few_plan<128>(M, N, nkb, straddle);
         if (p128.ns < p.ns) {
             p = p128;
             nt = 128;
