@@ -170,6 +170,25 @@ def _stream(stream, device):
     return stream.cuda_stream
 
 
+def _on_stream(stream):
+    """Context in which `stream` is current (nothing changes for None). Device memory that a call needs for
+    itself is allocated in it: the caching allocator gives a block back to the stream that it was allocated
+    on, in that stream's order. Allocated on another stream, the block could be handed out there again while
+    the call's kernels still use it, or still be in use by work queued there before."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _scratch(workspace, need, device, stream):
+    """The caller's workspace and its size, or `need` bytes allocated for a call on `stream` when None."""
+    if workspace is None and need > 0:
+        import torch
+        with _on_stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
 def state_bytes(layers, heads, dk, dv) -> int:
     return int(lib().kda_state_bytes(layers, heads, dk, dv))
 
@@ -401,14 +420,6 @@ def _current(device):
     return torch.cuda.device(device)
 
 
-def _proj_workspace(workspace, need, device):
-    """The caller's workspace and its size, or one allocated here when None."""
-    import torch
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return workspace, workspace.numel() * workspace.element_size()
-
-
 def kda_shortconv_decode_step_proj(x, ring, w, g, beta, state, out_gate, norm_weight, proj, proj_scales, y,
                                    gate="channel", act="sigmoid", l2_eps=1e-6, norm_eps=1e-6, overlap_prev=False,
                                    workspace=None, stream=None):
@@ -424,7 +435,7 @@ def kda_shortconv_decode_step_proj(x, ring, w, g, beta, state, out_gate, norm_we
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, B, H, D, x)
-    workspace, size = _proj_workspace(workspace, kda_shortconv_decode_step_proj_workspace_bytes(B, H, D), x.device)
+    workspace, size = _scratch(workspace, kda_shortconv_decode_step_proj_workspace_bytes(B, H, D), x.device, stream)
     flags = KDA_DECODE_OVERLAP_PREV if overlap_prev else 0
     with _current(x.device):
         _check(lib().kda_shortconv_decode_step_proj(
@@ -455,8 +466,8 @@ def kda_chunk_prefill_proj(q, k, v, g, beta, out_gate, norm_weight, proj, proj_s
         if st is not None and st.numel() != N * H * D * D:
             raise ValueError("state shape mismatch")
     Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, T, H, D, q)
-    workspace, size = _proj_workspace(workspace, kda_chunk_prefill_proj_workspace_bytes(T, N, H, D, chunk_size),
-                                      q.device)
+    workspace, size = _scratch(workspace, kda_chunk_prefill_proj_workspace_bytes(T, N, H, D, chunk_size), q.device,
+                               stream)
     with _current(q.device):
         _check(lib().kda_chunk_prefill_proj(
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens),
@@ -482,11 +493,7 @@ def kda_chunk_prefill_epi(q, k, v, g, beta, out, out_gate, norm_weight, gate="ch
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    ws_bytes = kda_chunk_prefill_workspace_bytes(T, N, H, D, chunk_size)
-    if workspace is None and ws_bytes > 0:
-        import torch
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wsz = _scratch(workspace, kda_chunk_prefill_workspace_bytes(T, N, H, D, chunk_size), q.device, stream)
     _check(lib().kda_chunk_prefill_epi(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
                                        _ptr(final_state), _ptr(out), _ptr(cu_seqlens), N, T, H, D, chunk_size,
                                        _dtype_code(q), code, float(l2_eps), _ptr(out_gate), _ptr(norm_weight),
@@ -505,14 +512,11 @@ def kda_chunk_prefill_scan(q, k, v, g, beta, out, segments, initial_state=None, 
     (allocated here when None)."""
     T, H, D = q.shape
     code = _check_gate(g, gate, (T,), H, D)
-    need = kda_chunk_prefill_scan_workspace_bytes(T, H, D, chunk_size, segments)
-    if workspace is None and need > 0:
-        import torch
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace, wsz = _scratch(workspace, kda_chunk_prefill_scan_workspace_bytes(T, H, D, chunk_size, segments), q.device,
+                              stream)
     _check(lib().kda_chunk_prefill_scan(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
                                         _ptr(final_state), _ptr(out), T, H, D, chunk_size, _dtype_code(q), code,
-                                        float(l2_eps), int(segments), _ptr(workspace),
-                                        0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                        float(l2_eps), int(segments), _ptr(workspace), wsz,
                                         _stream(stream, q.device)))
 
 
@@ -538,11 +542,7 @@ def kda_chunk_prefill(q, k, v, g, beta, out, initial_state=None, final_state=Non
     cu_seqlens int64 [N+1] on the device (or None for one sequence)."""
     T, H, D = q.shape
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    ws_bytes = kda_chunk_prefill_workspace_bytes(T, N, H, D, chunk_size)
-    if workspace is None and ws_bytes > 0:
-        import torch
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wsz = _scratch(workspace, kda_chunk_prefill_workspace_bytes(T, N, H, D, chunk_size), q.device, stream)
     _check(lib().kda_chunk_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
                                    _ptr(final_state), _ptr(out), _ptr(cu_seqlens), N, T, H, D, chunk_size,
                                    _dtype_code(q), float(l2_eps), _ptr(workspace), wsz,
@@ -555,11 +555,7 @@ def kda_chunk_prefill_gated(q, k, v, g, beta, out, gate="channel", initial_state
     T, H, D = q.shape
     code = _check_gate(g, gate, (T,), H, D)
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    ws_bytes = kda_chunk_prefill_workspace_bytes(T, N, H, D, chunk_size)
-    if workspace is None and ws_bytes > 0:
-        import torch
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wsz = _scratch(workspace, kda_chunk_prefill_workspace_bytes(T, N, H, D, chunk_size), q.device, stream)
     _check(lib().kda_chunk_prefill_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
                                          _ptr(final_state), _ptr(out), _ptr(cu_seqlens), N, T, H, D, chunk_size,
                                          _dtype_code(q), code, float(l2_eps), _ptr(workspace), wsz,
@@ -594,13 +590,13 @@ def kda_chunk_prefill_split(q, k, v, g, beta, out, cu_seqlens, gate="channel", i
     T, H, D = q.shape
     code = _check_gate(g, gate, (T,), H, D)
     host = _host_cu(cu_seqlens)
-    dev_cu = cu_seqlens if (hasattr(cu_seqlens, "is_cuda") and cu_seqlens.is_cuda) else \
-        torch.from_numpy(host).to(q.device)
+    dev_cu = cu_seqlens
+    if not (hasattr(cu_seqlens, "is_cuda") and cu_seqlens.is_cuda):
+        with _on_stream(stream):
+            dev_cu = torch.from_numpy(host).to(q.device)
     N = host.shape[0] - 1
     need = int(lib().kda_chunk_prefill_split_workspace_bytes(host.ctypes.data, N, H, D, chunk_size))
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wsz = _scratch(workspace, need, q.device, stream)
     _check(lib().kda_chunk_prefill_split(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
                                          _ptr(final_state), _ptr(out), _ptr(dev_cu), host.ctypes.data, N, T, H, D,
                                          chunk_size, _dtype_code(q), code, float(l2_eps), _ptr(workspace), wsz,

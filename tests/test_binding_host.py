@@ -1,0 +1,146 @@
+"""Host-side checks of the Python binding that need no GPU: what it allocates, on which stream, and what it
+refuses, with stand-ins for device tensors, streams and the library."""
+import contextlib
+
+import numpy as np
+import pytest
+
+from tests._util import ensure_built
+
+torch = pytest.importorskip("torch")
+F8, BF, F32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
+
+
+class _Dev:
+    """A device tensor's attributes without the device."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=F32, device="cuda:0"):
+        self.shape, self.dtype, self.device = shape, dtype, torch.device(device)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def get_device(self):
+        return self.device.index
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+
+class _Stream:
+    cuda_stream, device = 77, torch.device("cuda:0")
+
+
+class _Library:
+    """Answers the workspace questions from the real library and takes every call as successful."""
+
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_bytes"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def env(monkeypatch):
+    """The binding over _Library; `env.made` lists (bytes, stream that was current) of each allocation."""
+    ensure_built()
+    from linear_attention_recurrence_02_gb300 import kda
+    fake, state = _Library(kda.lib()), {"current": None}
+    made = []
+
+    @contextlib.contextmanager
+    def stream_context(s):
+        before, state["current"] = state["current"], s if s is not None else state["current"]
+        yield
+        state["current"] = before
+
+    def empty(n, dtype=None, device=None):
+        made.append((n, state["current"]))
+        return _Dev(n, dtype=torch.uint8)
+
+    class Host:  # what torch.from_numpy gives: its copy to the device is an allocation as well
+        def to(self, device):
+            return empty(4, device=device)
+
+    monkeypatch.setattr(kda, "lib", lambda: fake)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "from_numpy", lambda a: Host())
+    monkeypatch.setattr(torch.cuda, "stream", stream_context)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: type("Default", (), {"cuda_stream": 0})())
+    fake.made, fake.kda = made, kda
+    return fake
+
+
+def _decode(kda, B=4, H=2, D=64, hidden=256, dt=BF, **k):
+    a = dict(x=_Dev(B, 3, H, D, dtype=dt), ring=_Dev(B, 3, H, 3, D, dtype=dt), w=_Dev(3, H, D, 4), g=_Dev(B, H, D),
+             beta=_Dev(B, H), state=_Dev(B, H, D, D), out_gate=_Dev(B, H, D, dtype=dt), norm_weight=_Dev(D),
+             proj=_Dev(hidden, H * D, dtype=F8), proj_scales=_Dev(2, 1), y=_Dev(B, hidden, dtype=dt))
+    a.update(k)
+    kda.kda_shortconv_decode_step_proj(**a)
+
+
+def _prefill(kda, T=100, H=2, D=64, hidden=256, dt=BF, **k):
+    a = dict(q=_Dev(T, H, D, dtype=dt), k=_Dev(T, H, D, dtype=dt), v=_Dev(T, H, D, dtype=dt), g=_Dev(T, H, D),
+             beta=_Dev(T, H), out_gate=_Dev(T, H, D, dtype=dt), norm_weight=_Dev(D),
+             proj=_Dev(hidden, H * D, dtype=F8), proj_scales=_Dev(2, 1), y=_Dev(T, hidden, dtype=dt))
+    a.update(k)
+    kda.kda_chunk_prefill_proj(**a)
+
+
+def _old_prefill(name, T=40000, H=2, D=128, **k):
+    def call(kda, **extra):
+        a = dict(q=_Dev(T, H, D, dtype=BF), k=_Dev(T, H, D, dtype=BF), v=_Dev(T, H, D, dtype=BF), g=_Dev(T, H, D),
+                 beta=_Dev(T, H), out=_Dev(T, H, D, dtype=BF))
+        a.update(k)
+        a.update(extra)
+        getattr(kda, name)(**a)
+    return call
+
+
+_ALLOCATING = {
+    "decode_proj": (_decode, 1),
+    "prefill_proj": (_prefill, 1),
+    "prefill": (_old_prefill("kda_chunk_prefill", cu_seqlens=_Dev(4, dtype=torch.int64)), 1),
+    "prefill_gated": (_old_prefill("kda_chunk_prefill_gated", cu_seqlens=_Dev(4, dtype=torch.int64)), 1),
+    "prefill_epi": (_old_prefill("kda_chunk_prefill_epi", out_gate=_Dev(40000, 2, 128, dtype=BF),
+                                 norm_weight=_Dev(128), cu_seqlens=_Dev(4, dtype=torch.int64)), 1),
+    "prefill_scan": (_old_prefill("kda_chunk_prefill_scan", segments=4), 1),
+    "prefill_split": (_old_prefill("kda_chunk_prefill_split", cu_seqlens=np.array([0, 39000, 40000])), 2),
+}
+
+
+@pytest.mark.parametrize("which", sorted(_ALLOCATING))
+def test_own_memory_belongs_to_the_calls_stream(env, which):
+    """Memory that a binding allocates for a call on a given stream is allocated with that stream current: the
+    caching allocator then hands it out again only in that stream's order. Without a stream it is the current
+    one's."""
+    call, allocations = _ALLOCATING[which]
+    s = _Stream()
+    call(env.kda, stream=s)
+    assert [cur for _, cur in env.made] == [s] * allocations and all(n > 0 for n, _ in env.made)
+    assert env.calls and env.calls[-1][1][-1] == s.cuda_stream
+    env.made.clear()
+    call(env.kda)
+    assert [cur for _, cur in env.made] == [None] * allocations
+    assert env.calls[-1][1][-1] == 0
+
+
+def test_a_given_workspace_is_used_as_it_is(env):
+    need = env.real.kda_shortconv_decode_step_proj_workspace_bytes(4, 2, 64)
+    _decode(env.kda, workspace=_Dev(need, dtype=torch.uint8), stream=_Stream())
+    assert env.made == [] and env.calls[-1][1][-2] == need
