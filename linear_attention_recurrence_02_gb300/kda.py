@@ -392,6 +392,20 @@ def kda_fp8_linear(a, a_scales, w, w_scales, y, stream=None):
         _settle(status, fn, a.device, a, a_scales, w, w_scales, y, stream)
 
 
+def _check_kinds(like, floats, ints, x, workspace):
+    """Types and devices of a one-call way out's tensors (None: absent): the library sees pointers alone, and would
+    read and write past the end of a tensor of a narrower type. `like` have x's type, `floats` float32, `ints` int64."""
+    import torch
+    for group, dtype, what in ((like, x.dtype, "must have the inputs' dtype"),
+                               (floats, torch.float32, "must be float32"), (ints, torch.int64, "must be int64")):
+        for name, t in group.items():
+            if t is not None and t.dtype != dtype:
+                raise TypeError(f"{name} {what}")
+    for t in (*like.values(), *floats.values(), *ints.values(), workspace):
+        if t is not None and t.device != x.device:
+            raise ValueError("tensors must be on one CUDA device")
+
+
 def _check_proj(out_gate, norm_weight, proj, proj_scales, y, lead, H, D, x):
     """Shapes, types and devices of the output projection's arguments; returns Nout."""
     import torch
@@ -435,6 +449,8 @@ def kda_shortconv_decode_step_proj(x, ring, w, g, beta, state, out_gate, norm_we
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, B, H, D, x)
+    _check_kinds({"ring": ring}, {"w": w, "g": None if code == KDA_GATE_NONE else g, "beta": beta, "state": state},
+                 {}, x, workspace)
     workspace, size = _scratch(workspace, kda_shortconv_decode_step_proj_workspace_bytes(B, H, D), x.device, stream)
     flags = KDA_DECODE_OVERLAP_PREV if overlap_prev else 0
     with _current(x.device):
@@ -466,6 +482,9 @@ def kda_chunk_prefill_proj(q, k, v, g, beta, out_gate, norm_weight, proj, proj_s
         if st is not None and st.numel() != N * H * D * D:
             raise ValueError("state shape mismatch")
     Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, T, H, D, q)
+    _check_kinds({"k": k, "v": v}, {"g": None if code == KDA_GATE_NONE else g, "beta": beta,
+                                    "initial_state": initial_state, "final_state": final_state},
+                 {"cu_seqlens": cu_seqlens}, q, workspace)
     workspace, size = _scratch(workspace, kda_chunk_prefill_proj_workspace_bytes(T, N, H, D, chunk_size), q.device,
                                stream)
     with _current(q.device):

@@ -144,3 +144,54 @@ def test_a_given_workspace_is_used_as_it_is(env):
     need = env.real.kda_shortconv_decode_step_proj_workspace_bytes(4, 2, 64)
     _decode(env.kda, workspace=_Dev(need, dtype=torch.uint8), stream=_Stream())
     assert env.made == [] and env.calls[-1][1][-2] == need
+
+
+@pytest.mark.parametrize("bad,error", [
+    (dict(ring=_Dev(4, 3, 2, 3, 64)), TypeError),
+    (dict(w=_Dev(3, 2, 64, 4, dtype=BF)), TypeError),
+    (dict(g=_Dev(4, 2, 64, dtype=BF)), TypeError),
+    (dict(beta=_Dev(4, 2, dtype=torch.float64)), TypeError),
+    (dict(state=_Dev(4, 2, 64, 64, dtype=BF)), TypeError),
+    (dict(out_gate=_Dev(4, 2, 64)), TypeError),
+    (dict(x=_Dev(4, 3, 2, 64, dtype=torch.float16)), TypeError),
+    (dict(state=_Dev(4, 2, 64, 64, device="cuda:1")), ValueError),
+    (dict(ring=_Dev(4, 3, 2, 3, 64, dtype=BF, device="cuda:1")), ValueError),
+    (dict(beta=_Dev(4, 2, device="cuda:1")), ValueError),
+    (dict(workspace=_Dev(1 << 20, dtype=torch.uint8, device="cuda:1")), ValueError),
+])
+def test_decode_proj_refuses_types_and_devices(env, bad, error):
+    """Nothing reaches the library, which could not tell the types apart."""
+    with pytest.raises(error):
+        _decode(env.kda, **bad)
+    assert env.calls == [] and env.made == []
+
+
+@pytest.mark.parametrize("bad,error", [
+    (dict(k=_Dev(100, 2, 64)), TypeError),
+    (dict(v=_Dev(100, 2, 64, dtype=torch.float16)), TypeError),
+    (dict(g=_Dev(100, 2, 64, dtype=BF)), TypeError),
+    (dict(beta=_Dev(100, 2, dtype=BF)), TypeError),
+    (dict(initial_state=_Dev(1, 2, 64, 64, dtype=BF)), TypeError),
+    (dict(final_state=_Dev(1, 2, 64, 64, dtype=BF)), TypeError),
+    (dict(cu_seqlens=_Dev(2, dtype=torch.int32)), TypeError),
+    (dict(v=_Dev(100, 2, 64, dtype=BF, device="cuda:1")), ValueError),
+    (dict(final_state=_Dev(1, 2, 64, 64, device="cuda:1")), ValueError),
+    (dict(cu_seqlens=_Dev(2, dtype=torch.int64, device="cuda:1")), ValueError),
+    (dict(workspace=_Dev(1 << 24, dtype=torch.uint8, device="cuda:1")), ValueError),
+])
+def test_prefill_proj_refuses_types_and_devices(env, bad, error):
+    with pytest.raises(error):
+        _prefill(env.kda, **bad)
+    assert env.calls == [] and env.made == []
+
+
+def test_one_call_ways_out_take_what_they_document(env):
+    """Optional tensors absent and present, every gate form, fp32 and bf16."""
+    for dt in (BF, F32):
+        _decode(env.kda, dt=dt)
+        _decode(env.kda, dt=dt, g=_Dev(4, 2), gate="head")
+        _decode(env.kda, dt=dt, g=None, gate="none")
+        _prefill(env.kda, dt=dt)
+        _prefill(env.kda, dt=dt, g=None, gate="none", initial_state=_Dev(1, 2, 64, 64), final_state=_Dev(1, 2, 64, 64),
+                 cu_seqlens=_Dev(2, dtype=torch.int64))
+    assert len(env.calls) == 10
