@@ -851,6 +851,9 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                         }
                     } else {
                         store_rows(y + mw * ldy + n, ldy, piece, M - mw < 32 ? M - mw : 32, N - n < JR ? N - n : JR);
+                        // an empty group: the wait above counts a group for every piece, and would take this one's
+                        // predecessor, whose copy may still read the next piece, for the latest
+                        if (lane == 0) bulk_commit();
                     }
                 }
             }

@@ -1,0 +1,60 @@
+"""GPU tests of kda_fp8_linear where its parts meet: results that leave through two alternating pieces of shared
+memory. Bounds as counted in tests/_fp8.py, evaluated in fp64 on the GPU."""
+import pytest
+
+from tests import _fp8
+from tests._util import cuda_or_skip, ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    torch = cuda_or_skip()
+    ensure_built()
+    from linear_attention_recurrence_02_gb300 import kda
+    return torch, kda
+
+
+def _case(torch, seed, M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    a = (torch.randn((M, K), generator=g, device="cuda") * 120).clamp(-448, 448).to(torch.float8_e4m3fn)
+    w = (torch.randn((N, K), generator=g, device="cuda") * 110).clamp(-448, 448).to(torch.float8_e4m3fn)
+    kb = _fp8.nblocks(K)
+    sa = torch.exp(torch.randn((kb, M), generator=g, device="cuda")) / 100
+    sw = torch.exp(torch.randn((_fp8.nblocks(N), kb), generator=g, device="cuda")) / 100
+    return a, sa, w, sw
+
+
+def _bound(torch, a, sa, w, sw):
+    """The product and the bound of tests/_fp8.py's check_linear without its bf16 term, in fp64."""
+    K, N = a.shape[1], w.shape[0]
+    y = mag = 0.0
+    rows = torch.arange(N, device="cuda") // _fp8.BLOCK
+    for b in range(_fp8.nblocks(K)):
+        c = slice(b * _fp8.BLOCK, (b + 1) * _fp8.BLOCK)
+        ab, wb = a[:, c].double(), w[:, c].double()
+        s = sa[b].double()[:, None] * sw[rows, b].double()[None, :]
+        y, mag = y + (ab @ wb.t()) * s, mag + (ab.abs() @ wb.abs().t()) * s
+    return y, mag * (2 * 128 + 2 + _fp8.nblocks(K)) * _fp8.U + 1e-37
+
+
+@pytest.mark.parametrize("M,N,K", [(19_800, 2603, 16), (19_800, 2635, 16), (19_800, 2635, 144), (20_011, 331, 128)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_ragged_columns_of_many_token_tiles(env, M, N, K, out):
+    """More token tiles than CTA pairs, so that a pair stores two tiles of the last columns one after the other, of
+    which the last piece goes by ordinary stores between tensor copies: every element, several times."""
+    torch, kda = env
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[out]
+    a, sa, w, sw = _case(torch, N + K, M, N, K)
+    ref, tol = _bound(torch, a, sa, w, sw)
+    if out == "bf16":
+        tol = tol + ref.abs() * 2.0 ** -8
+    ld = (N + 7) // 8 * 8
+    big = torch.empty((M, ld), dtype=dt, device="cuda")
+    for k in range(6):
+        big.fill_(-9.0 - k)
+        kda.kda_fp8_linear(a, sa, w, sw, big[:, :N])
+        assert bool(((big[:, :N].double() - ref).abs() <= tol).all())
+        assert bool((big[:, N:] == -9.0 - k).all())
+    kda.kda_sync_status()
