@@ -62,6 +62,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();  // .aligned wants the warp's lanes together; some callers come from a lane's own branch
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // address in the cluster's shared window of this CTA's `p` in CTA `rank`
@@ -957,7 +958,6 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
             }
         }
         if (SPLIT) {  // the joining warps' two meetings
-            __syncwarp();
             cluster_sync();
             cluster_sync();
         }

@@ -39,7 +39,7 @@ def _bound(torch, a, sa, w, sw):
     return y, mag * (2 * 128 + 2 + _fp8.nblocks(K)) * _fp8.U + 1e-37
 
 
-@pytest.mark.parametrize("M,N,K", [(19_800, 2603, 16), (19_800, 2635, 16), (19_800, 2635, 144), (20_011, 331, 128)])
+@pytest.mark.parametrize("M,N,K", [(19_800, 2603, 16), (19_800, 2635, 16), (19_800, 2635, 144), (20_011, 587, 528)])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_linear_ragged_columns_of_many_token_tiles(env, M, N, K, out):
     """More token tiles than CTA pairs, so that a pair stores two tiles of the last columns one after the other, of
@@ -57,4 +57,19 @@ def test_linear_ragged_columns_of_many_token_tiles(env, M, N, K, out):
         kda.kda_fp8_linear(a, sa, w, sw, big[:, :N])
         assert bool(((big[:, :N].double() - ref).abs() <= tol).all())
         assert bool((big[:, N:] == -9.0 - k).all())
+    kda.kda_sync_status()
+
+
+def test_linear_shared_tiles_back_to_back(env):
+    """Tiles shared by two and four CTA pairs, forty calls without a wait in between: the same bits each time."""
+    torch, kda = env
+    for M, N, K in ((500, 4000, 4112), (250, 3800, 12304)):
+        a, sa, w, sw = _case(torch, M, M, N, K)
+        outs = [torch.full((M, N), float("nan"), device="cuda") for _ in range(40)]
+        for y in outs:
+            kda.kda_fp8_linear(a, sa, w, sw, y)
+        ref, tol = _bound(torch, a, sa, w, sw)
+        assert bool(((outs[0].double() - ref).abs() <= tol).all())
+        for y in outs[1:]:
+            assert torch.equal(y, outs[0])
     kda.kda_sync_status()
