@@ -786,7 +786,12 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
             if constexpr (SPLIT) {
                 // The pairs' sums meet: each group of 64 features belongs to one pair of the cluster; the
                 // others send it theirs, [group][pair][feature / 4][token] in the ring's place, and it adds them
-                // to its own in the pairs' order. (One tile per cluster: the rings are free from here on.)
+                // to its own in the pairs' order. (One tile per cluster: the rings are free from here on.) Sums of
+                // a thread whose waits gave up are sent as NaN, not for the others' to pass as results.
+                if (!ok) {
+#pragma unroll
+                    for (int j = 0; j < JC / 2; ++j) acc[j] = 0x7fffffff7fffffffull;
+                }
                 cluster_sync();
                 const int per = 4 / S, row = 32 * (warp & 3) + lane;  // groups of a pair
                 auto val = [&](int j) { return __uint_as_float((uint32_t)(acc[j >> 1] >> (32 * (j & 1)))); };
