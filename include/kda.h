@@ -305,8 +305,9 @@ kda_status kda_gated_rmsnorm_fp8(const void *o, const void *gate, const float *w
  *     N and ldy keep their values. y may not alias another argument. With many
  *     tokens, rows a multiple of 16 bytes apart are written fastest.
  * e4m3 products are exact and are summed in fp32; the sums of the K blocks are
- * scaled and joined in fp32, in an order that depends on the sizes alone: the
- * same inputs give the same bits.
+ * scaled and joined in fp32, in an order that depends on M, N, K and the GPU
+ * alone: the same inputs give the same bits, whatever the strides, and the same
+ * sums before their rounding to out_dtype.
  * Requires M >= 0 (0 is a no-op), N >= 1, K a positive multiple of 16, lda and
  * ldw multiples of 16 that are >= K, ldy >= N. a and w are read by TMA
  * tensor copies (KDA_ERR_CUDA if the driver's tensor-map encoder rejects

@@ -1102,7 +1102,9 @@ static kda_status run_linear(const void *a, const float *sa, const void *w, cons
     // more, whichever is estimated fastest: that kernel, 64 or 128 tokens at a time, or the many-token one.
     int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     const int nkb = (K + KB - 1) / KB;
-    const bool straddle = lda % 128 != 0 || ldw % 128 != 0;
+    // Rows of contiguous operands straddle 128-byte lines by K. The strides themselves stay out of the choice: it
+    // sets the order of the sums, and a matrix has the same bits whole and as a slice of wider rows.
+    const bool straddle = K % 128 != 0;
     FewPlan p = nt == 16   ? few_plan<16>(M, N, nkb, straddle)
                 : nt == 32 ? few_plan<32>(M, N, nkb, straddle)
                            : few_plan<64>(M, N, nkb, straddle);

@@ -73,3 +73,23 @@ def test_linear_shared_tiles_back_to_back(env):
         for y in outs[1:]:
             assert torch.equal(y, outs[0])
     kda.kda_sync_status()
+
+
+@pytest.mark.parametrize("M,N,K,ld", [(48, 39_680, 6912, 6928), (96, 21_760, 6656, 6672), (128, 19_968, 5376, 5392),
+                                      (128, 19_968, 5360, 5376), (300, 30_000, 1024, 1040), (33, 700, 400, 512),
+                                      (500, 4000, 4096, 4112)])
+def test_linear_bits_do_not_depend_on_strides(env, M, N, K, ld):
+    """Contiguous operands and slices of wider rows, results whole and as a slice, in fp32 and rounded to bf16."""
+    torch, kda = env
+    a, sa, w, sw = _case(torch, M + K, M, N, K)
+    wide = [torch.zeros((t.shape[0], ld), dtype=torch.uint8, device="cuda").view(t.dtype) for t in (a, w)]
+    for t, b in zip((a, w), wide):
+        b.view(torch.uint8)[:, :K] = t.view(torch.uint8)
+    want = torch.empty((M, N), device="cuda")
+    kda.kda_fp8_linear(a, sa, w, sw, want)
+    for x, z in ((wide[0], w), (a, wide[1]), wide):
+        for dt in (torch.float32, torch.bfloat16):
+            for ldy in (N, N + 5):
+                y = torch.empty((M, ldy), dtype=dt, device="cuda")[:, :N]
+                kda.kda_fp8_linear(x[:, :K], sa, z[:, :K], sw, y)
+                assert torch.equal(y, want.to(dt))
