@@ -11,9 +11,11 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import shlex
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -34,23 +36,53 @@ def _nvcc():
     raise RuntimeError("nvcc not found")
 
 
-def _deps():
-    return sorted(glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + [os.path.join(INCLUDE, "kda.h")])
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, [*glob.glob(os.path.join(CSRC, "*.cu")), *glob.glob(os.path.join(CSRC, "*.cuh")),
+                        os.path.join(INCLUDE, "kda.h")])
+
+
+def _fastcall_up_to_date() -> bool:
+    return _newer(FASTCALL, glob.glob(os.path.join(CSRC, "*.c")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(FASTCALL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(FASTCALL))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _library_up_to_date() and _fastcall_up_to_date()
+
+
+def _compile_fastcall():
+    cc = shlex.split(os.environ.get("CC", "")) or [c for c in (shutil.which("gcc"), shutil.which("cc")) if c][:1]
+    if not cc:
+        raise RuntimeError("no C compiler found")
+    src, out = os.path.join(CSRC, "kda_fastcall.c"), FASTCALL + f".tmp{os.getpid()}"
+    r = subprocess.run([*cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+                        src, "-o", out], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(out, FASTCALL)
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile every csrc/*.cu for sm_103a and link libkda.so; returns its path."""
-    if not force and up_to_date():
-        return LIB
+    """Compile every csrc/*.cu for sm_103a and link libkda.so; returns its path. The Python extension is
+    built beside it; the library does without, so where that fails there is a warning."""
     os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        host = ex.submit(_compile_fastcall) if force or not _fastcall_up_to_date() else None
+        if force or not _library_up_to_date():
+            _compile_library(ex, verbose)
+        if host is not None:
+            try:
+                host.result()
+            except (RuntimeError, OSError) as e:
+                warnings.warn(f"{os.path.basename(FASTCALL)} was not built (it needs a C compiler and Python.h); "
+                              f"the Python binding of the 8-bit operators will not work: {e}")
+    return LIB
+
+
+def _compile_library(ex, verbose):
     nvcc = _nvcc()
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -64,21 +96,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
             f.write(r.stderr)
         return obj
 
-    def compile_fastcall():
-        cc = next((c for c in (os.environ.get("CC"), shutil.which("gcc"), shutil.which("cc")) if c), None)
-        if cc is None:
-            raise RuntimeError("no C compiler found")
-        src, out = os.path.join(CSRC, "kda_fastcall.c"), FASTCALL + f".tmp{os.getpid()}"
-        r = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
-                            src, "-o", out], capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{cc} failed for {src}:\n{r.stdout}\n{r.stderr}")
-        os.replace(out, FASTCALL)
-
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        host = ex.submit(compile_fastcall)
-        objs = list(ex.map(compile_one, srcs))
-        host.result()
+    objs = list(ex.map(compile_one, srcs))
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
@@ -87,7 +105,6 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         for o in objs:
             print(open(o + ".ptxas.txt").read())
-    return LIB
 
 
 if __name__ == "__main__":

@@ -331,7 +331,7 @@ def _fastcall():
         import torch
         path = _build.FASTCALL
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it first "
+            raise RuntimeError(f"{path} is missing: build it first, with a C compiler and Python.h "
                                "(python -c 'import __graft_entry__ as g; g.build()')")
         spec = importlib.util.spec_from_loader(
             "kda_fastcall", importlib.machinery.ExtensionFileLoader("kda_fastcall", path))
