@@ -3,7 +3,7 @@
 Each ``csrc/*.cu`` is compiled in parallel to an object file, then linked
 into ``_build/libkda.so`` (CUDA runtime linked statically, no other
 dependencies). ``csrc/kda_fastcall.c``, the host side of the 8-bit operators'
-binding, is compiled by the C compiler into ``_build/kda_fastcall.so``, a
+binding, is compiled by the C compiler into ``_build/kda_fastcall.<abi>.so``, a
 CPython extension. Nothing is installed outside the source tree.
 """
 from __future__ import annotations
@@ -23,7 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkda.so")
-FASTCALL = os.path.join(BUILD, "kda_fastcall.so")
+# the suffix names the interpreter's version and the machine: another Python builds its own
+FASTCALL = os.path.join(BUILD, "kda_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fPIC", "-Xptxas", "-v"] + ARCH

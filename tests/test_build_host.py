@@ -64,3 +64,10 @@ def test_the_c_compiler_may_come_with_arguments(compilers, monkeypatch):
     monkeypatch.setenv("CC", "ccache gcc -pthread")
     build.build_library()
     assert [c[:3] for c in compilers.commands if c[0] != "/nvcc"] == [["ccache", "gcc", "-pthread"]]
+
+
+def test_the_extension_belongs_to_one_interpreter():
+    """Its name ends in this interpreter's suffix, so that another Python builds its own instead of loading it."""
+    import sysconfig
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert "cpython" in suffix and os.path.basename(build.FASTCALL) == "kda_fastcall" + suffix
