@@ -18,13 +18,6 @@
 #include "kda_tc.cuh"
 
 namespace kda {
-namespace tcp {
-// the driver's tensor-map encoder, looked up once (kda_prefill_tc.cu)
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn();
-}  // namespace tcp
 namespace lin {
 
 constexpr int KB = 128;                             // K block: channels per scale

@@ -56,6 +56,11 @@ int current_sms();
 int prefill_auto_segments(int64_t T, int H, int C);
 
 namespace tcp {
+// The driver's tensor-map encoder, looked up once (NULL where the driver has none).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
 // 2-D tiled TMA map over a row-major [rows][inner] tensor of `elem`-byte
 // elements with a box of box_inner x box_rows; false if the encoder fails.
 bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint32_t elem, uint64_t inner,
