@@ -330,13 +330,15 @@ __global__ void __launch_bounds__(Few<NT>::NTHREADS, Few<NT>::PER_SM)
             }
             if (SPLIT) break;
         }
-        // every copy lands before shared memory is used otherwise or goes away
+        // Every copy lands, and every release of a stage arrives, before shared memory is used otherwise or goes
+        // away: nothing else waits for the last MMAs' arrivals on `empty`.
         for (int i = 0; i < F::ST; ++i) {
             if (--st < 0) {
                 st = F::ST - 1;
                 ph ^= 1;
             }
             if (!mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
+            ok = wait_more(empty + st, ph ^ 1, ok);
         }
     } else if (warp == F::JW + 1) {
         int st = 0, as = 0;
@@ -882,16 +884,17 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                     }
                 }
             }
-            // Every copy of both CTAs lands before shared memory goes away (the even CTA's barriers count
-            // them): the ring's next phase of each stage is the one that the last copies complete.
-            if (rank == 0)
-                for (int i = 0; i < stages; ++i) {
-                    if (--st < 0) {
-                        st = stages - 1;
-                        ph ^= 1;
-                    }
-                    if (!tc::mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
+            // Every copy of both CTAs lands (the even CTA's barriers count them), and every release of a stage
+            // arrives at each CTA, before shared memory goes away: the phases of each stage that its last copies
+            // and the MMAs that read them complete.
+            for (int i = 0; i < stages; ++i) {
+                if (--st < 0) {
+                    st = stages - 1;
+                    ph ^= 1;
                 }
+                if (rank == 0 && !tc::mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
+                ok = wait_more(empty + st, ph ^ 1, ok);
+            }
         } else if (warp == JW + 1) {
             if (rank == 0) {
                 int st = 0, as = 0;
