@@ -72,6 +72,21 @@ template <> struct Elem<__nv_bfloat16> {
     __device__ __forceinline__ static void store(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 };
 
+// Ordinary loads, for memory that the kernel ahead on the stream may write. A programmatic dependent launch
+// starts before that kernel ends, and the read-only path (__ldg, or what the compiler makes of a const
+// __restrict__ pointer) wants memory that nothing writes for as long as the kernel lives.
+__device__ __forceinline__ float ld_plain(const float *p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_plain(const float4 *p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // 1 / sqrt(ss + eps), or 0 when ss + eps == 0 (zero vector stays zero).
 __device__ __forceinline__ float inv_norm(float ss, float eps) {
     float den = ss + eps;

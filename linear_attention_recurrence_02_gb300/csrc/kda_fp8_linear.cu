@@ -202,7 +202,7 @@ template <int NT, typename TO, bool SPLIT>
 __global__ void __launch_bounds__(Few<NT>::NTHREADS, Few<NT>::PER_SM)
     linear_few_kernel(const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_a,
-                      const float *__restrict__ sa, const float *__restrict__ sw,
+                      const float *sa, const float *sw,
                       TO *__restrict__ y, int M, int N, int nkb, int64_t ldy, int mt,
                       int S, unsigned units, unsigned *err) {
     using namespace tc;
@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(Few<NT>::NTHREADS, Few<NT>::PER_SM)
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int e = t2 + 64 * i, j = e % NT, kb = kc + e / NT < k1 ? kc + e / NT : k1 - 1;
-                    av[i] = __ldg(sa + (int64_t)kb * M + (m0 + j < M ? m0 + j : M - 1));
-                    wv[i] = __ldg(swp + kb);
+                    av[i] = ld_plain(sa + (int64_t)kb * M + (m0 + j < M ? m0 + j : M - 1));
+                    wv[i] = ld_plain(swp + kb);
                 }
                 ok = wait_more(sempty + cs, cph, ok);
 #pragma unroll
@@ -669,8 +669,8 @@ __device__ __forceinline__ void store_rows(TO *to, int64_t ld, const uint8_t *fr
 template <typename TO, bool SPLIT>
 __global__ void __launch_bounds__(many::NTHREADS, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                       const __grid_constant__ CUtensorMap tm_y, const float *__restrict__ sa,
-                       const float *__restrict__ sw, TO *__restrict__ y, int M, int N, int nkb, int64_t ldy,
+                       const __grid_constant__ CUtensorMap tm_y, const float *sa,
+                       const float *sw, TO *__restrict__ y, int M, int N, int nkb, int64_t ldy,
                        unsigned mt, unsigned tile0, unsigned tiles, int by_tma, int S, int stages,
                        unsigned *err) {
     using namespace tc;
@@ -940,9 +940,9 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                         const float *ap = sa + (int64_t)kc * M;
                         float *b = reinterpret_cast<float *>(sm + SCALES) + cs * (CHUNK / 4) + (w2 + i) * 256 + lane;
                         float av[4];
-                        const float wa = __ldg(w0 + kc), wb = __ldg(w1 + kc);
+                        const float wa = ld_plain(w0 + kc), wb = ld_plain(w1 + kc);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) av[q] = __ldg(ap + (m0 + 32 * q < M ? m0 + 32 * q : M - 1));
+                        for (int q = 0; q < 4; ++q) av[q] = ld_plain(ap + (m0 + 32 * q < M ? m0 + 32 * q : M - 1));
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             b[32 * q] = av[q] * wa;

@@ -48,7 +48,7 @@ static void launch_dependent(void (*kern)(P...), unsigned grid, dim3 block, cuda
 // x + residual itself, not its rounding to sum_out's type.
 template <typename TX, typename TR, bool RES, int VPT>
 __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX *x, const TR *res,
-                                                               const float *__restrict__ w, TR *sum_out,
+                                                               const float *w, TR *sum_out,
                                                                uint8_t *__restrict__ y, float *__restrict__ scales,
                                                                int64_t T, int N, float inv_n, float eps) {
     __shared__ float red[32];
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX *x, cons
         const bool in = live && v < nv;
         if (in) {
             float wv[8];
-            const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + 8 * v));
-            const float4 w1 = __ldg(reinterpret_cast<const float4 *>(w + 8 * v) + 1);
+            const float4 w0 = ld_plain(reinterpret_cast<const float4 *>(w + 8 * v));
+            const float4 w1 = ld_plain(reinterpret_cast<const float4 *>(w + 8 * v) + 1);
             wv[0] = w0.x; wv[1] = w0.y; wv[2] = w0.z; wv[3] = w0.w;
             wv[4] = w1.x; wv[5] = w1.y; wv[6] = w1.z; wv[7] = w1.w;
 #pragma unroll
@@ -182,8 +182,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 template <int D, typename T, int ACT>
-__global__ void __launch_bounds__(GATED_NT, 10) gated_rmsnorm_fp8_kernel(const T *__restrict__ o, const T *__restrict__ gate,
-                                                                const float *__restrict__ w, uint8_t *__restrict__ y,
+__global__ void __launch_bounds__(GATED_NT, 10) gated_rmsnorm_fp8_kernel(const T *o, const T *gate,
+                                                                const float *w, uint8_t *__restrict__ y,
                                                                 float *__restrict__ scales, int64_t Ttot, int C,
                                                                 int nb, float eps) {
     const int ln = threadIdx.x & 7;
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(GATED_NT, 10) gated_rmsnorm_fp8_kernel(const T
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[i] = 0.f;
         }
-        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + j + 8 * q)),
-                     w1 = __ldg(reinterpret_cast<const float4 *>(w + j + 8 * q) + 1);
+        const float4 w0 = ld_plain(reinterpret_cast<const float4 *>(w + j + 8 * q)),
+                     w1 = ld_plain(reinterpret_cast<const float4 *>(w + j + 8 * q) + 1);
         const float2 wv[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
                               make_float2(w1.z, w1.w)};
 #pragma unroll

@@ -93,3 +93,48 @@ def test_linear_bits_do_not_depend_on_strides(env, M, N, K, ld):
                 y = torch.empty((M, ldy), dtype=dt, device="cuda")[:, :N]
                 kda.kda_fp8_linear(x[:, :K], sa, z[:, :K], sw, y)
                 assert torch.equal(y, want.to(dt))
+
+
+def test_scales_and_weights_written_by_the_kernel_ahead(env):
+    """What a product writes is the next norm's weight and the next product's scales of both kinds, buffers used
+    again at once with other values and no wait in between: the bits of the same calls made one at a time."""
+    torch, kda = env
+    K, f8 = 512, torch.float8_e4m3fn
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((24, K), generator=gen, device="cuda")
+    a, sa, w, sw = _case(torch, 6, 6, K, 256)  # six rows of products: the weights of six rounds
+    d, sd, v, sv = _case(torch, 7, 300, 640, K)
+    og = torch.randn((24, 4, 128), generator=gen, device="cuda")
+
+    def rounds(wait):
+        weight = torch.zeros((1, K), device="cuda")  # one buffer for every round's weight and scales
+        q, s = torch.zeros((24, K), dtype=f8, device="cuda"), torch.zeros((4, 24), device="cuda")
+        y = torch.zeros((24, 640), device="cuda")
+        out = []
+
+        def call(fn, *args, **k):
+            fn(*args, **k)
+            if wait:
+                torch.cuda.synchronize()
+
+        for i in range(6):
+            call(kda.kda_fp8_linear, a[i:i + 1], sa[:, i:i + 1].contiguous(), w, sw, weight)
+            call(kda.kda_add_rmsnorm_fp8, x, weight[0], q, s)
+            out += [q.view(torch.uint8).clone(), s.clone()]
+            call(kda.kda_fp8_linear, a[i:i + 1], sa[:, i:i + 1].contiguous(), w, sw, weight)
+            call(kda.kda_gated_rmsnorm_fp8, x.view(24, 4, 128), og, weight[0, :128], q.view(24, 4, 128), s)
+            call(kda.kda_fp8_linear, q, s, v, sv, y)  # scales from the norm just ahead
+            out += [q.view(torch.uint8).clone(), y.clone()]
+            call(kda.kda_fp8_linear, a[i:i + 1], sa[:, i:i + 1].contiguous(), w, sw, weight)
+            call(kda.kda_fp8_linear, q, s, v, weight[0, :20].view(5, 4), y)  # a weight's scales from a product
+            out.append(y.clone())
+            z = torch.zeros((128, 640), device="cuda")
+            call(kda.kda_fp8_linear, a[i:i + 1], sa[:, i:i + 1].contiguous(), w, sw, weight)
+            call(kda.kda_fp8_linear, d[:128], weight.view(4, 128), v, sv, z)  # and a token's
+            out.append(z)
+        return out
+
+    for _ in range(5):
+        for got, want in zip(rounds(False), rounds(True)):
+            assert torch.equal(got, want)
+    kda.kda_sync_status()
