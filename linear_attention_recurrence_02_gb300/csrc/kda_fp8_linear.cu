@@ -330,23 +330,24 @@ __global__ void __launch_bounds__(Few<NT>::NTHREADS, Few<NT>::PER_SM)
             }
             if (SPLIT) break;
         }
-        // Every copy lands, and every release of a stage arrives, before shared memory is used otherwise or goes
-        // away: nothing else waits for the last MMAs' arrivals on `empty`.
+        // every copy lands before shared memory is used otherwise or goes away
         for (int i = 0; i < F::ST; ++i) {
             if (--st < 0) {
                 st = F::ST - 1;
                 ph ^= 1;
             }
             if (!mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
-            ok = wait_more(empty + st, ph ^ 1, ok);
         }
     } else if (warp == F::JW + 1) {
         int st = 0, as = 0;
         uint32_t ph = 0, aph = 1;  // the accumulators start out free
         const uint64_t a0 = sdesc_sw128(sbase, 16, 1024), b0 = sdesc_sw128(sbase + 128 * KB, 16, 1024);
+        // Blocks after which a stage is filled again. The last ones' stages are not released: no one waits for
+        // them, and an arrival could come after the CTA has left.
+        int64_t refills = (SPLIT ? 1 : (int64_t)((units - first + gridDim.x - 1) / gridDim.x)) * (k1 - k0) - F::ST;
         for (unsigned u = first; u < units; u += gridDim.x) {
             const int n0 = feature(u), m0 = token(u);
-            for (int kb = k0; kb < k1; ++kb) {
+            for (int kb = k0; kb < k1; ++kb, --refills) {
                 const uint64_t a = a0 + (uint64_t)(st * (F::STAGE / 16)), b = b0 + (uint64_t)(st * (F::STAGE / 16));
                 ok = wait_more(full + st, ph, ok);
                 ok = wait_more(aempty + as, aph, ok);
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(Few<NT>::NTHREADS, Few<NT>::PER_SM)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_f8(tbase + as * NT, a + 2 * ks, b + 2 * ks, idesc_f8(128, NT), ks > 0);
-                    mma_commit(empty + st);
+                    if (refills > 0) mma_commit(empty + st);
                     mma_commit(afull + as);
                 }
                 if (++as == F::AS) {
@@ -884,24 +885,26 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                     }
                 }
             }
-            // Every copy of both CTAs lands (the even CTA's barriers count them), and every release of a stage
-            // arrives at each CTA, before shared memory goes away: the phases of each stage that its last copies
-            // and the MMAs that read them complete.
-            for (int i = 0; i < stages; ++i) {
-                if (--st < 0) {
-                    st = stages - 1;
-                    ph ^= 1;
+            // Every copy of both CTAs lands before shared memory goes away (the even CTA's barriers count
+            // them): the ring's next phase of each stage is the one that the last copies complete.
+            if (rank == 0)
+                for (int i = 0; i < stages; ++i) {
+                    if (--st < 0) {
+                        st = stages - 1;
+                        ph ^= 1;
+                    }
+                    if (!tc::mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
                 }
-                if (rank == 0 && !tc::mbar_wait(full + st, ph ^ 1, WAIT_LIMIT)) ok = false;
-                ok = wait_more(empty + st, ph ^ 1, ok);
-            }
         } else if (warp == JW + 1) {
             if (rank == 0) {
                 int st = 0, as = 0;
                 uint32_t ph = 0, aph = 1;  // the accumulators start out free
                 const uint64_t a0 = sdesc_sw128(sbase, 16, 1024), b0 = sdesc_sw128(sbase + A_BYTES, 16, 1024);
+                // blocks after which a stage is filled again: the last ones' stages are not released, as no one
+                // waits for them and an arrival could come after a CTA has left
+                int64_t refills = (int64_t)((tiles - first + npairs - 1) / npairs) * (kb1 - kb0) - stages;
                 for (unsigned tile = first; tile < tiles; tile += npairs) {
-                    for (int kb = kb0; kb < kb1; ++kb) {
+                    for (int kb = kb0; kb < kb1; ++kb, --refills) {
                         const uint64_t a = a0 + (uint64_t)(st * (STAGE / 16)), b = b0 + (uint64_t)(st * (STAGE / 16));
                         ok = wait_more(full + st, ph, ok);
                         ok = wait_more(aempty + as, aph, ok);
@@ -912,7 +915,7 @@ __global__ void __launch_bounds__(many::NTHREADS, 1)
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_f8_pair(tbase + as * BN, a + 2 * ks, b + 2 * ks, idesc_f8(BM, BN), ks > 0);
                             commit_pair(afull + as, lead);
-                            commit_pair(empty + st, lead);
+                            if (refills > 0) commit_pair(empty + st, lead);
                         }
                         as ^= 1;
                         aph ^= as == 0;
