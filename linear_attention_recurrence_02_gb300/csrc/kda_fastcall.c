@@ -33,7 +33,8 @@ static struct {
     int ready;
 } S;
 
-static PyObject *n_dtype, *n_shape, *n_get_device, *n_is_contiguous, *n_data_ptr, *n_stride, *n_cuda_stream;
+static PyObject *n_dtype, *n_shape, *n_get_device, *n_is_contiguous, *n_data_ptr, *n_stride, *n_cuda_stream,
+    *n_device_index;
 
 enum { DT_F32 = 0, DT_BF16 = 1, DT_F8 = 2, DT_OTHER = -1 };
 
@@ -114,13 +115,24 @@ static int one_device(const Tensor *t, const Tensor *const *others, int n) {
     return 0;
 }
 
-/* Handle of `stream`, or of the current stream of device `dev` where it is None. 1: found, 0: error set,
- * -1: a default stream (whose handle, 0, names no device) of a device that is not the current one, or None
- * there. */
+/* Handle of `stream`, or of the current stream of device `dev` where it is None. 1: found, 0: error set (a
+ * stream of another device among them, where the kernels would run beside the tensors' memory), -1: a default
+ * stream (whose handle, 0, names no device) of a device that is not the current one, or None there. */
 static int find_stream(PyObject *stream, long dev, void **handle) {
     PyObject *o;
     *handle = NULL;
     if (stream != Py_None) {
+        long long on;
+        if (long_of(PyObject_GetAttr(stream, n_device_index), &on)) {
+            if (on != dev) {
+                PyErr_SetString(PyExc_ValueError, "stream must be on the tensors' device");
+                return 0;
+            }
+        } else if (PyErr_ExceptionMatches(PyExc_AttributeError)) {
+            PyErr_Clear(); /* a stream that does not say */
+        } else {
+            return 0;
+        }
         if ((o = PyObject_GetAttr(stream, n_cuda_stream)) == NULL) return 0;
         *handle = PyLong_AsVoidPtr(o);
         Py_DECREF(o);
@@ -300,7 +312,7 @@ PyMODINIT_FUNC PyInit_kda_fastcall(void) {
         const char *text;
     } names[] = {{&n_dtype, "dtype"},       {&n_shape, "shape"},       {&n_get_device, "get_device"},
                  {&n_is_contiguous, "is_contiguous"}, {&n_data_ptr, "data_ptr"}, {&n_stride, "stride"},
-                 {&n_cuda_stream, "cuda_stream"}};
+                 {&n_cuda_stream, "cuda_stream"}, {&n_device_index, "device_index"}};
     for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i)
         if ((*names[i].name = PyUnicode_InternFromString(names[i].text)) == NULL) return NULL;
     return PyModule_Create(&module);

@@ -392,9 +392,10 @@ def kda_fp8_linear(a, a_scales, w, w_scales, y, stream=None):
         _settle(status, fn, a.device, a, a_scales, w, w_scales, y, stream)
 
 
-def _check_kinds(like, floats, ints, x, workspace):
+def _check_kinds(like, floats, ints, x, workspace, stream):
     """Types and devices of a one-call way out's tensors (None: absent): the library sees pointers alone, and would
-    read and write past the end of a tensor of a narrower type. `like` have x's type, `floats` float32, `ints` int64."""
+    read and write past the end of a tensor of a narrower type. `like` have x's type, `floats` float32, `ints` int64.
+    A given stream has to be on their device too."""
     import torch
     for group, dtype, what in ((like, x.dtype, "must have the inputs' dtype"),
                                (floats, torch.float32, "must be float32"), (ints, torch.int64, "must be int64")):
@@ -404,6 +405,8 @@ def _check_kinds(like, floats, ints, x, workspace):
     for t in (*like.values(), *floats.values(), *ints.values(), workspace):
         if t is not None and t.device != x.device:
             raise ValueError("tensors must be on one CUDA device")
+    if stream is not None and getattr(stream, "device", x.device) != x.device:
+        raise ValueError("stream must be on the tensors' device")
 
 
 def _check_proj(out_gate, norm_weight, proj, proj_scales, y, lead, H, D, x):
@@ -450,7 +453,7 @@ def kda_shortconv_decode_step_proj(x, ring, w, g, beta, state, out_gate, norm_we
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, B, H, D, x)
     _check_kinds({"ring": ring}, {"w": w, "g": None if code == KDA_GATE_NONE else g, "beta": beta, "state": state},
-                 {}, x, workspace)
+                 {}, x, workspace, stream)
     workspace, size = _scratch(workspace, kda_shortconv_decode_step_proj_workspace_bytes(B, H, D), x.device, stream)
     flags = KDA_DECODE_OVERLAP_PREV if overlap_prev else 0
     with _current(x.device):
@@ -484,7 +487,7 @@ def kda_chunk_prefill_proj(q, k, v, g, beta, out_gate, norm_weight, proj, proj_s
     Nout = _check_proj(out_gate, norm_weight, proj, proj_scales, y, T, H, D, q)
     _check_kinds({"k": k, "v": v}, {"g": None if code == KDA_GATE_NONE else g, "beta": beta,
                                     "initial_state": initial_state, "final_state": final_state},
-                 {"cu_seqlens": cu_seqlens}, q, workspace)
+                 {"cu_seqlens": cu_seqlens}, q, workspace, stream)
     workspace, size = _scratch(workspace, kda_chunk_prefill_proj_workspace_bytes(T, N, H, D, chunk_size), q.device,
                                stream)
     with _current(q.device):

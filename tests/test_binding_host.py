@@ -33,9 +33,15 @@ class _Dev:
     def element_size(self):
         return self.dtype.itemsize
 
+    def stride(self):
+        return tuple(int(np.prod(self.shape[i + 1:])) for i in range(len(self.shape)))
+
 
 class _Stream:
-    cuda_stream, device = 77, torch.device("cuda:0")
+    cuda_stream = 77
+
+    def __init__(self, index=0):
+        self.device, self.device_index = torch.device("cuda", index), index
 
 
 class _Library:
@@ -59,6 +65,7 @@ def env(monkeypatch):
     """The binding over _Library; `env.made` lists (bytes, stream that was current) of each allocation."""
     ensure_built()
     from linear_attention_recurrence_02_gb300 import kda
+    kda._fastcall()  # over the real library
     fake, state = _Library(kda.lib()), {"current": None}
     made = []
 
@@ -195,3 +202,34 @@ def test_one_call_ways_out_take_what_they_document(env):
         _prefill(env.kda, dt=dt, g=None, gate="none", initial_state=_Dev(1, 2, 64, 64), final_state=_Dev(1, 2, 64, 64),
                  cu_seqlens=_Dev(2, dtype=torch.int64))
     assert len(env.calls) == 10
+
+
+def test_streams_of_another_device_are_refused(env):
+    """By the one-call ways out and by the three operators (no tokens: the library then returns before CUDA)."""
+    for call in (_decode, _prefill):
+        with pytest.raises(ValueError, match="stream"):
+            call(env.kda, stream=_Stream(1))
+    assert env.calls == [] and env.made == []
+    kda = env.kda
+
+    def add(stream):
+        kda.kda_add_rmsnorm_fp8(_Dev(0, 256), _Dev(256), _Dev(0, 256, dtype=F8), _Dev(2, 0), stream=stream)
+
+    def gated(stream):
+        kda.kda_gated_rmsnorm_fp8(_Dev(0, 2, 128), _Dev(0, 2, 128), _Dev(128), _Dev(0, 2, 128, dtype=F8), _Dev(2, 0),
+                                  stream=stream)
+
+    def linear(stream):
+        kda.kda_fp8_linear(_Dev(0, 256, dtype=F8), _Dev(2, 0), _Dev(100, 256, dtype=F8), _Dev(1, 2), _Dev(0, 100),
+                           stream=stream)
+
+    class Handle:  # a stream that does not say where it is
+        cuda_stream = 78
+
+    for call in (add, gated, linear):
+        call(_Stream(0))
+        call(Handle())
+        with pytest.raises(ValueError, match="stream must be on the tensors' device"):
+            call(_Stream(1))
+        with pytest.raises(AttributeError):
+            call(object())
