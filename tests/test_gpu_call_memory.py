@@ -107,3 +107,24 @@ def test_own_workspace_on_another_stream(env, make):
         for t in after:
             assert bool((t == 255).all())
     kda.kda_sync_status()
+
+
+def test_ways_out_without_tokens(env):
+    """No sequences at a decode step and no tokens of a prompt: nothing is launched but the states' passage."""
+    torch, kda = env
+    H, D, hidden, bf = 4, 128, 256, torch.bfloat16
+    w, ws = _weight(torch, torch.Generator(device="cuda").manual_seed(1), hidden, H * D)
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    nw = torch.ones(D, device="cuda")
+    kda.kda_shortconv_decode_step_proj(z(0, 3, H, D, dt=bf), z(0, 3, H, 3, D, dt=bf), z(3, H, D, 4), z(0, H, D), z(0, H),
+                                       z(0, H, D, D), z(0, H, D, dt=bf), nw, w, ws, z(0, hidden, dt=bf))
+    none = [z(0, H, D, dt=bf)] * 3 + [z(0, H, D), z(0, H), z(0, H, D, dt=bf), nw, w, ws, z(0, hidden, dt=bf)]
+    for n, cu in ((1, None), (3, torch.zeros(4, dtype=torch.int64, device="cuda"))):
+        s0 = torch.randn((n, H, D, D), device="cuda")
+        s1 = torch.full_like(s0, float("nan"))
+        for k in ({}, {"stream": torch.cuda.Stream()}):
+            torch.cuda.synchronize()
+            kda.kda_chunk_prefill_proj(*none, initial_state=s0, final_state=s1, cu_seqlens=cu, **k)
+            torch.cuda.synchronize()
+            assert torch.equal(s0, s1)
+    kda.kda_sync_status()
