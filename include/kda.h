@@ -267,7 +267,8 @@ kda_status kda_gated_rmsnorm(const void *o, const void *gate, const float *weigh
  *
  * A row whose mean square plus eps is exactly zero gives zeros. The norm takes
  * the fp32 sum itself, not its rounding to res_dtype; |h| must stay below
- * about 1e19, where the sum of squares passes fp32.
+ * about 1e19, where the sum of squares passes fp32 (and with eps = 0 above
+ * about 1e-18, where squares lose bits below it).
  *   x [T,N] dtype; residual [T,N] res_dtype or NULL; weight [N] fp32
  *   sum_out [T,N] res_dtype or NULL: receives h; it may be residual, or x
  *     where dtype = res_dtype
@@ -284,7 +285,8 @@ kda_status kda_add_rmsnorm_fp8(const void *x, const void *residual, const float 
  * the output projection: the norm runs over each (token, head) row of D
  * channels as there, the scales' blocks over the token's H * D channels (one
  * head per block at D = 128, 128 / D heads below). The activation of the gate
- * uses the fast exponential and division.
+ * uses the fast exponential and division. |o| has the range of h in
+ * kda_add_rmsnorm_fp8.
  *   o, gate [T,H,D] dtype; weight [D] fp32; y [T,H,D] e4m3 codes;
  *   scales [ceil(H*D/128),T] fp32. y and scales may not alias another argument.
  * Requires T >= 0 (0 is a no-op), H >= 1, D in {16,32,64,128}, eps >= 0.
@@ -304,7 +306,9 @@ kda_status kda_gated_rmsnorm_fp8(const void *o, const void *gate, const float *w
  *   y [M,N] out_dtype, row stride ldy (strides in elements); elements between
  *     N and ldy keep their values. y may not alias another argument. With many
  *     tokens, rows a multiple of 16 bytes apart are written fastest.
- * e4m3 products are exact and are summed in fp32; the sums of the K blocks are
+ * e4m3 products are exact and are summed in fp32; the two scales of a block are
+ * multiplied in fp32, whose normal range their product must keep (a zero sum
+ * times an infinite product is NaN); the sums of the K blocks are
  * scaled and joined in fp32, in an order that depends on M, N, K and the GPU
  * alone: the same inputs give the same bits, whatever the strides, and the same
  * sums before their rounding to out_dtype.

@@ -143,8 +143,8 @@ __device__ __forceinline__ void tma_load_once(void *dst, const CUtensorMap *map,
 // with few tokens still feeds whole 128-row tiles from every SM, as S CTAs of a
 // cluster with a run of the K blocks each (SPLIT), or as CTAs that walk several
 // units, so that one's first blocks arrive while the one before is stored (128 x
-// 36864 x 4096: 27.6 us; 29.5 and, with a CTA per unit, 33.3 before the results'
-// stores were predicated). JW warps join the block
+// 36864 x 4096: 25.8 us; while the results' stores were still branches 29.5, and
+// 33.3 with a CTA per unit). JW warps join the block
 // sums (a thread holds its feature's sums for TPW tokens; the products of the
 // token scales with the weight block's come from shared memory), the next
 // streams the weight and token tiles through a ring of ST stages, the next issues
@@ -153,10 +153,10 @@ __device__ __forceinline__ void tma_load_once(void *dst, const CUtensorMap *map,
 // shared memory: each CTA adds up its share of the tokens over the S CTAs in
 // their order. Two CTAs fit an SM, of 128 tokens one.
 // Why 128 tokens: the weight tile is read once where 64 would read it twice, and
-// a tile of 256 x 256 would be half empty (100 x 12288 x 8192: 22.4 us, 28.3 at
-// 64, 27.4 in the many-token kernel; 80 x 2912 x 4096: 7.8, 8.2 and 12.2).
+// a tile of 256 x 256 would be half empty (100 x 12288 x 8192: 22.0 us, 27.9 at
+// 64, 26.5 in the many-token kernel; 128 x 12288 x 4096: 13.0, 15.7 and 16.1).
 // A weight tile that one CTA alone reads is marked first to leave L2 (64 x
-// 36864 x 4096: 27.1 us, 28.5 without), where the state, the activations and
+// 36864 x 4096: 23.4 us, 24.8 without), where the state, the activations and
 // the next call's tokens stay.
 // A programmatic dependent launch: before the kernel ahead of it on the stream
 // has completed it only prefetches weight tiles into L2, which cannot serve a
@@ -470,7 +470,12 @@ template <int NT> static void few_resident(int (&at_once)[9], int most) {
 }
 
 // Estimated times in ns choose between kernels and splits of K; their constants are fitted to measurements at
-// 8 to 224 weight tiles of 4 to 64 K blocks, which they meet within a tenth. A call's CTAs take `ctas` and the
+// 8 to 224 weight tiles of 4 to 64 K blocks, which they meet within a tenth. Of 90 sizes drawn over the whole range
+// (1 to 800 tokens) 76 run within 7 % of the best kernel and split. The others lose 8 to 23 %: up to 16 weight tiles
+// of 12 to 41 K blocks, where six or eight CTAs a tile would be right (8 x 24 x 1984: 3.55 us, 2.96), two tokens
+// and 73 to 93 tiles, where none should be split (2 x 11797 x 2768: 10.8 us, 8.8), and rows that straddle 128-byte
+// lines (146 x 11144 x 2640: 16.6 us, 14.4 in the many-token kernel; the worst known, with a long K, is
+// 182 x 10432 x 11312: 64 us at 64 tokens, 41 there). A call's CTAs take `ctas` and the
 // weights' bytes 2.5 ns per 16 KB tile: the longer of the two and some of the shorter.
 static int64_t with_weights(int64_t ctas, int N, int nkb) {
     const int64_t bytes = ((int64_t)N + 127) / 128 * nkb * 5 / 2;
@@ -482,9 +487,9 @@ static int64_t with_weights(int64_t ctas, int N, int nkb) {
 // meeting of the partial sums MEET, 0.7 us more on shared SMs; CTAs that fill the GPU 0.6 to 1.2 us more than a
 // few (the next call's cannot set up beside them); and a further wave of clusters a call's time, of units that a
 // CTA walks 1.1 us. With 64 tokens or more, rows that straddle 128-byte lines take half as long again where CTAs
-// walk units (300 x 30000 x 1040: 29 us, 22 in the many-token kernel).
-// (1 x 12288 x 4096, 96 tiles: 10.3 us at S = 3, 11.1 at 1 or 2, 14.6 at 4; 64 x 12288 x 4096: 12.8 us at 2 or 3,
-// 13.3 at 1, 17.7 at 4; 64 x 4096 x 8192, 32 tiles: 10.5 us at 4, 19.6 at 1.)
+// walk units (300 x 30000 x 1040: 28.6 us, 21.5 in the many-token kernel).
+// (1 x 12288 x 4096, 96 tiles: 9.6 us at S = 3, 10.8 at 1, 11.2 at 2, 13.5 at 4; 64 x 12288 x 4096: 12.2 us at 2 or
+// 3, 13.0 at 1, 17.0 at 4; 64 x 4096 x 8192, 32 tiles: 10.2 us at 4, 19.5 at 1.)
 struct FewPlan {
     int64_t units;
     int S, at_once;  // clusters that run at once
@@ -637,7 +642,7 @@ template <int N> __device__ __forceinline__ void bulk_wait_read_but() {
 // row) to rows of any alignment: 4 bytes a lane, sixteen rows' reads in flight, predicated stores. Where a
 // row of 2-byte elements starts between two words, each lane's word is joined from two neighbours' halves and
 // the elements at the ends go by themselves. (3000 x 20001 x 464: bf16 63 us, 78 with a branch a row, 131 with
-// an element a lane; f32 88. Rows of 20000 elements, which a tensor copy stores: 45 and 60. Rows that start inside
+// an element a lane; f32 86. Rows of 20000 elements, which a tensor copy stores: 42 and 58. Rows that start inside
 // a 32-byte sector also write that sector in two parts.)
 template <typename TO>
 __device__ __forceinline__ void store_rows(TO *to, int64_t ld, const uint8_t *from, int rows, int cols) {
@@ -1044,8 +1049,8 @@ struct ManyPlan {
 
 // 350 ns a K block, 1 us a tile, 3.5 us a launch and 1.2 us more for one that fills the GPU; a split takes 3 or
 // 5.5 us (2 or 4 pairs) for the meeting of the partial sums, and pays for tiles that would leave most pairs idle,
-// be it all of them or a last wave's, when K is long. (512 x 4096 x 12288, 32 tiles: 25 us at S = 2, 35.5 whole;
-// 240 x 3800 x 12288, 15 tiles: 19 us at 4, 35 whole.)
+// be it all of them or a last wave's, when K is long. (512 x 4096 x 12288, 32 tiles: 25 us at S = 2, 35 whole;
+// 240 x 3800 x 12288, 15 tiles: 19 us at 4, 22.5 at 2, 34.5 whole; 2560 x 2250 x 8192: 45.5 and 51.3.)
 template <typename TO> static ManyPlan many_plan(int64_t M, int N, int nkb) {
     ManyPlan p{0, 0, 1, INT64_MAX};
     p.tiles = ((M + many::BM - 1) / many::BM) * (((int64_t)N + many::BN - 1) / many::BN);
@@ -1063,9 +1068,9 @@ template <typename TO> static ManyPlan many_plan(int64_t M, int N, int nkb) {
 }
 
 // Four stages and two pieces where a pair has tiles after its first and short ones: results leave beside the next
-// tile's K blocks (4864 x 4096 x 512: 14.6 us, 15.7 with one piece; x 2048: 32.2 and 33.0; 3000 x 20000 x 464:
-// 44.6 and 47.8). Else five and one, for weights that come from memory (128 x 12288 x 4096: 16.5 us, 17.6 with
-// four; 182 x 10432 x 11312: 38.6 and 41.6; 4096 x 4096 x 12288 the same).
+// tile's K blocks (4864 x 4096 x 512: 14.6 us, 15.7 with one piece; x 2048: 32.6 and 33.1; 3000 x 20000 x 464:
+// 42.7 and 46.2). Else five and one, for weights that come from memory (128 x 12288 x 4096: 16.2 us, 17.2 with
+// four; 182 x 10432 x 11312: 40.8 and 42.4; 4096 x 4096 x 12288 the same).
 static int many_stages(bool more_tiles, int nkb) { return more_tiles && nkb <= 16 ? many::ST - 1 : many::ST; }
 
 template <typename TO>

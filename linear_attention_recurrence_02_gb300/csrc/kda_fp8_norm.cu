@@ -164,10 +164,12 @@ static kda_status dispatch_add(bool res_bf16, const void *x, const void *res, co
 // two at a time (f32x2), the gate's activation by the hardware exponential
 // and reciprocal without their handling of denormals (a few ulp, far below the
 // 2^-4 step of e4m3; a gate below about -87 closes fully), three-way maxima.
-// 4096 x 96 heads x 128, bf16: 41.4 us (42.1 without the bound to ten blocks
-// an SM; 45.1 with blocks of 256 threads, 52.2 with 64; 44.1 at best as a
-// persistent grid that loads a unit ahead; 56.5 with 8 channels a lane and one
-// product at a time).
+// 4096 x 96 heads x 128, bf16: 40.1 us (41.1 without the bound to ten blocks
+// an SM; 41.2 with blocks of 256 threads, 50.3 with 64). The bound suits that
+// form: bf16 SiLU takes 43.2 us with it and 41.5 without, fp32 74.7 and 70.5 (a
+// few registers spill), fp32 SiLU 71.5 and 71.4. When it took 41.4 us, a
+// persistent grid that loads a unit ahead took 44.1 at best, and 8 channels a
+// lane with one product at a time 56.5.
 constexpr int GATED_NT = 128;
 __device__ __forceinline__ float sigmoid_fast(float z) {
     float e, r;
