@@ -587,6 +587,117 @@ kda_status kda_chunk_prefill_noalloc(const void *q, const void *k, const void *v
                                      void *out, const int64_t *cu_seqlens, int N, int64_t T, int H, int D,
                                      int C, kda_dtype dtype, float l2_eps, kda_stream_t stream);
 
+/*
+ * The softmax-attention layers that a hybrid stack keeps between its KDA
+ * layers ("为什么 Kimi K3 敢把 KV Cache 扔掉？一篇讲透 GPT-2 到 K3 的架构进化", section
+ * 7: three KDA layers to one of full attention): norms and rotation of the
+ * queries and keys, a paged cache that holds keys and values in 4 bits, and
+ * attention over it.
+ *
+ * kda_qk_norm_rope: RMSNorm of each (token, head) row of q and k and the
+ * rotation by the token's position, in one pass.
+ *   y = x / sqrt(mean x^2 + eps) * w   (fp32; skipped where the weight is NULL)
+ *   channel pair i of the first R channels turns by positions[t] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin), the pair being channels i and
+ *   i + R/2, or with interleaved = 1 channels 2i and 2i + 1; channels from R on
+ *   stay as they are
+ *
+ *   q [T,Hq,D], k [T,Hk,D] dtype, q_out and k_out alike: heads contiguous, tokens
+ *            at the given strides in elements (parts of one wider row, as a
+ *            common projection leaves them); q_out may be q and k_out k, with
+ *            equal strides. Hk = 0: no k (k and k_out may be NULL)
+ *   q_weight, k_weight  [D] fp32, or NULL
+ *   positions int64 [T], inv_freq fp64 [R/2] radians a position; unused with R = 0.
+ *            The product is formed modulo a full turn in integers: an angle is as
+ *            exact at position 2^31 as at 1. Frequencies are finite.
+ * Requires T >= 0, D in {16,32,64,128}, R a multiple of 16 up to D; strides
+ * multiples of 16 bytes. A row whose mean square plus eps is zero normalises to
+ * zero. A programmatic dependent launch that waits for the kernel before it.
+ */
+kda_status kda_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const float *q_weight,
+                            const float *k_weight, const int64_t *positions, const double *inv_freq, int64_t T,
+                            int Hq, int Hk, int D, int R, int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                            int64_t k_out_stride, int interleaved, float eps, kda_dtype dtype, kda_stream_t stream);
+
+/*
+ * The cache: uint8 [pages][Hk][page_size / 16][18 * D], D = 64 or 128, page_size
+ * 16, 32, 64, 128 or 256. A block of 18 * D bytes holds 16 tokens of one
+ * key/value head. A group of 32 channels of a token shares a scale s (bf16, five
+ * significant bits); code c in 1..15 stands for (c - 8) * s, with
+ *   s = max |x| / 7 rounded up to five significant bits, at least 2^-100 and at
+ *       most 2^123 (values past 7 * 2^123 are cut there)
+ *   c = 8 + x / s rounded to nearest, halves to even
+ * so that what the cache holds are bf16 numbers. A group with a value that is
+ * not finite gets the scale NaN and reads back as NaN. A block is, in bytes,
+ *   keys    [16 tokens][4 quarters j][D/32 groups g][4]: channels 32g + 8j + 0..7
+ *   scales  [16 tokens][D/32][2]
+ *   values  [8 token pairs p][8 places][2 tokens][D/32 groups g][2]: place
+ *           (r + 2p) mod 8 has channels 32g + 8(r/2) + (r mod 2) + {0, 2, 4, 6}
+ *   scales  [8 token pairs][D/32][2 tokens][2]
+ * Four bytes hold their even channels in the lower half, the odd ones in the
+ * upper; a half is its four codes, the first lowest, rotated left by three bits.
+ *
+ * Sequences in the cache, for the three calls below:
+ *   block_table int32 [B][table_cols], rows table_stride elements apart: the page
+ *               of tokens 0..page_size-1, page_size..2*page_size-1, ... of each
+ *   lens        int64 [B]: tokens of each sequence, the new ones included
+ *   cu_seqlens  int64 [B+1]: the new tokens of sequence b are rows cu_seqlens[b]
+ *               to cu_seqlens[b+1]-1 of the call's tensors and the last ones of
+ *               its lens[b]; rows from cu_seqlens[B] on belong to no sequence and
+ *               are left as they are. NULL: one new token each, T = B
+ * A sequence of length 0 is padding: nothing is written for it, and its rows of
+ * kda_kv4_attention's out are zero. Lengths and offsets may pass 32 bits where
+ * the products of sizes do; table_cols * page_size is below 2^31.
+ * A page or length outside the cache and cu_seqlens out of order are found on
+ * the device: nothing outside the tensors is touched, the rows concerned are
+ * skipped or meaningless, and kda_sync_status reports KDA_ERR_DEVICE_CHECK.
+ * Programmatic dependent launches that wait for the kernel before them.
+ */
+size_t kda_kv4_cache_bytes(int64_t pages, int Hk, int page_size, int D);
+
+/* New keys and values k, v [T,Hk,D] dtype (tokens at strides in elements that
+ * are multiples of 16 bytes, heads contiguous) quantised into the cache. No two
+ * new tokens may share a place. */
+kda_status kda_kv4_append(const void *k, const void *v, void *cache, const int32_t *block_table,
+                          const int64_t *lens, const int64_t *cu_seqlens, int B, int64_t T, int Hk, int D,
+                          int page_size, int64_t pages, int table_cols, int64_t table_stride, int64_t k_stride,
+                          int64_t v_stride, kda_dtype dtype, kda_stream_t stream);
+
+/* What the cache holds for the last cu_seqlens[b+1] - cu_seqlens[b] tokens of
+ * each sequence (all of them, say), into k, v [T,Hk,D] dtype: exact in both
+ * types. Arguments as kda_kv4_append. */
+kda_status kda_kv4_read(const void *cache, const int32_t *block_table, const int64_t *lens,
+                        const int64_t *cu_seqlens, void *k, void *v, int B, int64_t T, int Hk, int D, int page_size,
+                        int64_t pages, int table_cols, int64_t table_stride, int64_t k_stride, int64_t v_stride,
+                        kda_dtype dtype, kda_stream_t stream);
+
+/*
+ * Softmax attention of new queries over the cache. Query head h reads key/value
+ * head h / (Hq / Hk); new token i of n stands at position lens[b] - n + i.
+ *   out = softmax(scale * q K^T + mask) V,  lse = log sum exp of the scores
+ *   q, out [T,Hq,D] dtype (token strides in elements, multiples of 16 bytes)
+ *   lse    [T,Hq] fp32 or NULL
+ *   causal 1: a query sees the tokens up to its own position; 0: all lens[b]
+ *          (the states of an encoder, say)
+ *   window > 0: only the tokens less than `window` before its position; 0: all
+ * A query that sees nothing gets zeros and lse = -infinity. Scores, maxima, sums and
+ * the output's sums are fp32. With dtype bf16 the softmax factors are rounded
+ * to bf16 for the second product; with fp32 both products take all 24 bits.
+ * A token whose keys are not finite makes the queries that see it NaN, one
+ * whose values are not finite those of its channels at least; queries that do
+ * not see it are not touched.
+ * Cached tokens are cut into equal runs for the SMs whatever the lengths, and the
+ * pieces joined in a fixed order: the same call gives the same bits.
+ *   workspace: kda_kv4_attention_workspace_bytes bytes (of the current device),
+ *   16-byte aligned; scratch, needs no clearing, not shared by calls that may overlap.
+ */
+kda_status kda_kv4_attention(const void *q, const void *cache, const int32_t *block_table, const int64_t *lens,
+                             const int64_t *cu_seqlens, void *out, float *lse, int B, int64_t T, int Hq, int Hk,
+                             int D, int page_size, int64_t pages, int table_cols, int64_t table_stride,
+                             int64_t q_stride, int64_t out_stride, float scale, int causal, int64_t window,
+                             kda_dtype dtype, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+size_t kda_kv4_attention_workspace_bytes(int B, int64_t T, int Hq, int Hk, int D, kda_dtype dtype);
+
 /* Synchronise `stream`, then report (and clear) any device-side error flag
  * raised by earlier calls on the stream's device: KDA_ERR_DEVICE_CHECK,
  * KDA_ERR_TIMEOUT, KDA_ERR_CUDA for an asynchronous CUDA error, else KDA_OK. */

@@ -189,5 +189,7 @@ extern "C" kda_status kda_sync_status(kda_stream_t stream) {
     if (word & DEVERR_TIMEOUT) return fail(KDA_ERR_TIMEOUT, "a bounded device-side wait gave up");
     if (word & DEVERR_SEQLENS)
         return fail(KDA_ERR_DEVICE_CHECK, "cu_seqlens is not non-decreasing from 0 to T; affected sequences skipped");
+    if (word & DEVERR_PAGES)
+        return fail(KDA_ERR_DEVICE_CHECK, "a sequence length or a page of the block table is outside the cache");
     return KDA_OK;
 }

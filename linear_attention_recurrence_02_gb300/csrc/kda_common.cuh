@@ -31,8 +31,8 @@ inline bool valid_head_dim(int D) { return D == 16 || D == 32 || D == 64 || D ==
 kda_status check_ptr(const void *p, const char *name);
 
 // Device-side error word (one per device): bit 0 = bad cu_seqlens,
-// bit 1 = bounded wait timed out.
-enum : unsigned { DEVERR_SEQLENS = 1u, DEVERR_TIMEOUT = 2u };
+// bit 1 = bounded wait timed out, bit 2 = a length or page outside the cache.
+enum : unsigned { DEVERR_SEQLENS = 1u, DEVERR_TIMEOUT = 2u, DEVERR_PAGES = 4u };
 unsigned *device_error_word();  // device address of the word on the current device
 
 // Device address of a file-scope __device__ variable on the current device.
@@ -61,7 +61,28 @@ inline cudaError_t smem_attr_once(int bytes) {
     return e;
 }
 
+// Programmatic dependent launch: the kernel may start while the one before it on the stream drains.
+template <typename... P, typename... A>
+inline void launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kern, args...);  // an error is left for check_launch
+}
+
 // ---------------------------------------------------------------- device side
+// Waits for the kernel before on the stream (its results are then visible), then lets the kernel behind start.
+__device__ __forceinline__ void dependent_launch() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 template <typename T> struct Elem;
 template <> struct Elem<float> {
     __device__ __forceinline__ static float load(const float *p) { return *p; }

@@ -1,6 +1,6 @@
 /*
- * kda_fastcall.c -- argument checks and calls of the 8-bit operators' Python
- * binding, as a small CPython extension.
+ * kda_fastcall.c -- argument checks and calls of the Python binding of the 8-bit
+ * operators and of the softmax-attention layers', as a small CPython extension.
  *
  * A decode step's norm or projection takes 2-4 us on the GPU, less than the
  * interpreter needs to read the shapes, types, devices and pointers of its
@@ -15,6 +15,7 @@
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <math.h>
 #include <stdint.h>
 
 typedef int (*add_rmsnorm_fn)(const void *, const void *, const float *, void *, void *, float *, int64_t, int, int,
@@ -24,11 +25,28 @@ typedef int (*gated_rmsnorm_fn)(const void *, const void *, const float *, void 
 typedef int (*linear_fn)(const void *, const float *, const void *, const float *, void *, int64_t, int, int, int64_t,
                          int64_t, int64_t, int, void *);
 
+typedef int (*norm_rope_fn)(const void *, const void *, void *, void *, const float *, const float *, const int64_t *,
+                            const double *, int64_t, int, int, int, int, int64_t, int64_t, int64_t, int64_t, int, float,
+                            int, void *);
+typedef int (*kv4_append_fn)(const void *, const void *, void *, const int32_t *, const int64_t *, const int64_t *, int,
+                             int64_t, int, int, int, int64_t, int, int64_t, int64_t, int64_t, int, void *);
+typedef int (*kv4_read_fn)(const void *, const int32_t *, const int64_t *, const int64_t *, void *, void *, int, int64_t,
+                           int, int, int, int64_t, int, int64_t, int64_t, int64_t, int, void *);
+typedef int (*kv4_attention_fn)(const void *, const void *, const int32_t *, const int64_t *, const int64_t *, void *,
+                                float *, int, int64_t, int, int, int, int, int64_t, int, int64_t, int64_t, int64_t, float,
+                                int, int64_t, int, void *, size_t, void *);
+typedef size_t (*kv4_space_fn)(int, int64_t, int, int, int, int);
+
 static struct {
     add_rmsnorm_fn add_rmsnorm;
     gated_rmsnorm_fn gated_rmsnorm;
     linear_fn linear;
-    PyObject *f32, *bf16, *f8;            /* torch dtypes */
+    norm_rope_fn norm_rope;
+    kv4_append_fn kv4_append;
+    kv4_read_fn kv4_read;
+    kv4_attention_fn kv4_attention;
+    kv4_space_fn kv4_space;
+    PyObject *f32, *bf16, *f8, *f64, *i64, *i32, *u8; /* torch dtypes */
     PyObject *get_device, *raw_stream;    /* current device index; device index -> stream handle */
     int ready;
 } S;
@@ -36,7 +54,7 @@ static struct {
 static PyObject *n_dtype, *n_shape, *n_get_device, *n_is_contiguous, *n_data_ptr, *n_stride, *n_cuda_stream,
     *n_device_index;
 
-enum { DT_F32 = 0, DT_BF16 = 1, DT_F8 = 2, DT_OTHER = -1 };
+enum { DT_F32 = 0, DT_BF16 = 1, DT_F8 = 2, DT_F64, DT_I64, DT_I32, DT_U8, DT_OTHER = -1 };
 
 typedef struct {
     int64_t dim[4];
@@ -71,7 +89,8 @@ static int look(PyObject *t, Tensor *r, int whole) {
     }
     Py_DECREF(o);
     if ((o = PyObject_GetAttr(t, n_dtype)) == NULL) return 0;
-    r->dt = o == S.f32 ? DT_F32 : o == S.bf16 ? DT_BF16 : o == S.f8 ? DT_F8 : DT_OTHER;
+    r->dt = o == S.f32 ? DT_F32 : o == S.bf16 ? DT_BF16 : o == S.f8 ? DT_F8 : o == S.i64 ? DT_I64 : o == S.i32 ? DT_I32
+          : o == S.u8 ? DT_U8 : o == S.f64 ? DT_F64 : DT_OTHER;
     Py_DECREF(o);
     long long v;
     if (!long_of(PyObject_CallMethodNoArgs(t, n_get_device), &v)) return 0;
@@ -276,23 +295,212 @@ static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return PyLong_FromLong(st);
 }
 
-/* (address of kda_add_rmsnorm_fp8, of kda_gated_rmsnorm_fp8, of kda_fp8_linear, torch.float32, torch.bfloat16,
- * torch.float8_e4m3fn, current device index (callable), device index -> stream handle (callable)) */
+/* Token stride of a [T,H,D] tensor whose heads and channels are contiguous. */
+static int token_stride(PyObject *t, const Tensor *d, int64_t *ld) {
+    PyObject *o = PyObject_CallMethodNoArgs(t, n_stride);
+    if (o == NULL) return 0;
+    int64_t st[3];
+    for (int i = 0; i < 3; ++i) st[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(o, i));
+    Py_DECREF(o);
+    if (PyErr_Occurred()) return 0;
+    if ((st[2] != 1 && d->dim[2] > 1) || (st[1] != d->dim[2] && d->dim[1] > 1)) {
+        PyErr_SetString(PyExc_ValueError, "heads must be contiguous");
+        return 0;
+    }
+    *ld = d->dim[0] > 1 ? st[0] : d->dim[1] * d->dim[2];
+    return 1;
+}
+
+/* An optional tensor: looked at where it is there; p = NULL, dev = -2 and contiguous where it is None. */
+static int look_at(PyObject *t, Tensor *r, int whole) {
+    if (t != Py_None) return look(t, r, whole);
+    *r = (Tensor){.p = NULL, .dt = DT_OTHER, .dev = -2, .contiguous = 1};
+    return 1;
+}
+/* Like one_device, skipping what is absent. */
+static int one_device_of(const Tensor *t, const Tensor *const *others, int n) {
+    const Tensor *there[12];
+    int m = 0;
+    for (int i = 0; i < n; ++i)
+        if (others[i]->dev != -2) there[m++] = others[i];
+    return one_device(t, there, m);
+}
+
+/* (q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream) */
+static PyObject *norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (!arity(n, 11)) return NULL;
+    Tensor q, k, qo, ko, pos, fr, qw, kw;
+    if (!look(a[0], &q, 0) || !look_at(a[1], &k, 0) || !look(a[2], &qo, 0) || !look_at(a[3], &ko, 0) ||
+        !look_at(a[4], &pos, 1) || !look_at(a[5], &fr, 1) || !look_at(a[6], &qw, 1) || !look_at(a[7], &kw, 1))
+        return NULL;
+    const int has_k = a[1] != Py_None, turns = a[5] != Py_None;
+    if (has_k != (a[3] != Py_None) || turns != (a[4] != Py_None))
+        return bad(PyExc_ValueError, "k and k_out, positions and inv_freq go together");
+    if (q.nd != 3 || (has_k && k.nd != 3)) return bad(PyExc_ValueError, SHAPE);
+    const int64_t T = q.dim[0], Hq = q.dim[1], D = q.dim[2], Hk = has_k ? k.dim[1] : 0, R = turns ? 2 * fr.dim[0] : 0;
+    if (!is_shape(&qo, 3, T, Hq, D) || (has_k && (!is_shape(&k, 3, T, Hk, D) || !is_shape(&ko, 3, T, Hk, D))) ||
+        (turns && (fr.nd != 1 || !is_shape(&pos, 1, T, 0, 0))) || (a[6] != Py_None && !is_shape(&qw, 1, D, 0, 0)) ||
+        (a[7] != Py_None && !is_shape(&kw, 1, D, 0, 0)) || Hq > INT32_MAX || Hk > INT32_MAX || D > INT32_MAX ||
+        R > INT32_MAX)
+        return bad(PyExc_ValueError, SHAPE);
+    if (qo.dt != q.dt || (has_k && (k.dt != q.dt || ko.dt != q.dt)))
+        return bad(PyExc_TypeError, "q, k and the outputs must have one dtype");
+    if (q.dt != DT_F32 && q.dt != DT_BF16) return bad(PyExc_TypeError, DTYPE);
+    if (turns && pos.dt != DT_I64) return bad(PyExc_TypeError, "positions must be int64");
+    if (turns && fr.dt != DT_F64) return bad(PyExc_TypeError, "inv_freq must be float64");
+    if ((a[6] != Py_None && qw.dt != DT_F32) || (a[7] != Py_None && kw.dt != DT_F32)) return bad(PyExc_TypeError, FLOATS);
+    const Tensor *others[] = {&k, &qo, &ko, &pos, &fr, &qw, &kw};
+    if (!one_device_of(&q, others, 7)) return NULL;
+    int64_t ld[4] = {0, 0, 0, 0};
+    if (!token_stride(a[0], &q, ld) || (has_k && !token_stride(a[1], &k, ld + 1)) || !token_stride(a[2], &qo, ld + 2) ||
+        (has_k && !token_stride(a[3], &ko, ld + 3)))
+        return NULL;
+    const double eps = PyFloat_AsDouble(a[8]);
+    if (eps == -1.0 && PyErr_Occurred()) return NULL;
+    const int inter = PyObject_IsTrue(a[9]);
+    if (inter < 0) return NULL;
+    void *h = NULL;
+    const int found = find_stream(a[10], q.dev, &h);
+    if (found == 0) return NULL;
+    if (found < 0) return PyLong_FromLong(-1);
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = S.norm_rope(q.p, k.p, qo.p, ko.p, qw.p, kw.p, pos.p, fr.p, T, (int)Hq, (int)Hk, (int)D, (int)R, ld[0], ld[1], ld[2],
+                     ld[3], inter, (float)eps, q.dt, h);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* A cache, the sequences in it and a tensor x [T,H,D] of new tokens. */
+typedef struct {
+    Tensor cache, table, lens, cu;
+    int64_t B, T, Hk, D, pages, cols, table_stride;
+    int page;
+} Cached;
+
+static int look_cached(PyObject *cache, PyObject *table, PyObject *lens, PyObject *cu, const Tensor *x, Cached *c) {
+    if (!look(cache, &c->cache, 1) || !look(table, &c->table, 0) || !look(lens, &c->lens, 1) || !look_at(cu, &c->cu, 1))
+        return 0;
+    if (c->cache.nd != 4 || c->table.nd != 2 || c->lens.nd != 1 || x->nd != 3) return bad(PyExc_ValueError, SHAPE) != NULL;
+    c->pages = c->cache.dim[0];
+    c->Hk = c->cache.dim[1];
+    c->B = c->lens.dim[0];
+    c->T = x->dim[0];
+    c->D = x->dim[2];
+    c->cols = c->table.dim[1];
+    if (c->cache.dim[3] != 18 * c->D || c->table.dim[0] != c->B || (cu != Py_None && !is_shape(&c->cu, 1, c->B + 1, 0, 0)) ||
+        c->Hk > INT32_MAX || c->D > INT32_MAX || c->B > INT32_MAX || c->cols > INT32_MAX || c->cache.dim[2] > 1 << 20 ||
+        x->dim[1] > INT32_MAX)
+        return bad(PyExc_ValueError, SHAPE) != NULL;
+    c->page = 16 * (int)c->cache.dim[2];
+    if (c->cache.dt != DT_U8) return bad(PyExc_TypeError, "cache must be uint8") != NULL;
+    if (c->table.dt != DT_I32) return bad(PyExc_TypeError, "block_table must be int32") != NULL;
+    if (c->lens.dt != DT_I64 || (cu != Py_None && c->cu.dt != DT_I64))
+        return bad(PyExc_TypeError, "lens and cu_seqlens must be int64") != NULL;
+    if (x->dt != DT_F32 && x->dt != DT_BF16) return bad(PyExc_TypeError, DTYPE) != NULL;
+    return row_stride(table, &c->table, &c->table_stride);
+}
+
+/* (k, v, cache, block_table, lens, cu_seqlens, stream, read) */
+static PyObject *kv4_rows(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (!arity(n, 8)) return NULL;
+    Tensor k, v;
+    Cached c;
+    if (!look(a[0], &k, 0) || !look(a[1], &v, 0) || !look_cached(a[2], a[3], a[4], a[5], &k, &c)) return NULL;
+    if (k.dim[1] != c.Hk || !is_shape(&v, 3, k.dim[0], k.dim[1], k.dim[2])) return bad(PyExc_ValueError, SHAPE);
+    if (k.dt != v.dt) return bad(PyExc_TypeError, "k and v must have one dtype");
+    const Tensor *others[] = {&v, &c.cache, &c.table, &c.lens, &c.cu};
+    if (!one_device_of(&k, others, 5)) return NULL;
+    int64_t ks, vs;
+    if (!token_stride(a[0], &k, &ks) || !token_stride(a[1], &v, &vs)) return NULL;
+    void *h = NULL;
+    const int found = find_stream(a[6], k.dev, &h);
+    if (found == 0) return NULL;
+    if (found < 0) return PyLong_FromLong(-1);
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    if (a[7] == Py_True)
+        st = S.kv4_read(c.cache.p, c.table.p, c.lens.p, c.cu.p, k.p, v.p, (int)c.B, c.T, (int)c.Hk, (int)c.D, c.page, c.pages,
+                        (int)c.cols, c.table_stride, ks, vs, k.dt, h);
+    else
+        st = S.kv4_append(k.p, v.p, c.cache.p, c.table.p, c.lens.p, c.cu.p, (int)c.B, c.T, (int)c.Hk, (int)c.D, c.page,
+                          c.pages, (int)c.cols, c.table_stride, ks, vs, k.dt, h);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* (q, cache, block_table, lens, out, cu_seqlens, scale or None, causal, window, lse, workspace, stream). With no
+ * workspace where one is needed: its size as a negative number below -1. */
+static PyObject *kv4_attention(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (!arity(n, 12)) return NULL;
+    Tensor q, out, lse, ws;
+    Cached c;
+    if (!look(a[0], &q, 0) || !look(a[4], &out, 0) || !look_at(a[9], &lse, 1) || !look_at(a[10], &ws, 1) ||
+        !look_cached(a[1], a[2], a[3], a[5], &q, &c))
+        return NULL;
+    const int64_t Hq = q.dim[1];
+    if (!is_shape(&out, 3, c.T, Hq, c.D) || (a[9] != Py_None && !is_shape(&lse, 2, c.T, Hq, 0)))
+        return bad(PyExc_ValueError, SHAPE);
+    if (out.dt != q.dt) return bad(PyExc_TypeError, "out must have q's dtype");
+    if (a[9] != Py_None && lse.dt != DT_F32) return bad(PyExc_TypeError, "lse must be float32");
+    if (a[10] != Py_None && ws.dt != DT_U8) return bad(PyExc_TypeError, "workspace must be uint8");
+    const Tensor *others[] = {&out, &lse, &ws, &c.cache, &c.table, &c.lens, &c.cu};
+    if (!one_device_of(&q, others, 7)) return NULL;
+    int64_t qs, os;
+    if (!token_stride(a[0], &q, &qs) || !token_stride(a[4], &out, &os)) return NULL;
+    const double scale = a[6] == Py_None ? 1.0 / sqrt((double)c.D) : PyFloat_AsDouble(a[6]);
+    if (scale == -1.0 && PyErr_Occurred()) return NULL;
+    const int causal = PyObject_IsTrue(a[7]);
+    if (causal < 0) return NULL;
+    const int64_t window = PyLong_AsLongLong(a[8]);
+    if (window == -1 && PyErr_Occurred()) return NULL;
+    void *h = NULL;
+    const int found = find_stream(a[11], q.dev, &h);
+    if (found == 0) return NULL;
+    if (found < 0) return PyLong_FromLong(-1);
+    size_t size = 1;
+    if (a[10] == Py_None) {
+        const size_t need = S.kv4_space((int)c.B, c.T, (int)Hq, (int)c.Hk, (int)c.D, q.dt);
+        if (need > 0) return PyLong_FromLongLong(-(long long)need);
+        size = 0;
+    }
+    for (int i = 0; a[10] != Py_None && i < ws.nd; ++i) size *= (size_t)ws.dim[i];
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = S.kv4_attention(q.p, c.cache.p, c.table.p, c.lens.p, c.cu.p, out.p, lse.p, (int)c.B, c.T, (int)Hq, (int)c.Hk,
+                         (int)c.D, c.page, c.pages, (int)c.cols, c.table_stride, qs, os, (float)scale, causal, window, q.dt,
+                         ws.p, size, h);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* (addresses of kda_add_rmsnorm_fp8, kda_gated_rmsnorm_fp8, kda_fp8_linear, kda_qk_norm_rope, kda_kv4_append,
+ * kda_kv4_read, kda_kv4_attention, kda_kv4_attention_workspace_bytes; torch's float32, bfloat16, float8_e4m3fn,
+ * float64, int64, int32, uint8; current device index (callable), device index -> stream handle (callable)) */
 static PyObject *setup(PyObject *self, PyObject *args) {
     (void)self;
-    PyObject *p[3], *o[5];
-    if (!PyArg_ParseTuple(args, "OOOOOOOO", &p[0], &p[1], &p[2], &o[0], &o[1], &o[2], &o[3], &o[4])) return NULL;
-    void *f[3];
-    for (int i = 0; i < 3; ++i)
-        if ((f[i] = PyLong_AsVoidPtr(p[i])) == NULL)
+    enum { FNS = 8, OBJECTS = 9 };
+    PyObject **slot[OBJECTS] = {&S.f32, &S.bf16, &S.f8, &S.f64, &S.i64, &S.i32, &S.u8, &S.get_device, &S.raw_stream};
+    if (PyTuple_GET_SIZE(args) != FNS + OBJECTS) return bad(PyExc_TypeError, "wrong number of arguments");
+    void *f[FNS];
+    for (int i = 0; i < FNS; ++i)
+        if ((f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(args, i))) == NULL)
             return PyErr_Occurred() ? NULL : bad(PyExc_ValueError, "a function's address is NULL");
     S.add_rmsnorm = (add_rmsnorm_fn)f[0];
     S.gated_rmsnorm = (gated_rmsnorm_fn)f[1];
     S.linear = (linear_fn)f[2];
-    PyObject **slot[5] = {&S.f32, &S.bf16, &S.f8, &S.get_device, &S.raw_stream};
-    for (int i = 0; i < 5; ++i) {
-        Py_INCREF(o[i]);
-        Py_XSETREF(*slot[i], o[i]);
+    S.norm_rope = (norm_rope_fn)f[3];
+    S.kv4_append = (kv4_append_fn)f[4];
+    S.kv4_read = (kv4_read_fn)f[5];
+    S.kv4_attention = (kv4_attention_fn)f[6];
+    S.kv4_space = (kv4_space_fn)f[7];
+    for (int i = 0; i < OBJECTS; ++i) {
+        PyObject *o = PyTuple_GET_ITEM(args, FNS + i);
+        Py_INCREF(o);
+        Py_XSETREF(*slot[i], o);
     }
     S.ready = 1;
     Py_RETURN_NONE;
@@ -303,6 +511,9 @@ static PyMethodDef methods[] = {
     {"add_rmsnorm", (PyCFunction)(void (*)(void))add_rmsnorm, METH_FASTCALL, "kda_add_rmsnorm_fp8"},
     {"gated_rmsnorm", (PyCFunction)(void (*)(void))gated_rmsnorm, METH_FASTCALL, "kda_gated_rmsnorm_fp8"},
     {"linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, "kda_fp8_linear"},
+    {"norm_rope", (PyCFunction)(void (*)(void))norm_rope, METH_FASTCALL, "kda_qk_norm_rope"},
+    {"kv4_rows", (PyCFunction)(void (*)(void))kv4_rows, METH_FASTCALL, "kda_kv4_append and kda_kv4_read"},
+    {"kv4_attention", (PyCFunction)(void (*)(void))kv4_attention, METH_FASTCALL, "kda_kv4_attention"},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "kda_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -22,22 +22,6 @@ namespace kda {
 // Both are programmatic dependent launches that wait for the kernel before
 // them first thing, then let the kernel behind them start: a kda_fp8_linear
 // that reads their output sets itself up and prefetches its weights meanwhile.
-__device__ __forceinline__ void dependent_launch() {
-    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
-}
-template <typename... P, typename... A>
-static void launch_dependent(void (*kern)(P...), unsigned grid, dim3 block, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = block;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kern, args...);  // an error is left for check_launch
-}
 
 // ---------------------------------------------------------------- residual add + RMSNorm
 // A row of N channels is held by blockDim.x threads, VPT vectors of 8
@@ -137,7 +121,7 @@ static kda_status launch_add(const void *x, const void *res, const float *w, voi
     const int64_t blocks = (T + rows - 1) / rows;
     if (blocks > 0x7fffffffLL) return invalid("T too large for one launch");
     auto go = [&](auto kern) {
-        launch_dependent(kern, (unsigned)blocks, dim3((unsigned)nt, (unsigned)rows), s, static_cast<const TX *>(x),
+        launch_dependent(kern, dim3((unsigned)blocks), dim3((unsigned)nt, (unsigned)rows), 0, s, static_cast<const TX *>(x),
                          static_cast<const TR *>(res), w, static_cast<TR *>(sum_out), static_cast<uint8_t *>(y),
                          scales, T, N, 1.0f / (float)N, eps);
     };
@@ -269,7 +253,7 @@ static kda_status dispatch_gated(int D, const void *o, const void *gate, const f
     const int64_t blocks = (Ttot * nb + GATED_NT / 8 - 1) / (GATED_NT / 8);
     if (blocks > 0x7fffffffLL) return invalid("T*H*D too large for one launch");
     auto go = [&](auto kern) {
-        launch_dependent(kern, (unsigned)blocks, dim3(GATED_NT), s, static_cast<const T *>(o), static_cast<const T *>(gate),
+        launch_dependent(kern, dim3((unsigned)blocks), dim3(GATED_NT), 0, s, static_cast<const T *>(o), static_cast<const T *>(gate),
                          w, static_cast<uint8_t *>(y), scales, Ttot, C, nb, eps);
     };
     switch (D) {

@@ -95,6 +95,13 @@ _SIGNATURES = {
                                _cf, _vp, _vp, _ci, _cf, _vp, _sz, _vp], _ci),
     "kda_chunk_prefill_scan": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _ci, _ci, _cf, _ci,
                                 _vp, _sz, _vp], _ci),
+    "kda_qk_norm_rope": ([_vp] * 8 + [_i64, _ci, _ci, _ci, _ci, _i64, _i64, _i64, _i64, _ci, _cf, _ci, _vp], _ci),
+    "kda_kv4_cache_bytes": ([_i64, _ci, _ci, _ci], _sz),
+    "kda_kv4_append": ([_vp] * 6 + [_ci, _i64, _ci, _ci, _ci, _i64, _ci, _i64, _i64, _i64, _ci, _vp], _ci),
+    "kda_kv4_read": ([_vp] * 6 + [_ci, _i64, _ci, _ci, _ci, _i64, _ci, _i64, _i64, _i64, _ci, _vp], _ci),
+    "kda_kv4_attention": ([_vp] * 7 + [_ci, _i64, _ci, _ci, _ci, _ci, _i64, _ci, _i64, _i64, _i64, _cf, _ci, _i64, _ci,
+                                       _vp, _sz, _vp], _ci),
+    "kda_kv4_attention_workspace_bytes": ([_ci, _i64, _ci, _ci, _ci, _ci], _sz),
     "kda_sync_status": ([_vp], _ci),
     "kda_selftest_bounded_wait": ([ctypes.c_longlong, _vp], _ci),
 }
@@ -323,7 +330,8 @@ _calls = None
 
 
 def _fastcall():
-    """The extension that checks the 8-bit operators' tensors and calls the library (raises if not built)."""
+    """The extension that checks the tensors of the 8-bit operators and of the softmax-attention layers' and calls the
+    library (raises if not built)."""
     global _calls
     if _calls is None:
         import importlib.machinery
@@ -338,11 +346,12 @@ def _fastcall():
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         handle = lib()
-        mod.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in (handle.kda_add_rmsnorm_fp8,
-                                                                     handle.kda_gated_rmsnorm_fp8,
-                                                                     handle.kda_fp8_linear)),
-                  torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch._C._cuda_getDevice,
-                  torch._C._cuda_getCurrentRawStream)
+        mod.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                      handle.kda_add_rmsnorm_fp8, handle.kda_gated_rmsnorm_fp8, handle.kda_fp8_linear,
+                      handle.kda_qk_norm_rope, handle.kda_kv4_append, handle.kda_kv4_read, handle.kda_kv4_attention,
+                      handle.kda_kv4_attention_workspace_bytes)),
+                  torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.float64, torch.int64, torch.int32, torch.uint8,
+                  torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
         _calls = mod
     return _calls
 
@@ -635,6 +644,75 @@ def kda_chunk_prefill_noalloc(q, k, v, g, beta, out, initial_state=None, final_s
     _check(lib().kda_chunk_prefill_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
                                            _ptr(final_state), _ptr(out), _ptr(cu_seqlens), N, T, H, D, chunk_size,
                                            _dtype_code(q), float(l2_eps), _stream(stream, q.device)))
+
+
+def kda_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, stream=None):
+    """RMSNorm of every query and key head (skipped where its weight is None) and the rotation of the first
+    2 * len(inv_freq) channels by positions * inv_freq. q [T,Hq,D], k [T,Hk,D] and the outputs: heads contiguous,
+    any token stride; k and k_out may be None; q_out may be q, k_out k. positions int64 [T] and inv_freq fp64 [R/2]
+    (both None: no rotation); weights [D] fp32. interleaved: pairs are neighbouring channels, else i and i + R/2."""
+    fn = (_calls or _fastcall()).norm_rope
+    args = (q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream)
+    status = fn(*args)
+    if status:
+        _settle(status, fn, q.device, *args)
+
+
+def kda_kv4_cache_bytes(pages, Hk, page_size, D) -> int:
+    return int(lib().kda_kv4_cache_bytes(pages, Hk, page_size, D))
+
+
+def kda_kv4_cache_shape(pages, Hk, page_size, D):
+    """Shape of the uint8 tensor that holds `pages` pages of page_size tokens of Hk key/value heads."""
+    return pages, Hk, page_size // 16, 18 * D
+
+
+def kda_kv4_append(k, v, cache, block_table, lens, cu_seqlens=None, stream=None):
+    """Quantise new keys and values k, v [T,Hk,D] (heads contiguous, any token stride) into the 4-bit cache (uint8
+    [pages,Hk,page_size/16,18*D]). block_table int32 [B,cols]; lens int64 [B] counts the new tokens; cu_seqlens int64
+    [B+1] (None: one new token for each sequence): the new tokens are the last ones of each sequence."""
+    fn = (_calls or _fastcall()).kv4_rows
+    status = fn(k, v, cache, block_table, lens, cu_seqlens, stream, False)
+    if status:
+        _settle(status, fn, k.device, k, v, cache, block_table, lens, cu_seqlens, stream, False)
+
+
+def kda_kv4_read(cache, block_table, lens, k, v, cu_seqlens=None, stream=None):
+    """What the cache holds for the last cu_seqlens[b+1] - cu_seqlens[b] tokens of each sequence, into k, v
+    [T,Hk,D]. Arguments as kda_kv4_append."""
+    fn = (_calls or _fastcall()).kv4_rows
+    status = fn(k, v, cache, block_table, lens, cu_seqlens, stream, True)
+    if status:
+        _settle(status, fn, k.device, k, v, cache, block_table, lens, cu_seqlens, stream, True)
+
+
+def kda_kv4_attention(q, cache, block_table, lens, out, cu_seqlens=None, scale=None, causal=True, window=0, lse=None,
+                      workspace=None, stream=None):
+    """out = softmax(scale q K^T + mask) V over the 4-bit cache for new queries q [T,Hq,D] (heads contiguous, any token
+    stride; out alike), Hq a multiple of the cache's heads. scale: 1/sqrt(D) when None. causal: a query sees the tokens
+    up to its own position, else all of lens[b]; window > 0: only the last `window` of them. lse [T,Hq] fp32 or None
+    receives the log of the sum of exponentials. workspace: a device uint8 tensor of
+    kda_kv4_attention_workspace_bytes (allocated here when None); other arguments as kda_kv4_append."""
+    fn = (_calls or _fastcall()).kv4_attention
+    args = (q, cache, block_table, lens, out, cu_seqlens, scale, causal, window, lse)
+    status = fn(*args, workspace, stream)
+    if status == -1:
+        with _current(q.device):
+            return kda_kv4_attention(*args[:6], scale=scale, causal=causal, window=window, lse=lse, workspace=workspace,
+                                     stream=stream)
+    if status < -1:
+        workspace, _ = _scratch(None, -status, q.device, stream)
+        status = fn(*args, workspace, stream)
+    if status:
+        _check(status)
+
+
+def kda_kv4_attention_workspace_bytes(B, T, Hq, Hk, D, dtype) -> int:
+    """Workspace of kda_kv4_attention for B sequences and T new tokens; dtype torch.bfloat16 or torch.float32."""
+    import torch
+    code = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}[dtype]
+    return int(lib().kda_kv4_attention_workspace_bytes(B, T, Hq, Hk, D, code))
 
 
 def kda_selftest_bounded_wait(limit_cycles=2_000_000, stream=None, device=None):
