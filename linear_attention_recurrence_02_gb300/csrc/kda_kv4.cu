@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(NT) kv4_read_kernel(Cache c, T *k, T *v, int64
     int64_t pos = 0;
     if (t < c.T && token_place(c, t, b, pos)) page = page_of(c, b, pos, err);
     const int in_page = (int)(pos & ((1 << c.page_shift) - 1)), tt = in_page & (BLOCK - 1);
+    const Expand expand;
     uint32_t word[HU][2], scale[HU][2];
 #pragma unroll
     for (int u = 0; u < HU; ++u) {

@@ -43,14 +43,25 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 
 // ---------------------------------------------------------------- expanding
 // A word's eight codes as four pairs of bf16: f[i] = 16 + the codes of channels 2i and 2i + 1.
-// `swapped` is the word with the bytes of each half exchanged.
-__device__ __forceinline__ void codes16(uint32_t w, uint32_t swapped, uint32_t (&f)[4]) {
-    constexpr uint32_t MASK = 0x00780078u, BASE = 0x41804180u;
-    f[0] = (w & MASK) | BASE;
-    f[1] = ((w >> 4) & MASK) | BASE;
-    f[2] = (swapped & MASK) | BASE;
-    f[3] = ((swapped >> 4) & MASK) | BASE;
-}
+// `swapped` is the word with the bytes of each half exchanged. One of the two constants is hidden from the
+// compiler, which otherwise puts both into instructions: an instruction holds one, so that masking and
+// joining take two instead of one.
+struct Expand {
+    uint32_t base;
+    __device__ __forceinline__ Expand() { asm volatile("mov.b32 %0, 0x41804180;" : "=r"(base)); }
+    __device__ __forceinline__ uint32_t join(uint32_t x) const {
+        uint32_t r;
+        asm("lop3.b32 %0, %1, 0x00780078, %2, 0xea;" : "=r"(r) : "r"(x), "r"(base));  // (x & mask) | base
+        return r;
+    }
+    __device__ __forceinline__ void codes16(uint32_t w, uint32_t swapped, uint32_t (&f)[4]) const {
+        f[0] = join(w);
+        f[1] = join(w >> 4);
+        f[2] = join(swapped);
+        f[3] = join(swapped >> 4);
+    }
+    __device__ __forceinline__ void operator()(uint32_t w, uint32_t swapped, uint32_t s2, uint32_t n2, uint32_t (&f)[4]) const;
+};
 __device__ __forceinline__ uint32_t swap_bytes(uint32_t w) { return prmt(w, 0, 0x2301); }
 
 // (16 + c) s - 24 s, exact: 24 s has seven significant bits, the result at most eight.
@@ -64,7 +75,8 @@ __device__ __forceinline__ uint32_t minus24(uint32_t s2) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(s2), "r"(0xC1C0C1C0u));
     return d;
 }
-__device__ __forceinline__ void expand(uint32_t w, uint32_t swapped, uint32_t s2, uint32_t n2, uint32_t (&f)[4]) {
+__device__ __forceinline__ void Expand::operator()(uint32_t w, uint32_t swapped, uint32_t s2, uint32_t n2,
+                                                   uint32_t (&f)[4]) const {
     codes16(w, swapped, f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = fma_bf16x2(f[i], s2, n2);

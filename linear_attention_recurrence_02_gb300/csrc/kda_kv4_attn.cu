@@ -13,8 +13,9 @@
 // tcgen05 takes its operands from shared memory or TMEM, where expanded codes would have to be written
 // first: at the rate at which HBM delivers codes that alone is about all that shared memory can write.
 //
-// Each warp is on its own: it takes every fourth tile of 32 tokens of the CTA's run, brings its tiles in
-// by bulk copies through a ring of three, and keeps a running maximum and sum (moved only when a score passes the
+// Each warp is on its own: it takes every fourth tile of 64 tokens of the CTA's run, brings its tiles in
+// through a ring of two (by 16-byte asynchronous copies of all lanes: a bulk copy's issue by one lane, its
+// barrier and the wait on it took as many issue slots as a third of the tile's arithmetic), and keeps a running maximum and sum (moved only when a score passes the
 // maximum by 2^8: the factors stay in range and most tiles rescale nothing). At an item's end the four
 // warps' results are joined through shared memory.
 #include <algorithm>
@@ -28,26 +29,35 @@
 namespace kda {
 namespace kv4 {
 
-constexpr int WARPS = 4, STAGES = 3, TILE = 32;
-constexpr long long WAIT_LIMIT_KV4 = 2000000000LL;  // clock cycles (about 1 s)
+constexpr int WARPS = 4, STAGES = 2, TILE = 64, BLOCKS = TILE / BLOCK;
 constexpr float SLACK = 8.f;  // log2 of how far scores may pass the running maximum before it moves
 
-template <int D, int NTL> struct FewSmem {
-    static constexpr int R = 8 * NTL, STAGE = 2 * Format<D>::BYTES;
+// Where the run's computing (one for the CTA) and its copies (one a warp) stand. In shared memory, because
+// they are needed once an item and would fill forty registers.
+struct Places {
+    Walk walk, ahead[WARPS];
+    Segment seg[2], copied[WARPS];
+};
+
+template <int D, int NTL, int QS> struct FewSmem {
+    static constexpr int R = 8 * NTL, STAGE = BLOCKS * Format<D>::BYTES;
     static constexpr int RING = WARPS * STAGES * STAGE;
-    static constexpr int SUM = RING, ML = SUM + WARPS * 8 * (D + 1) * 4, BAR = ML + WARPS * R * 8;
-    static constexpr int BYTES = BAR + WARPS * STAGES * 8;
+    static constexpr int RAW = NTL * (D / 32) * 512 * (QS == 1 ? 1 : 2);  // an item's rows of q, [2] of them
+    static constexpr int Q = RING, SPLIT = Q + 2 * RAW, ZERO = SPLIT + (QS == 1 ? 0 : NTL * (D / 32) * QS * 512);
+    static constexpr int SUM = ZERO + NTL * (D / 32) * 64;
+    static constexpr int ML = SUM + WARPS * 8 * 65 * 4;
+    static constexpr int PLACES = ML + WARPS * R * 8, BYTES = PLACES + (int)sizeof(Places);
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -76,125 +86,190 @@ template <int N> __device__ __forceinline__ void lds(uint32_t (&w)[N], const uin
     }
 }
 
-// A warp's copies: walks the CTA's run ahead of the computing, tile by tile.
+// A warp's copies: walks the CTA's run ahead of the computing, tile by tile. The pages of the next tile are
+// looked up when the one before it is asked for, so that no copy waits for a lookup.
 template <int D, int R> struct Loader {
-    Walk w;
-    Segment g;
-    int tile;
-    bool more;
+    Walk *w;
+    Segment *g;
+    const int32_t *row;  // of the block table
+    int tile, last, h, page;  // page: lane l's is that of block l of the tile
+    bool more, bad;
 
-    __device__ __forceinline__ void start(const AttnArgs &a, const Walk &from, int warp) {
-        w = from;
-        more = next_segment<R, TILE>(a, w, g);
-        tile = g.first + warp;
-        settle(a, warp);
+    // All lanes: on to the run's next item that has a tile for this warp.
+    __device__ __forceinline__ void next_item(const AttnArgs &a, int warp, int lane) {
+        do {
+            if (lane == 0) next_segment<R, TILE>(a, *w, *g);
+            __syncwarp();
+            more = g->there;
+            row = a.c.table + g->b * a.c.table_stride;
+            tile = g->first + warp;
+            last = g->last;
+            h = g->h;
+            __syncwarp();
+        } while (more && tile >= last);
+        if (more) look(a, lane);
     }
-    __device__ __forceinline__ void settle(const AttnArgs &a, int warp) {
-        while (more && tile >= g.last) {
-            more = next_segment<R, TILE>(a, w, g);
-            tile = g.first + warp;
-        }
+    // Blocks behind the sequence's last token, whose page need not exist, are read from the tile's first page.
+    __device__ __forceinline__ void look(const AttnArgs &a, int lane) {
+        const int at = BLOCK * (lane & (BLOCKS - 1));
+        page = row[(tile * TILE + (tile * TILE + at < g->len ? at : 0)) >> a.c.page_shift];
     }
-    // Lane 0: the copies of the next tile into `dst`; a page outside the cache is flagged and read as page 0.
-    __device__ __forceinline__ void issue(const AttnArgs &a, uint8_t *dst, uint64_t *bar) const {
-        constexpr int BYTES = Format<D>::BYTES;
-        const int sh = a.c.page_shift, in_page = (1 << sh) - 1;
-        const int tok = tile * TILE, copies = sh == 4 ? (tok + 16 < g.len ? 2 : 1) : 1;
-        const uint32_t bytes = sh == 4 ? BYTES : 2 * BYTES;
-        tc::mbar_arrive_expect_tx(bar, bytes * copies);
-        for (int i = 0; i < copies; ++i) {
-            const int at = tok + 16 * i;
-            int page = a.c.table[g.b * a.c.table_stride + (at >> sh)];
-            if (page < 0 || page >= a.c.pages) {
-                atomicOr(a.err, DEVERR_PAGES);
-                page = 0;
+    // Where a block of the page that stands for it begins; a page outside the cache is read as page 0 and flagged
+    // at the end.
+    __device__ __forceinline__ const uint8_t *block_at(const AttnArgs &a, int p, int block) {
+        const bool out = (uint32_t)p >= (uint32_t)a.c.pages;
+        bad |= out;
+        return a.c.data + ((((int64_t)(out ? 0 : p) * a.c.Hk + h) << (a.c.page_shift - 4)) + block) * Format<D>::BYTES;
+    }
+    // The copies of the tile into `to` (a shared memory address), 16 bytes a lane at a time, and on to the next.
+    __device__ __forceinline__ void issue(const AttnArgs &a, uint32_t to, int warp, int lane) {
+        constexpr int BYTES = Format<D>::BYTES, CHUNKS = BYTES / 16;
+        to += 16 * lane;
+        const int in_page = (1 << (a.c.page_shift - 4)) - 1;
+        if ((1 << a.c.page_shift) >= TILE) {  // one page
+            const uint8_t *src = block_at(a, __shfl_sync(0xffffffffu, page, 0), BLOCKS * tile & in_page) + 16 * lane;
+#pragma unroll
+            for (int k = 0; k < (BLOCKS * CHUNKS + 31) / 32; ++k)
+                if (BLOCKS * CHUNKS % 32 == 0 || 32 * k + lane < BLOCKS * CHUNKS)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * k), "l"(src + 512 * k)
+                                 : "memory");
+        } else {
+            for (int i = 0; i < BLOCKS; ++i) {
+                const uint8_t *src = block_at(a, __shfl_sync(0xffffffffu, page, i), (BLOCKS * tile + i) & in_page) + 16 * lane;
+#pragma unroll
+                for (int k = 0; k < (CHUNKS + 31) / 32; ++k)
+                    if (32 * k + lane < CHUNKS)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * BYTES + 512 * k),
+                                     "l"(src + 512 * k)
+                                     : "memory");
             }
-            const int64_t block = ((((int64_t)page * a.c.Hk + g.h) << (sh - 4)) + ((at & in_page) >> 4));
-            tc::bulk_load(dst + i * BYTES, a.c.data + block * BYTES, bytes, bar);
         }
-    }
-    __device__ __forceinline__ void advance(const AttnArgs &a, int warp) {
         tile += WARPS;
-        settle(a, warp);
+        if (tile < last) look(a, lane);
+        else next_item(a, warp, lane);
     }
 };
 
+// CTAs of an SM: as many as registers (without spills) and shared memory allow.
+constexpr int few_per_sm(int D) { return D == 64 ? 3 : 2; }
+
 template <int D, typename T, int NTL>
-__global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __grid_constant__ AttnArgs a) {
-    using Sm = FewSmem<D, NTL>;
-    constexpr int R = Sm::R, G = D / 32, QS = sizeof(T) == 4 ? 3 : 1, BYTES = Format<D>::BYTES;
+__global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int G = D / 32, QS = sizeof(T) == 4 ? 3 : 1, BYTES = Format<D>::BYTES;
+    using Sm = FewSmem<D, NTL, QS>;
+    constexpr int R = Sm::R;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+    const Expand expand;
     uint8_t *ring = smem + warp * STAGES * Sm::STAGE;
     float *sum = reinterpret_cast<float *>(smem + Sm::SUM);
     float2 *ml = reinterpret_cast<float2 *>(smem + Sm::ML);
-    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Sm::BAR) + warp * STAGES;
-    if (lane == 0) {
-        for (int i = 0; i < STAGES; ++i) tc::mbar_init(bar + i, 1);
-        tc::fence_mbar_init();
-    }
-    __syncwarp();
+    float4 *zero = reinterpret_cast<float4 *>(smem + Sm::ZERO);
     dependent_launch();
 
     const int64_t total = line_tiles<R, TILE>(a, lane), run = run_length(total, a.ctas, WARPS);
     const int64_t start = blockIdx.x * run;
+    if (threadIdx.x == 0) a.joint[blockIdx.x].pieces = 0;
     if (start >= total) return;  // the whole CTA
-    Walk w = walk_at<R, TILE>(a, start, lane);
-    w.left = min(run, total - start);
-    Loader<D, R> ld;
-    ld.start(a, w, warp);
-    int issued = 0;
-    for (; issued < STAGES && ld.more; ++issued) {
-        if (lane == 0) ld.issue(a, ring + issued * Sm::STAGE, bar + issued);
-        ld.advance(a, warp);
+    Places *at = reinterpret_cast<Places *>(smem + Sm::PLACES);
+    {
+        Walk w = walk_at<R, TILE>(a, start, lane);
+        w.left = min(run, total - start);
+        if (lane == 0) {
+            at->ahead[warp] = w;
+            if (warp == 0) {
+                next_segment<R, TILE>(a, w, at->seg[0]);
+                at->walk = w;
+            }
+        }
     }
+    __syncthreads();
+    Loader<D, R> ld;
+    ld.w = at->ahead + warp;
+    ld.g = at->copied + warp;
+    ld.bad = false;
+    ld.next_item(a, warp, lane);
+    const uint32_t ring_at = tc::smem_u32(ring);
+    auto copy_next = [&](uint32_t dst) {  // one group a tile, an empty one behind the run's end
+        if (ld.more) ld.issue(a, dst, warp, lane);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < STAGES; ++i) copy_next(ring_at + i * Sm::STAGE);
 
-    int stage = 0, phase = 0, inflight = issued;
-    bool ok = true;
-    Segment g;
-    while (next_segment<R, TILE>(a, w, g)) {
-        // this lane's rows as the operand's column r, and its two columns 2j, 2j + 1 of the accumulators
-        uint32_t qf[NTL][G][4][QS];
+    // An item's rows of q on their way: lane (r, j) has channels 32g + 8j + 0..7 of row r. Zeros for rows that the
+    // last block does not have.
+    auto copy_rows = [&](const Segment &g, uint8_t *dst) {
+        for (int x = warp; x < NTL * G; x += WARPS) {
+            const int nt = x / G, gr = x % G, rr = g.block * R + nt * 8 + r, i = a.by_group(rr);
+            const bool live = i < g.n;
+            const T *p = static_cast<const T *>(a.q) +
+                         (live ? (g.t0 + i) * a.q_stride + (int64_t)(g.h * a.group + rr - i * a.group) * D + 8 * j + 32 * gr : 0);
+#pragma unroll
+            for (int k = 0; k < (QS == 1 ? 1 : 2); ++k)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 tc::smem_u32(dst + (x * (QS == 1 ? 1 : 2) + k) * 512 + lane * 16)),
+                             "l"(p + 4 * k), "r"(live ? 16 : 0)
+                             : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int stage = 0;
+    bool idle = true;  // no tile of this warp's since its last copy of rows
+    copy_rows(at->seg[0], smem + Sm::Q);
+    for (int turn = 0; at->seg[turn].there; turn ^= 1) {
+        const Segment g = at->seg[turn];
+        // The rows' copies have landed: behind them stands one tile's group at most where this warp had a tile
+        // since, and none where it had not.
+        if (idle) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        idle = true;
+        if (threadIdx.x == 0) {
+            next_segment<R, TILE>(a, at->walk, at->seg[turn ^ 1]);
+            if (g.piece == 1)
+                a.joint[blockIdx.x] = Joint{g.t0, g.n, g.block, g.h, (int)div64(g.rest + run - 1, run) + 1};
+        }
+        if constexpr (QS > 1) {  // fp32: as three bf16 terms
+            for (int x = warp; x < NTL * G; x += WARPS) {
+                const float4 *p = reinterpret_cast<const float4 *>(smem + Sm::Q + turn * Sm::RAW) + x * 64 + lane;
+                const float4 u = p[0], v = p[32];
+                uint32_t f[4][QS];
+                split_bf16<QS>(u.x, u.y, f[0]);
+                split_bf16<QS>(u.z, u.w, f[1]);
+                split_bf16<QS>(v.x, v.y, f[2]);
+                split_bf16<QS>(v.z, v.w, f[3]);
+#pragma unroll
+                for (int k = 0; k < QS; ++k)
+                    reinterpret_cast<uint4 *>(smem + Sm::SPLIT)[(x * QS + k) * 32 + lane] =
+                        make_uint4(f[0][k], f[1][k], f[2][k], f[3][k]);
+            }
+        }
+        const uint4 *qs = reinterpret_cast<const uint4 *>(smem + (QS == 1 ? Sm::Q + turn * Sm::RAW : Sm::SPLIT));
         int hi[NTL][2], lo[NTL][2];
 #pragma unroll
         for (int nt = 0; nt < NTL; ++nt) {
-            const int rr = g.block * R + nt * 8 + r, i = rr / a.group;
-            const bool live = i < g.n;
-            const T *p = static_cast<const T *>(a.q) + (g.t0 + i) * a.q_stride +
-                         (int64_t)(g.h * a.group + rr - i * a.group) * D + 8 * j;
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                if constexpr (QS == 1) {
-                    const uint4 v = live ? *reinterpret_cast<const uint4 *>(p + 32 * gr) : make_uint4(0, 0, 0, 0);
-                    qf[nt][gr][0][0] = v.x; qf[nt][gr][1][0] = v.y; qf[nt][gr][2][0] = v.z; qf[nt][gr][3][0] = v.w;
-                } else {
-                    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float4 x = live ? *reinterpret_cast<const float4 *>(p + 32 * gr) : z;
-                    const float4 y = live ? *reinterpret_cast<const float4 *>(p + 32 * gr + 4) : z;
-                    split_bf16<QS>(x.x, x.y, qf[nt][gr][0]);
-                    split_bf16<QS>(x.z, x.w, qf[nt][gr][1]);
-                    split_bf16<QS>(y.x, y.y, qf[nt][gr][2]);
-                    split_bf16<QS>(y.z, y.w, qf[nt][gr][3]);
-                }
-            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int pos = g.len - g.n + (g.block * R + nt * 8 + 2 * j + e) / a.group;
+                const int pos = g.len - g.n + a.by_group(g.block * R + nt * 8 + 2 * j + e);
                 hi[nt][e] = a.causal ? min(pos + 1, g.len) : g.len;
                 lo[nt][e] = a.window > 0 ? pos - a.window + 1 : 0;
             }
         }
         // tiles between these two ends are seen whole by every row
-        const int i0 = g.block * R / a.group, i1 = min(g.n * a.group - 1, g.block * R + R - 1) / a.group;
+        const int i0 = a.by_group(g.block * R), i1 = a.by_group(min(g.n * a.group - 1, g.block * R + R - 1));
         const int whole_hi = a.causal ? g.len - g.n + i0 + 1 : g.len;
         const int whole_lo = a.window > 0 ? g.len - g.n + i1 - a.window + 1 : 0;
 
-        float o[G][2][NTL][4], mx[NTL][2], l[NTL][2];
+        // of each column: its reference maximum (in log2 units, negated; 0 where there is none yet), the score that
+        // moves it, and the sum of its factors
+        float o[G][2][NTL][4], neg[NTL][2], bar[NTL][2], l[NTL][2];
+        const float slack = SLACK / a.scale_log2;
 #pragma unroll
         for (int nt = 0; nt < NTL; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mx[nt][e] = -INFINITY;
+                neg[nt][e] = 0.f;
+                bar[nt][e] = -INFINITY;
                 l[nt][e] = 0.f;
             }
 #pragma unroll
@@ -205,25 +280,30 @@ __global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __gri
                     for (int e = 0; e < 4; ++e) o[gr][mt][nt][e] = 0.f;
         }
 
+        __syncthreads();
+        if constexpr (QS == 1) {
+            // What a column's product with a group of codes starts from: -24 times the sum of its 32 channels, since
+            // the codes come as 16 + c and stand for c - 8.
+            for (int x = warp; x < NTL * G; x += WARPS) {
+                const uint4 v = qs[x * 32 + lane];
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint32_t m24 = 0xC1C0C1C0u;
+                mma16816(z, m24, m24, m24, m24, v.x, v.y);
+                mma16816(z, m24, m24, m24, m24, v.z, v.w);
+                if (r == 0) zero[x * 4 + j] = make_float4(z[0], z[1], z[0], z[1]);
+            }
+            __syncthreads();
+        }
+        if (at->seg[turn ^ 1].there) copy_rows(at->seg[turn ^ 1], smem + Sm::Q + (turn ^ 1) * Sm::RAW);
         for (int tile = g.first + warp; tile < g.last; tile += WARPS) {
             const uint8_t *buf = ring + stage * Sm::STAGE;
-            if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(bar + stage, phase, WAIT_LIMIT_KV4))) {
-                // gave up: the copies in flight land before shared memory goes away, none is started any more
-                ok = false;
-                for (int i = 0, st = stage, ph = phase; i < inflight; ++i) {
-                    tc::mbar_wait(bar + st, ph, WAIT_LIMIT_KV4);
-                    if (++st == STAGES) {
-                        st = 0;
-                        ph ^= 1;
-                    }
-                }
-                if (lane == 0) atomicOr(a.err, DEVERR_TIMEOUT);
-            }
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+            __syncwarp();
             const int tok0 = tile * TILE;
             const bool edge = tok0 + TILE > min(whole_hi, g.len) || tok0 < whole_lo;
-            float s[2][NTL][4];
+            float s[BLOCKS][NTL][4];
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
+            for (int blk = 0; blk < BLOCKS; ++blk) {
                 const uint8_t *kb = buf + blk * BYTES;
                 uint32_t kw[2][G], ksc[2][(G + 1) / 2];
 #pragma unroll
@@ -242,24 +322,45 @@ __global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __gri
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     uint32_t f[2][4];
+                    if constexpr (QS == 1) {
+                        // bf16 queries: codes as they are, the group's scale on its scores. Sums of 32 products
+                        // of eight and five bits lose nothing that matters against the factors' bf16.
+                        float sc[2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t s2 = prmt(ksc[x][gr >> 1], 0, gr & 1 ? 0x3232 : 0x1010);
-                        expand(kw[x][gr], swap_bytes(kw[x][gr]), s2, minus24(s2), f[x]);
-                    }
+                        for (int x = 0; x < 2; ++x) {
+                            expand.codes16(kw[x][gr], swap_bytes(kw[x][gr]), f[x]);
+                            sc[x] = __uint_as_float(gr & 1 ? ksc[x][gr >> 1] & 0xffff0000u : ksc[x][gr >> 1] << 16);
+                        }
 #pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
+                        for (int nt = 0; nt < NTL; ++nt) {
+                            const uint4 q = qs[(nt * G + gr) * 32 + lane];
+                            const float4 c = zero[(nt * G + gr) * 4 + j];
+                            float z[4] = {c.x, c.y, c.z, c.w};
+                            mma16816(z, f[0][0], f[1][0], f[0][1], f[1][1], q.x, q.y);
+                            mma16816(z, f[0][2], f[1][2], f[0][3], f[1][3], q.z, q.w);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[blk][nt][e] = fmaf(z[e], sc[e >> 1], s[blk][nt][e]);
+                        }
+                    } else {  // fp32 queries: the cached values themselves, with nothing to cancel
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t s2 = prmt(ksc[x][gr >> 1], 0, gr & 1 ? 0x3232 : 0x1010);
+                            expand(kw[x][gr], swap_bytes(kw[x][gr]), s2, minus24(s2), f[x]);
+                        }
 #pragma unroll
                         for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
-                            for (int z = QS - 1; z >= 0; --z)
-                                mma16816(s[blk][nt], f[0][2 * ks], f[1][2 * ks], f[0][2 * ks + 1], f[1][2 * ks + 1],
-                                         qf[nt][gr][2 * ks][z], qf[nt][gr][2 * ks + 1][z]);
+                            for (int z = QS - 1; z >= 0; --z) {
+                                const uint4 q = qs[((nt * G + gr) * QS + z) * 32 + lane];
+                                mma16816(s[blk][nt], f[0][0], f[1][0], f[0][1], f[1][1], q.x, q.y);
+                                mma16816(s[blk][nt], f[0][2], f[1][2], f[0][3], f[1][3], q.z, q.w);
+                            }
+                    }
                 }
             }
             if (edge) {
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk)
+                for (int blk = 0; blk < BLOCKS; ++blk)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int tt = r + 8 * x, tok = tok0 + 16 * blk + tt;
@@ -280,19 +381,18 @@ __global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __gri
                             }
                     }
             }
-            // running maxima of the two columns, over the tile's 32 tokens
+            // The columns' reference maxima stay where no score of the tile passes one by 2^SLACK, which needs
+            // no exchange between lanes; else they are brought up to date.
             bool move = false;
             float top[NTL][2];
 #pragma unroll
             for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float m = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    top[nt][e] = m * a.scale_log2;
-                    move |= top[nt][e] > mx[nt][e] + SLACK;
+                    top[nt][e] = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+                    for (int blk = 1; blk < BLOCKS; ++blk) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[blk][nt][e], s[blk][nt][2 + e]));
+                    move |= top[nt][e] > bar[nt][e];
                 }
             if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -300,9 +400,17 @@ __global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __gri
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float m = fmaxf(mx[nt][e], top[nt][e]);
-                        f[e] = m == mx[nt][e] ? 1.f : exp2_fast(mx[nt][e] - m);
-                        mx[nt][e] = m;
+                        float m = top[nt][e];
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        f[e] = 1.f;
+                        if (m > bar[nt][e] - slack) {  // -infinity while there is no maximum
+                            const float n = -m * a.scale_log2;
+                            f[e] = bar[nt][e] == -INFINITY ? 0.f : exp2_fast(n - neg[nt][e]);
+                            neg[nt][e] = n;
+                            bar[nt][e] = m + slack;
+                        }
                         l[nt][e] *= f[e];
                     }
 #pragma unroll
@@ -314,26 +422,22 @@ __global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __gri
                 }
             }
             // factors, and their turn into the second product's operand
-            uint32_t p[2][NTL][2][QS];
 #pragma unroll
-            for (int nt = 0; nt < NTL; ++nt) {
-                const float m0 = mx[nt][0] == -INFINITY ? 0.f : -mx[nt][0], m1 = mx[nt][1] == -INFINITY ? 0.f : -mx[nt][1];
+            for (int blk = 0; blk < BLOCKS; ++blk) {
+                uint32_t p[NTL][2][QS];
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk)
+                for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float p0 = exp2_fast(fmaf(s[blk][nt][2 * x], a.scale_log2, m0));
-                        const float p1 = exp2_fast(fmaf(s[blk][nt][2 * x + 1], a.scale_log2, m1));
+                        const float p0 = exp2_fast(fmaf(s[blk][nt][2 * x], a.scale_log2, neg[nt][0]));
+                        const float p1 = exp2_fast(fmaf(s[blk][nt][2 * x + 1], a.scale_log2, neg[nt][1]));
                         l[nt][0] += p0;
                         l[nt][1] += p1;
                         uint32_t sp[QS];
                         split_bf16<QS>(p0, p1, sp);
 #pragma unroll
-                        for (int z = 0; z < QS; ++z) p[blk][nt][x][z] = transpose8x8(sp[z]);
+                        for (int z = 0; z < QS; ++z) p[nt][x][z] = transpose8x8(sp[z]);
                     }
-            }
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
                 const uint8_t *vb = buf + blk * BYTES;
                 uint32_t vw[2][G], vsc[2][G];  // pairs j and j + 4
 #pragma unroll
@@ -370,20 +474,13 @@ __global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __gri
 #pragma unroll
                             for (int z = QS - 1; z >= 0; --z)
                                 mma16816(o[gr][mt][nt], f[0][2 * mt], f[0][2 * mt + 1], f[1][2 * mt], f[1][2 * mt + 1],
-                                         p[blk][nt][0][z], p[blk][nt][1][z]);
+                                         p[nt][0][z], p[nt][1][z]);
                 }
             }
             __syncwarp();  // every lane has read the stage
-            --inflight;
-            if (ld.more && ok) {
-                if (lane == 0) ld.issue(a, ring + stage * Sm::STAGE, bar + stage);
-                ld.advance(a, warp);
-                ++inflight;
-            }
-            if (++stage == STAGES) {
-                stage = 0;
-                phase ^= 1;
-            }
+            copy_next(ring_at + stage * Sm::STAGE);
+            idle = false;
+            if (++stage == STAGES) stage = 0;
         }
 
         // the four warps' results of the item, brought to one maximum
@@ -395,8 +492,9 @@ __global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __gri
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (x != x) mx[nt][e] = 0.f;  // scores that are all NaN leave no maximum
-                if (r == 0) ml[warp * R + nt * 8 + 2 * j + e] = make_float2(mx[nt][e], x);
+                // no maximum: nothing seen, or scores that are all NaN
+                if (r == 0)
+                    ml[warp * R + nt * 8 + 2 * j + e] = make_float2(bar[nt][e] == -INFINITY && x == x ? -INFINITY : -neg[nt][e], x);
             }
         __syncthreads();
 #pragma unroll
@@ -407,118 +505,125 @@ __global__ void __launch_bounds__(32 * WARPS, 3) kv4_attn_few_kernel(const __gri
                 float m = -INFINITY;
 #pragma unroll
                 for (int x = 0; x < WARPS; ++x) m = fmaxf(m, ml[x * R + nt * 8 + 2 * j + e].x);
-                f[e] = mx[nt][e] == -INFINITY ? 0.f : exp2_fast(mx[nt][e] - m);
+                f[e] = m == -INFINITY ? 0.f : exp2_fast(-neg[nt][e] - m);
+                if (ml[warp * R + nt * 8 + 2 * j + e].x == -INFINITY) f[e] = 0.f;
             }
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr)
+            for (int c = 0; c < D / 64; ++c) {  // 64 channels at a time
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sum[(warp * 8 + 2 * j + (e & 1)) * (D + 1) + 32 * gr + 8 * (r >> 1) + (r & 1) + 4 * mt +
-                            2 * (e >> 1)] = o[gr][mt][nt][e] * f[e & 1];
-            __syncthreads();
+                    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int row = nt * 8 + 2 * warp + y, rr = g.block * R + row, i = rr / a.group;
-                float m = -INFINITY, total_l = 0.f;
+                        for (int e = 0; e < 4; ++e)
+                            sum[(warp * 8 + 2 * j + (e & 1)) * 65 + 32 * gr + 8 * (r >> 1) + (r & 1) + 4 * mt + 2 * (e >> 1)] =
+                                o[2 * c + gr][mt][nt][e] * f[e & 1];
+                __syncthreads();
 #pragma unroll
-                for (int x = 0; x < WARPS; ++x) m = fmaxf(m, ml[x * R + row].x);
+                for (int y = 0; y < 2; ++y) {
+                    const int row = nt * 8 + 2 * warp + y, rr = g.block * R + row, i = a.by_group(rr);
+                    float m = -INFINITY, total_l = 0.f, v0 = 0.f, v1 = 0.f;
 #pragma unroll
-                for (int x = 0; x < WARPS; ++x)
-                    if (ml[x * R + row].x != -INFINITY) total_l += ml[x * R + row].y * exp2_fast(ml[x * R + row].x - m);
-                float v[D / 32];
+                    for (int x = 0; x < WARPS; ++x) m = fmaxf(m, ml[x * R + row].x);
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    v[c] = 0.f;
-                    const int ch = 64 * (c >> 1) + 2 * lane + (c & 1);
-#pragma unroll
-                    for (int x = 0; x < WARPS; ++x) v[c] += sum[(x * 8 + 2 * warp + y) * (D + 1) + ch];
-                }
-                if (g.piece >= 0) {
-                    const int64_t at = ((int64_t)blockIdx.x * 2 + g.piece) * R + row;
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        *reinterpret_cast<float2 *>(a.part + at * D + 64 * c + 2 * lane) = make_float2(v[2 * c], v[2 * c + 1]);
-                    if (lane == 0)
-                        *reinterpret_cast<float2 *>(a.part + (int64_t)a.ctas * 2 * R * D + at * 2) = make_float2(m, total_l);
-                } else if (i < g.n) {
-                    const float inv = total_l == 0.f ? 0.f : 1.f / total_l;
-                    const int head = g.h * a.group + rr - i * a.group;
-                    T *p = static_cast<T *>(a.out) + (g.t0 + i) * a.out_stride + (int64_t)head * D;
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        const float x0 = v[2 * c] * inv, x1 = v[2 * c + 1] * inv;
-                        if constexpr (QS == 1)
-                            *reinterpret_cast<uint32_t *>(p + 64 * c + 2 * lane) = pack_bf16(x0, x1);
-                        else
-                            *reinterpret_cast<float2 *>(p + 64 * c + 2 * lane) = make_float2(x0, x1);
+                    for (int x = 0; x < WARPS; ++x) {
+                        if (ml[x * R + row].x != -INFINITY) total_l += ml[x * R + row].y * exp2_fast(ml[x * R + row].x - m);
+                        v0 += sum[(x * 8 + 2 * warp + y) * 65 + 2 * lane];
+                        v1 += sum[(x * 8 + 2 * warp + y) * 65 + 2 * lane + 1];
                     }
-                    if (lane == 0 && a.lse)
-                        a.lse[(g.t0 + i) * a.Hq + head] = total_l == 0.f ? -INFINITY : (m + log2f(total_l)) * 0.69314718f;
+                    if (g.piece >= 0) {
+                        const int64_t to = ((int64_t)blockIdx.x * 2 + g.piece) * R + row;
+                        *reinterpret_cast<float2 *>(a.part + to * D + 64 * c + 2 * lane) = make_float2(v0, v1);
+                        if (lane == 0) a.ml[to] = make_float2(m, total_l);
+                    } else if (i < g.n) {
+                        const float inv = total_l == 0.f ? 0.f : 1.f / total_l;
+                        const int head = g.h * a.group + rr - i * a.group;
+                        T *p = static_cast<T *>(a.out) + (g.t0 + i) * a.out_stride + (int64_t)head * D + 64 * c + 2 * lane;
+                        if constexpr (QS == 1) *reinterpret_cast<uint32_t *>(p) = pack_bf16(v0 * inv, v1 * inv);
+                        else *reinterpret_cast<float2 *>(p) = make_float2(v0 * inv, v1 * inv);
+                        if (lane == 0 && a.lse)
+                            a.lse[(g.t0 + i) * a.Hq + head] = total_l == 0.f ? -INFINITY : (m + log2f(total_l)) * 0.69314718f;
+                    }
                 }
+                __syncthreads();
             }
-            __syncthreads();
         }
     }
+    if (__any_sync(0xffffffffu, ld.bad) && lane == 0) atomicOr(a.err, DEVERR_PAGES);
 }
 
-// One row of the item that ends run blockIdx.x and goes on in the next, where that is the item's first piece.
-template <int D, typename T, int R, int TILE>
-__global__ void __launch_bounds__(D) kv4_attn_join_kernel(const __grid_constant__ AttnArgs a, int least) {
+// One row of the item that goes on behind run blockIdx.x: its pieces, in the runs' order within each of four
+// warps and then the warps'.
+template <int D, typename T, int R>
+__global__ void __launch_bounds__(128) kv4_attn_join_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int V = D / 32;
+    __shared__ float sum[4][D], ls[4];
     dependent_launch();
-    const int lane = threadIdx.x & 31, row = blockIdx.y;
-    const int64_t total = line_tiles<R, TILE>(a, lane), run = run_length(total, a.ctas, least);
-    const int64_t edge = (blockIdx.x + 1) * run;
-    if (edge >= total) return;
-    const Walk w = walk_at<R, TILE>(a, edge, lane);
-    const int64_t from = edge - w.t, to = from + w.s.tiles;  // the item's tiles
-    if (w.t == 0 || from < blockIdx.x * run) return;
-    const int block = w.item / a.c.Hk, h = w.item - block * a.c.Hk;
-    const int rr = block * R + row, i = rr / a.group;
-    if (i >= w.s.n) return;
-    const int pieces = (int)((to - 1) / run) - blockIdx.x + 1;
-    const float *mlp = a.part + (int64_t)a.ctas * 2 * R * D;
+    const Joint x = a.joint[blockIdx.x];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
+    const int rr = x.block * R + row, i = a.by_group(rr);
+    if (x.pieces == 0 || i >= x.n) return;
+    // the first piece is its run's second, all others their run's first
     auto at = [&](int p) { return ((int64_t)(blockIdx.x + p) * 2 + (p == 0)) * R + row; };
     float m = -INFINITY;
-    for (int p = lane; p < pieces; p += 32) m = fmaxf(m, mlp[at(p) * 2]);
+    for (int p = lane; p < x.pieces; p += 32) m = fmaxf(m, a.ml[at(p)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, v = 0.f;
+    float l = 0.f, v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = 0.f;
 #pragma unroll 4
-    for (int p = 0; p < pieces; ++p) {
-        const float2 x = *reinterpret_cast<const float2 *>(mlp + at(p) * 2);
-        const float f = x.x == -INFINITY ? 0.f : exp2_fast(x.x - m);
-        l = fmaf(x.y, f, l);
-        v = fmaf(a.part[at(p) * D + threadIdx.x], f, v);
+    for (int p = warp; p < x.pieces; p += 4) {
+        const float2 y = a.ml[at(p)];
+        const float f = y.x == -INFINITY ? 0.f : exp2_fast(y.x - m);
+        l = fmaf(y.y, f, l);
+        float w[V];
+        const float *from = a.part + at(p) * D + V * lane;
+        if constexpr (V == 4) {
+            const float4 z = *reinterpret_cast<const float4 *>(from);
+            w[0] = z.x; w[1] = z.y; w[2] = z.z; w[3] = z.w;
+        } else {
+            const float2 z = *reinterpret_cast<const float2 *>(from);
+            w[0] = z.x; w[1] = z.y;
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = fmaf(w[e], f, v[e]);
     }
-    const int head = h * a.group + rr - i * a.group;
-    const int64_t t = w.s.t0 + i;
-    Elem<T>::store(static_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D + threadIdx.x, l == 0.f ? 0.f : v / l);
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[warp][V * lane + e] = v[e];
+    if (lane == 0) ls[warp] = l;
+    __syncthreads();
+    l = ls[0] + ls[1] + ls[2] + ls[3];
+    const int head = x.h * a.group + rr - i * a.group;
+    const int64_t t = x.t0 + i;
+    if (threadIdx.x < D)
+        Elem<T>::store(static_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D + threadIdx.x,
+                       l == 0.f ? 0.f : (sum[0][threadIdx.x] + sum[1][threadIdx.x] + sum[2][threadIdx.x] + sum[3][threadIdx.x]) / l);
     if (threadIdx.x == 0 && a.lse) a.lse[t * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
 }
 
-template <int D, typename T, int R, int TILE> kda_status launch_join(const AttnArgs &a, int least, cudaStream_t s) {
-    launch_dependent(kv4_attn_join_kernel<D, T, R, TILE>, dim3(a.ctas - 1, R), dim3(D), 0, s, a, least);
+template <int D, typename T, int R> kda_status launch_join(const AttnArgs &a, cudaStream_t s) {
+    launch_dependent(kv4_attn_join_kernel<D, T, R>, dim3(a.ctas - 1, R), dim3(128), 0, s, a);
     return check_launch("kv4_attn_join_kernel");
 }
 
+static int few_ctas(int per_sm) {
+    const int sms = current_sms();
+    return per_sm * (sms > 0 ? sms : 152);
+}
+
 template <int D, typename T, int NTL> static kda_status attn_few(AttnArgs a, cudaStream_t s) {
-    using Sm = FewSmem<D, NTL>;
+    using Sm = FewSmem<D, NTL, sizeof(T) == 4 ? 3 : 1>;
     constexpr auto kern = kv4_attn_few_kernel<D, T, NTL>;
     if (smem_attr_once<kern>(Sm::BYTES) != cudaSuccess) return check_launch("kv4_attn_few_kernel: shared memory");
     // no more CTAs than the longest line that these sizes allow gives WARPS tiles each
     const int64_t blocks = a.c.T * a.group / Sm::R + a.c.B, tiles = ((int64_t)a.c.cols << a.c.page_shift) / TILE + 1;
-    a.ctas = (int)std::min<int64_t>(a.ctas, (blocks * a.c.Hk * tiles + WARPS - 1) / WARPS);
+    a.ctas = (int)std::min<int64_t>(few_ctas(few_per_sm(D)), (blocks * a.c.Hk * tiles + WARPS - 1) / WARPS);
+    place_pieces(a, a.part, Sm::R, D);
     launch_dependent(kern, dim3(a.ctas), dim3(32 * WARPS), Sm::BYTES, s, a);
     kda_status st = check_launch("kv4_attn_few_kernel");
     if (st || a.ctas == 1) return st;
-    return launch_join<D, T, Sm::R, TILE>(a, WARPS, s);
-}
-
-static int few_ctas() {
-    const int sms = current_sms();
-    return 3 * (sms > 0 ? sms : 152);
+    return launch_join<D, T, Sm::R>(a, s);
 }
 
 }  // namespace kv4
@@ -530,7 +635,7 @@ extern "C" size_t kda_kv4_attention_workspace_bytes(int B, int64_t T, int Hq, in
     if (B < 1 || T < 1 || Hq < 1 || Hk < 1 || Hq % Hk || (D != 64 && D != 128) ||
         (dtype != KDA_F32 && dtype != KDA_BF16))
         return 0;
-    return (size_t)kv4::few_ctas() * 2 * 16 * (size_t)(D + 2) * sizeof(float);
+    return kv4::pieces_bytes(kv4::few_ctas(kv4::few_per_sm(D)), 16, D);
 }
 
 extern "C" kda_status kda_kv4_attention(const void *q, const void *cache, const int32_t *block_table,
@@ -570,10 +675,11 @@ extern "C" kda_status kda_kv4_attention(const void *q, const void *cache, const 
     a.out_stride = out_stride;
     a.Hq = Hq;
     a.group = Hq / Hk;
+    a.by_group = kv4::Div(a.group);
+    a.by_hk = kv4::Div(Hk);
     a.causal = causal;
     a.window = window > 0x7fffff00LL ? 0 : (int)window;
     a.scale_log2 = scale * 1.44269504f;
-    a.ctas = kv4::few_ctas();
     a.few_rows = 0x7fffffff;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == KDA_F32) return D == 128 ? kv4::attn_few<128, float, 1>(a, s) : kv4::attn_few<64, float, 1>(a, s);

@@ -13,15 +13,40 @@
 namespace kda {
 namespace kv4 {
 
+// x / d for 0 <= x < 2^31 by a product with ceil(2^(31 + s) / d), 2^s >= d: a division costs some forty
+// instructions, and an item needs a dozen.
+struct Div {
+    uint32_t mul, shift;
+    Div() = default;
+    __host__ explicit Div(uint32_t d) {
+        shift = 0;
+        while ((1u << shift) < d) ++shift;
+        mul = (uint32_t)(((1ull << (31 + shift)) + d - 1) / d);
+    }
+    __device__ __forceinline__ int operator()(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> (31 + shift)); }
+};
+__device__ __forceinline__ int64_t div64(int64_t x, int64_t d) {
+    return ((x | d) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
+}
+
+// What the second kernel needs of an item that a run leaves unfinished; pieces = 0: there is none.
+struct Joint {
+    int64_t t0;
+    int n, block, h, pieces;
+};
+
 struct AttnArgs {
     const void *q;
     void *out;
     float *lse;       // or NULL
-    float *part;      // pieces: [CTA][2][R rows][D], then [CTA][2][R][2] maxima and sums
+    float *part;      // pieces: [CTA][2][R rows][D]
+    float2 *ml;       // their maxima and sums: [CTA][2][R]
+    Joint *joint;     // [CTA]: the item that goes on behind its run, where that is the item's first piece
     unsigned *err;
     Cache c;
     int64_t q_stride, out_stride;
     int Hq, group;    // query heads, and of one key/value head
+    Div by_group, by_hk;
     int causal, window;
     float scale_log2;  // scale * log2(e)
     int ctas;         // CTAs that cut the line
@@ -79,7 +104,7 @@ template <int R, int TILE> __device__ __forceinline__ int64_t line_tiles(const A
 }
 // Below `least` tiles a run is not cut further: a CTA's warps have one each.
 __device__ __forceinline__ int64_t run_length(int64_t total, int ctas, int least) {
-    const int64_t c = (total + ctas - 1) / ctas;
+    const int64_t c = div64(total + ctas - 1, ctas);
     return c < least ? least : c;
 }
 
@@ -112,7 +137,7 @@ template <int R, int TILE> __device__ __forceinline__ Walk walk_at(const AttnArg
             w.b = b0 + l;
             const int64_t rest = at - before - __shfl_sync(0xffffffffu, upto - mine, l);
             w.s = seq_at<R, TILE>(a, w.b, false);
-            w.item = (int)(rest / w.s.tiles);
+            w.item = (int)div64(rest, w.s.tiles);
             w.t = (int)(rest - (int64_t)w.item * w.s.tiles);
             w.left = 0;
             return w;
@@ -133,12 +158,15 @@ struct Segment {
     int b, block, h;
     int first, last;    // tiles of the sequence that it covers and some row sees: [first, last)
     int piece;          // -1: the whole item, 0: it began in an earlier run, 1: it goes on in the next
+    int rest;           // tiles that the item has behind this run
+    bool there;         // false: the run has no more
 };
 
-template <int R, int TILE> __device__ __forceinline__ bool next_segment(const AttnArgs &a, Walk &w, Segment &g) {
-    if (w.left <= 0) return false;
+template <int R, int TILE> __device__ __forceinline__ void next_segment(const AttnArgs &a, Walk &w, Segment &g) {
+    g.there = false;
+    if (w.left <= 0) return;
     while (w.item >= w.s.blocks * a.c.Hk) {
-        if (++w.b >= a.c.B) return false;
+        if (++w.b >= a.c.B) return;
         w.s = seq_at<R, TILE>(a, w.b, false);
         w.item = w.t = 0;
     }
@@ -147,10 +175,11 @@ template <int R, int TILE> __device__ __forceinline__ bool next_segment(const At
     g.n = w.s.n;
     g.len = w.s.len;
     g.b = w.b;
-    g.block = w.item / a.c.Hk;
+    g.block = a.by_hk(w.item);
     g.h = w.item - g.block * a.c.Hk;
     g.piece = w.t > 0 ? 0 : take < w.s.tiles ? 1 : -1;
-    const int i0 = g.block * R / a.group, i1 = min(w.s.n * a.group - 1, g.block * R + R - 1) / a.group;
+    g.rest = w.s.tiles - w.t - take;
+    const int i0 = a.by_group(g.block * R), i1 = a.by_group(min(w.s.n * a.group - 1, g.block * R + R - 1));
     const int hi = a.causal ? max(w.s.len - w.s.n + i1 + 1, 0) : w.s.len;
     const int lo = a.window > 0 ? max(w.s.len - w.s.n + i0 - a.window + 1, 0) : 0;
     g.first = max(w.s.lo_tile + w.t, lo / TILE);
@@ -161,7 +190,7 @@ template <int R, int TILE> __device__ __forceinline__ bool next_segment(const At
         w.t = 0;
         ++w.item;
     }
-    return true;
+    g.there = true;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -170,8 +199,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// Launches the kernel that joins the pieces of R rows each (tiles of TILE tokens, runs of at least `least`).
-template <int D, typename T, int R, int TILE> kda_status launch_join(const AttnArgs &a, int least, cudaStream_t s);
+// Bytes of the pieces of `ctas` runs of blocks of R rows, and where they stand in a workspace.
+inline size_t pieces_bytes(int ctas, int R, int D) {
+    return (size_t)ctas * (2 * (size_t)R * (D + 2) * sizeof(float) + sizeof(Joint));
+}
+inline void place_pieces(AttnArgs &a, void *workspace, int R, int D) {
+    a.part = static_cast<float *>(workspace);
+    a.ml = reinterpret_cast<float2 *>(a.part + (size_t)a.ctas * 2 * R * D);
+    a.joint = reinterpret_cast<Joint *>(a.ml + (size_t)a.ctas * 2 * R);
+}
+
+// Launches the kernel that joins the pieces of items of R rows.
+template <int D, typename T, int R> kda_status launch_join(const AttnArgs &a, cudaStream_t s);
 
 }  // namespace kv4
 }  // namespace kda
