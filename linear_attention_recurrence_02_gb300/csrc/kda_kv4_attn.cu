@@ -30,6 +30,7 @@ namespace kda {
 namespace kv4 {
 
 constexpr int WARPS = 4, STAGES = 2, TILE = 64, BLOCKS = TILE / BLOCK;
+constexpr int FEW_ROWS = 16;  // rows a key/value head up to which this kernel takes bf16 queries
 constexpr float SLACK = 8.f;  // log2 of how far scores may pass the running maximum before it moves
 
 // Where the run's computing (one for the CTA) and its copies (one a warp) stand. In shared memory, because
@@ -607,6 +608,9 @@ template <int D, typename T, int R> kda_status launch_join(const AttnArgs &a, cu
     return check_launch("kv4_attn_join_kernel");
 }
 
+template kda_status launch_join<128, __nv_bfloat16, 256>(const AttnArgs &a, cudaStream_t s);
+template kda_status launch_join<64, __nv_bfloat16, 256>(const AttnArgs &a, cudaStream_t s);
+
 static int few_ctas(int per_sm) {
     const int sms = current_sms();
     return per_sm * (sms > 0 ? sms : 152);
@@ -635,7 +639,8 @@ extern "C" size_t kda_kv4_attention_workspace_bytes(int B, int64_t T, int Hq, in
     if (B < 1 || T < 1 || Hq < 1 || Hk < 1 || Hq % Hk || (D != 64 && D != 128) ||
         (dtype != KDA_F32 && dtype != KDA_BF16))
         return 0;
-    return kv4::pieces_bytes(kv4::few_ctas(kv4::few_per_sm(D)), 16, D);
+    const size_t few = kv4::pieces_bytes(kv4::few_ctas(kv4::few_per_sm(D)), 16, D);
+    return dtype == KDA_BF16 && (T != B || Hq / Hk > kv4::FEW_ROWS) ? std::max(few, kv4::many_bytes(D)) : few;
 }
 
 extern "C" kda_status kda_kv4_attention(const void *q, const void *cache, const int32_t *block_table,
@@ -680,10 +685,20 @@ extern "C" kda_status kda_kv4_attention(const void *q, const void *cache, const 
     a.causal = causal;
     a.window = window > 0x7fffff00LL ? 0 : (int)window;
     a.scale_log2 = scale * 1.44269504f;
-    a.few_rows = 0x7fffffff;
+    a.most_rows = 0x7fffffff;
+    a.least_rows = 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == KDA_F32) return D == 128 ? kv4::attn_few<128, float, 1>(a, s) : kv4::attn_few<64, float, 1>(a, s);
-    if (a.group <= 8 && T == B)
-        return D == 128 ? kv4::attn_few<128, __nv_bfloat16, 1>(a, s) : kv4::attn_few<64, __nv_bfloat16, 1>(a, s);
+    if (!cu_seqlens) {  // one new token each: the rows are known
+        if (a.group > kv4::FEW_ROWS) return kv4::attn_many(a, D, s);
+        if (a.group <= 8)
+            return D == 128 ? kv4::attn_few<128, __nv_bfloat16, 1>(a, s) : kv4::attn_few<64, __nv_bfloat16, 1>(a, s);
+    } else if (T > B || a.group > kv4::FEW_ROWS) {
+        // each kernel takes the sequences that suit it; the second waits for the first, so they share the workspace
+        a.least_rows = kv4::FEW_ROWS + 1;
+        if ((st = kv4::attn_many(a, D, s)) || a.group > kv4::FEW_ROWS) return st;
+        a.least_rows = 0;
+        a.most_rows = kv4::FEW_ROWS;
+    }
     return D == 128 ? kv4::attn_few<128, __nv_bfloat16, 2>(a, s) : kv4::attn_few<64, __nv_bfloat16, 2>(a, s);
 }

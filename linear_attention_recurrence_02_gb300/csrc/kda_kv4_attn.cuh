@@ -50,7 +50,8 @@ struct AttnArgs {
     int causal, window;
     float scale_log2;  // scale * log2(e)
     int ctas;         // CTAs that cut the line
-    int few_rows;     // > 0: sequences of more rows a key/value head are left to the other kernel; < 0: of at most -few_rows
+    int most_rows;    // sequences with more rows a key/value head are another kernel's
+    int least_rows;   // and those with fewer
 };
 
 // A sequence as the items see it.
@@ -83,7 +84,7 @@ template <int R, int TILE> __device__ __forceinline__ Seq seq_at(const AttnArgs 
     s.n = (int)(t1 - t0);
     s.len = (int)len;
     const int rows = s.n * a.group;
-    if (a.few_rows > 0 ? rows > a.few_rows : rows <= -a.few_rows) s.n = 0;
+    if (rows > a.most_rows || rows < a.least_rows) s.n = 0;
     const int64_t lo = a.window > 0 ? len - s.n - a.window + 1 : 0;
     s.lo_tile = lo > 0 ? (int)lo / TILE : 0;
     s.tiles = max((s.len + TILE - 1) / TILE - s.lo_tile, 1);
@@ -208,6 +209,10 @@ inline void place_pieces(AttnArgs &a, void *workspace, int R, int D) {
     a.ml = reinterpret_cast<float2 *>(a.part + (size_t)a.ctas * 2 * R * D);
     a.joint = reinterpret_cast<Joint *>(a.ml + (size_t)a.ctas * 2 * R);
 }
+
+// The kernel for many rows (bf16): blocks of 256 rows, tcgen05. Uses many_bytes(D) of a.part.
+kda_status attn_many(const AttnArgs &a, int D, cudaStream_t s);
+size_t many_bytes(int D);
 
 // Launches the kernel that joins the pieces of items of R rows.
 template <int D, typename T, int R> kda_status launch_join(const AttnArgs &a, cudaStream_t s);
