@@ -42,18 +42,17 @@ __global__ void __launch_bounds__(NT) kv4_append_kernel(const T *k, const T *v, 
         uint32_t word[2], scale[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float x[8];
-            if (live) {
-                unpack8(i == 0 ? rk[u] : rv[u], x);
-            } else {
+            float f[8] = {};
+            if (live) unpack8(i == 0 ? rk[u] : rv[u], f);
+            float2 x[4];
+            float m = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            for (int e = 0; e < 4; ++e) {
+                x[e] = make_float2(f[2 * e], f[2 * e + 1]);
+                m = max_nan(m, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
             }
-            uint32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const float s = group_scale(m);
             word[i] = quantise8(x, s);
             scale[i] = __float_as_uint(s) >> 16;

@@ -84,11 +84,15 @@ __device__ __forceinline__ void Expand::operator()(uint32_t w, uint32_t swapped,
 __device__ __forceinline__ bool not_finite16(uint32_t bf16_bits) { return (bf16_bits & 0x7f80u) == 0x7f80u; }
 
 // ---------------------------------------------------------------- quantising
-// Bits of a group's scale from those of its largest |x| (compared as integers, so that a NaN is the
-// largest): NaN where a value is not finite.
-__device__ __forceinline__ float group_scale(uint32_t amax_bits) {
-    if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-    const float m = __uint_as_float(amax_bits);
+// Maximum that a NaN wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// A group's scale from its largest |x|: NaN where that is not finite.
+__device__ __forceinline__ float group_scale(float m) {
+    if (!(m < INFINITY)) return __uint_as_float(0x7fc00000u);
     // The smallest five-bit number with 7 s >= m (7 s is exact): m / 7 cut to five bits is at most two
     // steps below it, the second one where the product rounds below a number that m / 7 is just above.
     uint32_t b = __float_as_uint(m * (1.0f / 7.0f)) & ~0x7ffffu;
@@ -97,24 +101,34 @@ __device__ __forceinline__ float group_scale(uint32_t amax_bits) {
     return fminf(fmaxf(__uint_as_float(b), SCALE_MIN), SCALE_MAX);
 }
 
-// Word of eight channels. The quotient is rounded as a division would round it: with the reciprocal
-// correctly rounded, one residual step makes x * inv exact to the last bit (Markstein, "Computation of
+// Word of eight channels, as pairs of neighbours. The quotient is rounded as a division would round it: with the
+// reciprocal correctly rounded, one residual step makes x * inv exact to the last bit (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990); values that lie between two codes
-// are common, since inputs and scales have few bits.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float s) {
-    if (!(s == s)) return 0x40404040u;  // eight codes of 8
-    const float inv = __frcp_rn(s);
-    uint32_t half[2] = {0, 0};
+// are common, since inputs and scales have few bits. Adding 1.5 * 2^23 rounds to a whole number, halves to even;
+// the four codes of a half are joined as whole numbers in fp32 (below 2^16, so exactly), two halves at once.
+__device__ __forceinline__ uint32_t quantise8(float2 (&x)[4], float s) {
+    if (!(s == s)) return 0x44444444u;  // eight codes of 8, rotated
+    if (s == SCALE_MAX) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float q = x[i] * inv;
-        q = fmaf(fmaf(-q, s, x[i]), inv, q);
-        const int c = min(max(__float2int_rn(q), -7), 7) + 8;
-        half[i & 1] |= (uint32_t)c << (4 * (i >> 1));
+        for (int i = 0; i < 4; ++i)
+            x[i] = make_float2(fminf(fmaxf(x[i].x, -7.f * SCALE_MAX), 7.f * SCALE_MAX),
+                               fminf(fmaxf(x[i].y, -7.f * SCALE_MAX), 7.f * SCALE_MAX));
     }
+    const float inv = __frcp_rn(s);
+    const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-s, -s);
+    const float2 whole = make_float2(12582912.f, 12582912.f), less = make_float2(-12582912.f, -12582912.f);
+    float2 code = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) half[i] = ((half[i] << 3) | (half[i] >> 13)) & 0xffffu;
-    return half[0] | (half[1] << 16);
+    for (int i = 3; i >= 0; --i) {
+        float2 q = __fmul2_rn(x[i], inv2);
+        q = __ffma2_rn(__ffma2_rn(q, neg2, x[i]), inv2, q);
+        q = __fadd2_rn(__fadd2_rn(q, whole), less);
+        code = __ffma2_rn(code, make_float2(16.f, 16.f), q);
+    }
+    // + 8 for every code, and 2^23 so that the number stands in the lowest bits
+    code = __fadd2_rn(code, make_float2(8388608.f + 34952.f, 8388608.f + 34952.f));
+    const uint32_t w = __byte_perm(__float_as_uint(code.x), __float_as_uint(code.y), 0x5410);  // [odd][even]
+    return ((w << 3) & 0xfff8fff8u) | ((w >> 13) & 0x00070007u);
 }
 
 // ---------------------------------------------------------------- places

@@ -27,8 +27,10 @@ namespace kv4 {
 namespace many {
 
 constexpr int R = 256, TILE = 128, NT = 512;
-constexpr long long WAIT_LIMIT = 2000000000LL;  // clock cycles (about 1 s)
+constexpr uint32_t WAIT_TRIES = 1u << 25;        // of a wait before it gives up (about 1 s)
 constexpr float SLACK = 8.f;                    // log2 of how far scores may pass the reference maximum
+// What starting and finishing an item costs, in tiles: a run of many short items has as much less to compute.
+constexpr int ITEM_COST = 3;
 constexpr int SUMS = 4096;                      // sums of work kept while a CTA looks for its run
 
 // A place in the line of tiles; items are (sequence, block of rows, key/value head).
@@ -37,7 +39,7 @@ struct Place {
     int64_t t0;
     int b, n, len, blocks;
     int block, h, t;      // of the item, and its next tile
-    int first, tiles;     // the block's tiles: [first, first + tiles), at least one
+    int first, tiles;     // the block's tiles: [first, first + tiles), at least one; ITEM_COST more in the line
 };
 // What a run has of an item.
 struct Part {
@@ -75,7 +77,7 @@ __device__ __forceinline__ int64_t sequence_tiles(const AttnArgs &a, int b, int 
     for (int k = lane; k < s.blocks; k += 32) {
         int first, tiles;
         block_tiles(a, s.n, s.len, k, first, tiles);
-        sum += tiles;
+        sum += tiles + ITEM_COST;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -97,42 +99,58 @@ __device__ __forceinline__ void enter_sequence(const AttnArgs &a, Place &w) {
 
 __device__ __forceinline__ void next_part(const AttnArgs &a, Place &w, Part &g) {
     g.there = false;
-    if (w.left <= 0) return;
-    if (w.h >= a.c.Hk) {
-        ++w.block;
-        while (w.block >= w.blocks) {
-            if (++w.b >= a.c.B) return;
-            enter_sequence(a, w);
+    for (;;) {
+        if (w.left <= 0) return;
+        if (w.h >= a.c.Hk) {
+            ++w.block;
+            while (w.block >= w.blocks) {
+                if (++w.b >= a.c.B) return;
+                enter_sequence(a, w);
+            }
+            enter_block(a, w);
         }
-        enter_block(a, w);
+        const int from = w.t, take = (int)min((int64_t)(w.tiles + ITEM_COST - w.t), w.left), to = min(from + take, w.tiles);
+        const int h = w.h;
+        w.left -= take;
+        w.t += take;
+        if (w.t == w.tiles + ITEM_COST) {
+            w.t = 0;
+            ++w.h;
+        }
+        if (from >= w.tiles) continue;  // the item ended in the run before
+        g.t0 = w.t0;
+        g.b = w.b;
+        g.n = w.n;
+        g.len = w.len;
+        g.block = w.block;
+        g.h = h;
+        g.piece = from > 0 ? 0 : to < w.tiles ? 1 : -1;
+        g.rest = w.tiles - to;
+        g.first = w.first + from;
+        // a block that sees nothing has one tile in the line and none to compute
+        const bool nothing = g.first * TILE >= w.len ||
+                             (a.causal && w.len - w.n + a.by_group(min(w.n * a.group - 1, w.block * R + R - 1)) < 0);
+        g.last = nothing ? g.first : w.first + to;
+        g.there = true;
+        return;
     }
-    const int take = (int)min((int64_t)(w.tiles - w.t), w.left);
-    g.t0 = w.t0;
-    g.b = w.b;
-    g.n = w.n;
-    g.len = w.len;
-    g.block = w.block;
-    g.h = w.h;
-    g.piece = w.t > 0 ? 0 : take < w.tiles ? 1 : -1;
-    g.rest = w.tiles - w.t - take;
-    g.first = w.first + w.t;
-    // a block that sees nothing has one tile in the line and none to compute
-    g.last = g.first + take;
-    if (g.first * TILE >= w.len || (a.causal && w.len - w.n + a.by_group(min(w.n * a.group - 1, w.block * R + R - 1)) < 0))
-        g.last = g.first;
-    w.left -= take;
-    w.t += take;
-    if (w.t == w.tiles) {
-        w.t = 0;
-        ++w.h;
-    }
-    g.there = true;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// A bounded wait of few instructions: the waiting warps' polls take issue slots and integer units from the
+// working ones (a clock read and compared each time made a third of all instructions). NS > 0: nanoseconds
+// between the tries of a warp that is not in a hurry.
+template <int NS> __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+    for (uint32_t n = NS > 0 ? WAIT_TRIES / 8 : WAIT_TRIES; n > 0; --n) {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if constexpr (NS > 0) __nanosleep(NS);
+    }
+    return false;
 }
 
 // ---------------------------------------------------------------- issuing
@@ -293,7 +311,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
         for (int k = 0;; k += 32) {  // the block of rows
             int first = 0, tiles = 0;
             if (k + lane < w.blocks) block_tiles(a, w.n, w.len, k + lane, first, tiles);
-            const int64_t mine = (int64_t)tiles * a.c.Hk;
+            const int64_t mine = k + lane < w.blocks ? (int64_t)(tiles + ITEM_COST) * a.c.Hk : 0;
             int64_t upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -310,8 +328,8 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             before += __shfl_sync(0xffffffffu, upto, 31);
         }
         enter_block(a, w);
-        w.h = (int)div64(start - before, w.tiles);
-        w.t = (int)(start - before - (int64_t)w.h * w.tiles);
+        w.h = (int)div64(start - before, w.tiles + ITEM_COST);
+        w.t = (int)(start - before - (int64_t)w.h * (w.tiles + ITEM_COST));
         w.left = min(run, total - start);
         if (lane == 0)
             for (int x = 0; x < NT / 32; ++x) *reinterpret_cast<Place *>(sm + Sm::PLACES + 64 * x) = w;
@@ -319,12 +337,15 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
     __syncthreads();
 
     bool ok = true;
+    auto gave_up = [&]() {
+        ok = false;
+        if (lane == 0) atomicOr(a.err, DEVERR_TIMEOUT);
+    };
     auto wait = [&](uint64_t *b, int parity) {  // all lanes
-        if (!ok || __all_sync(0xffffffffu, mbar_try_wait(b, parity))) return;
-        if (!__all_sync(0xffffffffu, mbar_wait(b, parity, WAIT_LIMIT))) {
-            ok = false;
-            if (lane == 0) atomicOr(a.err, DEVERR_TIMEOUT);
-        }
+        if (ok && !__all_sync(0xffffffffu, wait_for<0>(b, parity))) gave_up();
+    };
+    auto wait_idly = [&](uint64_t *b, int parity) {
+        if (ok && !__all_sync(0xffffffffu, wait_for<100>(b, parity))) gave_up();
     };
     // All lanes: the run's next part, in the one of the warp's two places that the current part does not have. Parts
     // stay in shared memory: they are looked at once per item, and registers are short.
@@ -349,6 +370,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
         if (work) at_hand = advance();
         while (at_hand && at_hand->there) {
             const Part &g = *at_hand;
+            const Part *next = advance();
             const bool mine = g.n * a.group - g.block * R > 128 * i;
             const int rr = g.block * R + 128 * i + row, ti = a.by_group(rr), pos = g.len - g.n + ti;
             const int hi = a.causal ? min(pos + 1, g.len) : g.len, lo = a.window > 0 ? pos - a.window + 1 : 0;
@@ -450,7 +472,6 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                     l += sum.x + sum.y;
                     ++done;
                 }
-            const Part *next = advance();
             if (mine) {
                 if (l != l && top == -INFINITY) top = 0.f;  // scores that are all NaN leave no maximum
                 const float mx = top == -INFINITY ? -INFINITY : -neg;
@@ -666,10 +687,11 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             auto release = [&](uint64_t *b) {
                 if (ok) commit(b);
             };
-            for (const Part *g = advance(); g->there; g = advance()) {
-                const int nt = g->last - g->first;
+            for (const Part *g = advance(), *after; g->there; g = after) {
+                const int nt = g->last - g->first, rows = g->n * a.group - g->block * R;
+                after = advance();
                 if (nt <= 0) continue;
-                const int tiles = g->n * a.group - g->block * R > 128 ? 2 : 1;
+                const int tiles = rows > 128 ? 2 : 1;
                 wait(bar->k_full + (c & 1), (c >> 1) & 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -720,7 +742,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                 for (int i = 0; i < 2; ++i) {
                     const int r0 = g->block * R + 128 * i, rows = g->n * a.group - r0;
                     if (rows <= 0) break;
-                    wait(bar->q_empty + i, (n[i]++ & 1) ^ 1);
+                    wait_idly(bar->q_empty + i, (n[i]++ & 1) ^ 1);
                     for (int row = (warp - 13) * (256 / D) + lane / (D / 8); row < 128; row += 3 * (256 / D)) {
                         const int ti = a.by_group(r0 + row);
                         const bool live = row < rows;

@@ -102,6 +102,50 @@ def test_norm_rope_zero_rows_and_nan_rows_stay_apart(env):
     assert bool(qo[2, 1].isnan().all()) and not bool(qo.flatten(0, 1)[[0, 1, 2, 3, 4, 6, 7]].isnan().any())
 
 
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("T", [3, 1300])
+def test_norm_rope_with_one_weight(env, which, T):
+    """Only the queries or only the keys are normed, though their rows share warps."""
+    torch, kda = env
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    q, k = (torch.randn((T, h, 32), generator=gen, device="cuda") for h in (3, 2))
+    w = torch.rand(32, generator=gen, device="cuda")
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    kda.kda_qk_norm_rope(q, k, qo, ko, None, None, **{which + "_weight": w})
+    for x, y, n in ((q, qo, "q"), (k, ko, "k")):
+        want = ref.norm_rope(np64(x), np64(w) if n == which else None, [0] * T, None, 1e-6, False)
+        assert np.all(np.abs(np64(y) - want) <= 2.0 ** -20 * np.abs(want))
+
+
+@pytest.mark.parametrize("Hq,Hk,D,R,dt,inter", [(64, 8, 128, 128, "bfloat16", False), (3, 1, 64, 32, "float32", True),
+                                                (40, 0, 128, 64, "float32", False), (5, 4, 16, 16, "bfloat16", True)])
+def test_norm_rope_many_tokens(env, Hq, Hk, D, R, dt, inter):
+    """The form for many tokens gives each token what a call on it alone gives."""
+    torch, kda = env
+    dt = getattr(torch, dt)
+    gen = torch.Generator(device="cuda").manual_seed(Hq)
+    T = 4 * 2 * torch.cuda.get_device_properties(0).multi_processor_count + 5
+    wide = torch.randn((T, (Hq + Hk) * D + 16), generator=gen, device="cuda").to(dt)
+    q = wide[:, :Hq * D].unflatten(1, (Hq, D))
+    k = wide[:, Hq * D:(Hq + Hk) * D].unflatten(1, (Hk, D)) if Hk else None
+    w, pos = torch.rand(D, generator=gen, device="cuda"), torch.randint(0, 1 << 20, (T,), generator=gen, device="cuda")
+    freq = 10000.0 ** (-torch.arange(0, R, 2, dtype=torch.float64, device="cuda") / R)
+    qo, ko = torch.empty((T, Hq, D), dtype=dt, device="cuda"), torch.empty((T, Hk, D), dtype=dt, device="cuda") if Hk else None
+    kda.kda_qk_norm_rope(q, k, qo, ko, pos, freq, q_weight=w, k_weight=w, interleaved=inter)
+    kda.kda_sync_status()
+    q1, k1 = torch.empty_like(qo), None if ko is None else torch.empty_like(ko)
+    for a in range(0, T, 100):
+        s = slice(a, min(a + 100, T))
+        kda.kda_qk_norm_rope(q[s], None if k is None else k[s], q1[s], None if k is None else k1[s], pos[s], freq, q_weight=w,
+                             k_weight=w, interleaved=inter)
+    assert torch.equal(qo, q1) and (k is None or torch.equal(ko, k1))
+    wide2 = wide.clone()  # in place, too
+    q2 = wide2[:, :Hq * D].unflatten(1, (Hq, D))
+    k2 = wide2[:, Hq * D:(Hq + Hk) * D].unflatten(1, (Hk, D)) if Hk else None
+    kda.kda_qk_norm_rope(q2, k2, q2, k2, pos, freq, q_weight=w, k_weight=w, interleaved=inter)
+    assert torch.equal(q2, qo) and (k is None or torch.equal(k2, ko)) and torch.equal(wide2[:, -16:], wide[:, -16:])
+
+
 # ---------------------------------------------------------------- the cache
 def _layout(torch, rng, lens, page, spare=2, cols=None):
     """A block table over shuffled pages whose unused entries are pages that do not exist."""
