@@ -688,15 +688,17 @@ kda_status kda_kv4_read(const void *cache, const int32_t *block_table, const int
  * not see it are not touched.
  * Cached tokens are cut into equal runs for the SMs whatever the lengths, and the
  * pieces joined in a fixed order: the same call gives the same bits.
- *   workspace: kda_kv4_attention_workspace_bytes bytes (of the current device),
- *   16-byte aligned; scratch, needs no clearing, not shared by calls that may overlap.
+ *   workspace: kda_kv4_attention_workspace_bytes bytes (of the current device, for the
+ *   call's sizes; it does not depend on lengths, and may be 0: then NULL will do), 16-byte
+ *   aligned; scratch, needs no clearing, not shared by calls that may overlap.
  */
 kda_status kda_kv4_attention(const void *q, const void *cache, const int32_t *block_table, const int64_t *lens,
                              const int64_t *cu_seqlens, void *out, float *lse, int B, int64_t T, int Hq, int Hk,
                              int D, int page_size, int64_t pages, int table_cols, int64_t table_stride,
                              int64_t q_stride, int64_t out_stride, float scale, int causal, int64_t window,
                              kda_dtype dtype, void *workspace, size_t workspace_bytes, kda_stream_t stream);
-size_t kda_kv4_attention_workspace_bytes(int B, int64_t T, int Hq, int Hk, int D, kda_dtype dtype);
+size_t kda_kv4_attention_workspace_bytes(int B, int64_t T, int Hq, int Hk, int D, int page_size, int table_cols,
+                                         int with_cu_seqlens, int64_t window, kda_dtype dtype);
 
 /* Synchronise `stream`, then report (and clear) any device-side error flag
  * raised by earlier calls on the stream's device: KDA_ERR_DEVICE_CHECK,

@@ -35,7 +35,7 @@ typedef int (*kv4_read_fn)(const void *, const int32_t *, const int64_t *, const
 typedef int (*kv4_attention_fn)(const void *, const void *, const int32_t *, const int64_t *, const int64_t *, void *,
                                 float *, int, int64_t, int, int, int, int, int64_t, int, int64_t, int64_t, int64_t, float,
                                 int, int64_t, int, void *, size_t, void *);
-typedef size_t (*kv4_space_fn)(int, int64_t, int, int, int, int);
+typedef size_t (*kv4_space_fn)(int, int64_t, int, int, int, int, int, int, int64_t, int);
 
 static struct {
     add_rmsnorm_fn add_rmsnorm;
@@ -463,7 +463,8 @@ static PyObject *kv4_attention(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (found < 0) return PyLong_FromLong(-1);
     size_t size = 1;
     if (a[10] == Py_None) {
-        const size_t need = S.kv4_space((int)c.B, c.T, (int)Hq, (int)c.Hk, (int)c.D, q.dt);
+        const size_t need = S.kv4_space((int)c.B, c.T, (int)Hq, (int)c.Hk, (int)c.D, c.page, (int)c.cols,
+                                        a[5] != Py_None, window, q.dt);
         if (need > 0) return PyLong_FromLongLong(-(long long)need);
         size = 0;
     }

@@ -169,21 +169,23 @@ static kda_status check_rows(const void *k, const void *v, int64_t k_stride, int
     return KDA_OK;
 }
 
-// Four heads a thread once that still leaves every SM its threads (bf16, 8 heads of 128: 130560 tokens read
-// in 104 us with four, 119 with one), one head a thread below that, for latency.
-template <typename F> static kda_status launch_rows(const Cache &c, int D, F &&go) {
-    const int hu = c.T * c.Hk * (D / 8) >= (int64_t)current_sms() * 2048 * 4 && c.Hk >= 4 ? 4 : 1;
+// `most` heads a thread once that still leaves every SM its threads, one head a thread below that, for latency.
+// bf16, 8 heads of 128: 28672 tokens written in 28.8 us with four, 30.6 with two, 36 with one or eight; 102000 read
+// in 72 us with two, 78 with four, 90 with one.
+constexpr int APPEND_HEADS = 4, READ_HEADS = 2;
+template <typename F> static kda_status launch_rows(const Cache &c, int D, int most, F &&go) {
+    const int hu = c.T * c.Hk * (D / 8) >= (int64_t)current_sms() * 2048 * 4 && c.Hk >= most ? most : 1;
     const int64_t blocks = (c.T * ((c.Hk + hu - 1) / hu) * (D / 8) + NT - 1) / NT;
     if (blocks > 0x7fffffffLL) return invalid("T*Hk*D too large for one launch");
-    go((unsigned)blocks, hu);
+    go((unsigned)blocks, hu > 1);
     return KDA_OK;
 }
 
 template <int D, typename T>
 static kda_status append(const void *k, const void *v, const Cache &c, int64_t ks, int64_t vs, unsigned *err,
                          cudaStream_t s) {
-    const kda_status st = launch_rows(c, D, [&](unsigned blocks, int hu) {
-        auto kern = hu == 4 ? kv4_append_kernel<D, T, 4> : kv4_append_kernel<D, T, 1>;
+    const kda_status st = launch_rows(c, D, APPEND_HEADS, [&](unsigned blocks, bool several) {
+        auto kern = several ? kv4_append_kernel<D, T, APPEND_HEADS> : kv4_append_kernel<D, T, 1>;
         launch_dependent(kern, dim3(blocks), dim3(NT), 0, s, static_cast<const T *>(k), static_cast<const T *>(v), c, ks,
                          vs, err);
     });
@@ -191,8 +193,8 @@ static kda_status append(const void *k, const void *v, const Cache &c, int64_t k
 }
 template <int D, typename T>
 static kda_status read(const Cache &c, void *k, void *v, int64_t ks, int64_t vs, unsigned *err, cudaStream_t s) {
-    const kda_status st = launch_rows(c, D, [&](unsigned blocks, int hu) {
-        auto kern = hu == 4 ? kv4_read_kernel<D, T, 4> : kv4_read_kernel<D, T, 1>;
+    const kda_status st = launch_rows(c, D, READ_HEADS, [&](unsigned blocks, bool several) {
+        auto kern = several ? kv4_read_kernel<D, T, READ_HEADS> : kv4_read_kernel<D, T, 1>;
         launch_dependent(kern, dim3(blocks), dim3(NT), 0, s, c, static_cast<T *>(k), static_cast<T *>(v), ks, vs, err);
     });
     return st ? st : check_launch("kv4_read_kernel");

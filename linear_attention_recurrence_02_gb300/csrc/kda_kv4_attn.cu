@@ -30,6 +30,7 @@ namespace kda {
 namespace kv4 {
 
 constexpr int WARPS = 4, STAGES = 2, TILE = 64, BLOCKS = TILE / BLOCK;
+constexpr int MOST_GROUP = 8;  // CTAs of a cluster
 constexpr int FEW_ROWS = 16;  // rows a key/value head up to which this kernel takes bf16 queries
 constexpr float SLACK = 8.f;  // log2 of how far scores may pass the running maximum before it moves
 
@@ -154,7 +155,32 @@ template <int D, int R> struct Loader {
 // CTAs of an SM: as many as registers (without spills) and shared memory allow.
 constexpr int few_per_sm(int D) { return D == 64 ? 3 : 2; }
 
-template <int D, typename T, int NTL>
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The fp32 at shared memory address `at` of the cluster's CTA `rank`.
+__device__ __forceinline__ float peer_float(uint32_t at, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .u32 p;\n\tmapa.shared::cluster.u32 p, %1, %2;\n\tld.shared::cluster.f32 %0, [p];\n\t}"
+                 : "=f"(v)
+                 : "r"(at), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+// GROUP: a cluster has one item, whose tiles its CTAs share and whose results they join through each other's shared
+// memory. Else CTAs have runs of the line of tiles, and what they have of unfinished items goes to the workspace.
+template <int D, typename T, int NTL, bool GROUP>
 __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int G = D / 32, QS = sizeof(T) == 4 ? 3 : 1, BYTES = Format<D>::BYTES;
     using Sm = FewSmem<D, NTL, QS>;
@@ -168,20 +194,31 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
     float4 *zero = reinterpret_cast<float4 *>(smem + Sm::ZERO);
     dependent_launch();
 
-    const int64_t total = line_tiles<R, TILE>(a, lane), run = run_length(total, a.ctas, WARPS);
-    const int64_t start = blockIdx.x * run;
-    if (threadIdx.x == 0) a.joint[blockIdx.x].pieces = 0;
-    if (start >= total) return;  // the whole CTA
     Places *at = reinterpret_cast<Places *>(smem + Sm::PLACES);
-    {
-        Walk w = walk_at<R, TILE>(a, start, lane);
+    Walk w;
+    int64_t run = 0;
+    bool shared_out = false;  // GROUP: more than one CTA has tiles of the item
+    if constexpr (GROUP) {
+        const int size = cluster_size(), rank = cluster_rank();
+        if (!item_at<R, TILE>(a, blockIdx.x / size, lane, w)) return;  // the whole cluster
+        const int per = (w.s.tiles + size - 1) / size;
+        w.t = min(rank * per, w.s.tiles);
+        w.left = min(per, w.s.tiles - w.t);
+        shared_out = per < w.s.tiles;
+    } else {
+        const int64_t total = line_tiles<R, TILE>(a, lane);
+        run = run_length(total, a.ctas, WARPS);
+        const int64_t start = blockIdx.x * run;
+        if (threadIdx.x == 0) a.joint[blockIdx.x].pieces = 0;
+        if (start >= total) return;  // the whole CTA
+        w = walk_at<R, TILE>(a, start, lane);
         w.left = min(run, total - start);
-        if (lane == 0) {
-            at->ahead[warp] = w;
-            if (warp == 0) {
-                next_segment<R, TILE>(a, w, at->seg[0]);
-                at->walk = w;
-            }
+    }
+    if (lane == 0) {
+        at->ahead[warp] = w;
+        if (warp == 0) {
+            at->walk = w;
+            next_segment<R, TILE>(a, at->walk, at->seg[0]);
         }
     }
     __syncthreads();
@@ -217,7 +254,7 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
 
     int stage = 0;
     bool idle = true;  // no tile of this warp's since its last copy of rows
-    copy_rows(at->seg[0], smem + Sm::Q);
+    if (at->seg[0].there) copy_rows(at->seg[0], smem + Sm::Q);
     for (int turn = 0; at->seg[turn].there; turn ^= 1) {
         const Segment g = at->seg[turn];
         // The rows' copies have landed: behind them stands one tile's group at most where this warp had a tile
@@ -227,7 +264,7 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
         idle = true;
         if (threadIdx.x == 0) {
             next_segment<R, TILE>(a, at->walk, at->seg[turn ^ 1]);
-            if (g.piece == 1)
+            if (!GROUP && g.piece == 1)
                 a.joint[blockIdx.x] = Joint{g.t0, g.n, g.block, g.h, (int)div64(g.rest + run - 1, run) + 1};
         }
         if constexpr (QS > 1) {  // fp32: as three bf16 terms
@@ -532,7 +569,12 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
                         v0 += sum[(x * 8 + 2 * warp + y) * 65 + 2 * lane];
                         v1 += sum[(x * 8 + 2 * warp + y) * 65 + 2 * lane + 1];
                     }
-                    if (g.piece >= 0) {
+                    if (GROUP && g.piece >= 0) {  // the ring has nothing on its way any more
+                        float *to = reinterpret_cast<float *>(smem) + row * D + 64 * c + 2 * lane;
+                        to[0] = v0;
+                        to[1] = v1;
+                        if (lane == 0) reinterpret_cast<float2 *>(smem + R * D * 4)[row] = make_float2(m, total_l);
+                    } else if (g.piece >= 0) {
                         const int64_t to = ((int64_t)blockIdx.x * 2 + g.piece) * R + row;
                         *reinterpret_cast<float2 *>(a.part + to * D + 64 * c + 2 * lane) = make_float2(v0, v1);
                         if (lane == 0) a.ml[to] = make_float2(m, total_l);
@@ -551,6 +593,37 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
         }
     }
     if (__any_sync(0xffffffffu, ld.bad) && lane == 0) atomicOr(a.err, DEVERR_PAGES);
+    if constexpr (GROUP) {
+        if (!shared_out) return;  // the whole cluster
+        const int size = cluster_size(), rank = cluster_rank();
+        float2 *mine = reinterpret_cast<float2 *>(smem + R * D * 4);
+        if (!at->seg[0].there && threadIdx.x < R) mine[threadIdx.x] = make_float2(-INFINITY, 0.f);
+        cluster_sync();
+        const int h = w.item % a.c.Hk, block = w.item / a.c.Hk;
+        // CTA `rank` has every size-th row from its own on, a warp 32 of a row's channels
+        for (int x = warp; rank + size * (x / G) < R; x += WARPS) {
+            const int row = rank + size * (x / G), ch = 32 * (x % G) + lane, rr = block * R + row, i = a.by_group(rr);
+            if (i >= w.s.n) break;
+            const uint32_t ml_at = tc::smem_u32(mine + row), v_at = tc::smem_u32(smem) + (row * D + ch) * 4;
+            float pm[MOST_GROUP], m = -INFINITY, l = 0.f, v = 0.f;
+#pragma unroll
+            for (int p = 0; p < MOST_GROUP; ++p) {
+                pm[p] = p < size ? peer_float(ml_at, p) : -INFINITY;
+                m = fmaxf(m, pm[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < MOST_GROUP; ++p)
+                if (pm[p] != -INFINITY) {
+                    const float f = exp2_fast(pm[p] - m);
+                    l = fmaf(peer_float(ml_at + 4, p), f, l);
+                    v = fmaf(peer_float(v_at, p), f, v);
+                }
+            const int head = h * a.group + rr - i * a.group;
+            Elem<T>::store(static_cast<T *>(a.out) + (w.s.t0 + i) * a.out_stride + (int64_t)head * D + ch, l == 0.f ? 0.f : v / l);
+            if (ch == 0 && a.lse) a.lse[(w.s.t0 + i) * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+        }
+        cluster_sync();  // no CTA leaves while another still reads what it has
+    }
 }
 
 // One row of the item that goes on behind run blockIdx.x: its pieces, in the runs' order within each of four
@@ -616,13 +689,51 @@ static int few_ctas(int per_sm) {
     return per_sm * (sms > 0 ? sms : 152);
 }
 
+// Blocks of R rows and tiles of an item that these sizes allow, and the CTAs of a cluster where a cluster has one item
+// (0: the CTAs have runs). One item a cluster, of as many CTAs as fit the card at once, saves the second kernel (5 us
+// a call where launches follow one another) but leaves the SMs as unequal work as the lengths are: taken where even
+// the longest item that the block table has room for gives a warp four tiles at most (8 us).
+struct FewPlan {
+    int64_t blocks, tiles;
+    int group;
+};
+static FewPlan plan_few(const AttnArgs &a, int R, int cap) {
+    FewPlan p;
+    p.blocks = a.c.cu ? a.c.T * a.group / R + a.c.B : (int64_t)a.c.B * ((a.group + R - 1) / R);
+    p.tiles = ((int64_t)a.c.cols << a.c.page_shift) / TILE + 1;
+    if (a.window > 0) p.tiles = std::min(p.tiles, ((int64_t)a.window + (a.c.cu ? a.c.T : 1)) / TILE + 2);
+    p.group = MOST_GROUP;
+    while (p.group > 1 && (p.blocks * a.c.Hk * p.group > cap || p.group / 2 * WARPS >= p.tiles)) p.group /= 2;
+    if (p.tiles > 4 * WARPS * p.group || p.blocks * a.c.Hk * p.group > 0x7fffffffLL) p.group = 0;
+    return p;
+}
+
 template <int D, typename T, int NTL> static kda_status attn_few(AttnArgs a, cudaStream_t s) {
     using Sm = FewSmem<D, NTL, sizeof(T) == 4 ? 3 : 1>;
-    constexpr auto kern = kv4_attn_few_kernel<D, T, NTL>;
+    const int cap = few_ctas(few_per_sm(D));
+    const FewPlan plan = plan_few(a, Sm::R, cap);
+    if (plan.group > 0) {
+        constexpr auto kern = kv4_attn_few_kernel<D, T, NTL, true>;
+        if (smem_attr_once<kern>(Sm::BYTES) != cudaSuccess) return check_launch("kv4_attn_few_kernel: shared memory");
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(plan.blocks * a.c.Hk * plan.group));
+        cfg.blockDim = dim3(32 * WARPS);
+        cfg.dynamicSmemBytes = Sm::BYTES;
+        cfg.stream = s;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = (unsigned)plan.group;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 2;
+        cudaLaunchKernelEx(&cfg, kern, a);  // an error is left for check_launch
+        return check_launch("kv4_attn_few_kernel");
+    }
+    constexpr auto kern = kv4_attn_few_kernel<D, T, NTL, false>;
     if (smem_attr_once<kern>(Sm::BYTES) != cudaSuccess) return check_launch("kv4_attn_few_kernel: shared memory");
-    // no more CTAs than the longest line that these sizes allow gives WARPS tiles each
-    const int64_t blocks = a.c.T * a.group / Sm::R + a.c.B, tiles = ((int64_t)a.c.cols << a.c.page_shift) / TILE + 1;
-    a.ctas = (int)std::min<int64_t>(few_ctas(few_per_sm(D)), (blocks * a.c.Hk * tiles + WARPS - 1) / WARPS);
+    a.ctas = (int)std::min<int64_t>(cap, (plan.blocks * a.c.Hk * plan.tiles + WARPS - 1) / WARPS);
     place_pieces(a, a.part, Sm::R, D);
     launch_dependent(kern, dim3(a.ctas), dim3(32 * WARPS), Sm::BYTES, s, a);
     kda_status st = check_launch("kv4_attn_few_kernel");
@@ -635,12 +746,48 @@ template <int D, typename T, int NTL> static kda_status attn_few(AttnArgs a, cud
 
 using namespace kda;
 
-extern "C" size_t kda_kv4_attention_workspace_bytes(int B, int64_t T, int Hq, int Hk, int D, kda_dtype dtype) {
-    if (B < 1 || T < 1 || Hq < 1 || Hk < 1 || Hq % Hk || (D != 64 && D != 128) ||
-        (dtype != KDA_F32 && dtype != KDA_BF16))
+namespace kda {
+namespace kv4 {
+// The kernels of a call: which it takes, and the workspace that they need.
+struct Route {
+    bool many, few;  // many first
+    int row_tiles;   // of 8 rows, of the kernel for few rows
+    size_t bytes;
+};
+static Route route(const AttnArgs &a, int D, kda_dtype dtype) {
+    Route r = {false, true, 1, 0};
+    if (dtype == KDA_BF16) {
+        // one new token each: the rows are known; else, with more tokens than sequences, each kernel takes the sequences
+        // that suit it, and the second waits for the first, so that they share the workspace
+        r.many = a.group > FEW_ROWS || (a.c.cu && a.c.T > a.c.B);
+        r.few = a.group <= FEW_ROWS;
+        r.row_tiles = !a.c.cu && a.group <= 8 ? 1 : 2;
+    }
+    const int cap = few_ctas(few_per_sm(D));
+    if (r.few && plan_few(a, 8 * r.row_tiles, cap).group == 0) r.bytes = pieces_bytes(cap, 8 * r.row_tiles, D);
+    if (r.many) r.bytes = std::max(r.bytes, many_bytes(D));
+    return r;
+}
+}  // namespace kv4
+}  // namespace kda
+
+extern "C" size_t kda_kv4_attention_workspace_bytes(int B, int64_t T, int Hq, int Hk, int D, int page_size, int table_cols,
+                                                    int with_cu_seqlens, int64_t window, kda_dtype dtype) {
+    kv4::AttnArgs a = {};
+    if (B < 1 || T < 1 || Hq < 1 || Hk < 1 || Hq % Hk || (D != 64 && D != 128) || (dtype != KDA_F32 && dtype != KDA_BF16) ||
+        table_cols < 1 || page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) || window < 0)
         return 0;
-    const size_t few = kv4::pieces_bytes(kv4::few_ctas(kv4::few_per_sm(D)), 16, D);
-    return dtype == KDA_BF16 && (T != B || Hq / Hk > kv4::FEW_ROWS) ? std::max(few, kv4::many_bytes(D)) : few;
+    static const int64_t some = 0;
+    a.c.B = B;
+    a.c.T = T;
+    a.c.Hk = Hk;
+    a.c.cols = table_cols;
+    a.c.cu = with_cu_seqlens ? &some : nullptr;  // not looked at
+    a.c.page_shift = 4;
+    while ((1 << a.c.page_shift) < page_size) ++a.c.page_shift;
+    a.group = Hq / Hk;
+    a.window = window > 0x7fffff00LL ? 0 : (int)window;
+    return kv4::route(a, D, dtype).bytes;
 }
 
 extern "C" kda_status kda_kv4_attention(const void *q, const void *cache, const int32_t *block_table,
@@ -667,15 +814,9 @@ extern "C" kda_status kda_kv4_attention(const void *q, const void *cache, const 
         return invalid("token strides must be at least Hq*D");
     if (T > 1 && (q_stride % unit || out_stride % unit)) return invalid("token strides must be multiples of 16 bytes");
     if (out == q || out == cache || out == lse || lse == q || lse == cache) return invalid("out and lse must not alias other arguments");
-    const size_t need = kda_kv4_attention_workspace_bytes(B, T, Hq, Hk, D, dtype);
-    if (workspace_bytes < need) return invalid("workspace too small (kda_kv4_attention_workspace_bytes)");
-    if (need && (st = check_ptr(workspace, "workspace"))) return st;
-    if ((st = bind_stream_device(stream))) return st;
-    if (!(a.err = device_error_word())) return fail(KDA_ERR_CUDA, "device error word unavailable");
     a.q = q;
     a.out = out;
     a.lse = lse;
-    a.part = static_cast<float *>(workspace);
     a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.Hq = Hq;
@@ -687,18 +828,21 @@ extern "C" kda_status kda_kv4_attention(const void *q, const void *cache, const 
     a.scale_log2 = scale * 1.44269504f;
     a.most_rows = 0x7fffffff;
     a.least_rows = 0;
+    const kv4::Route r = kv4::route(a, D, dtype);
+    if (workspace_bytes < r.bytes) return invalid("workspace too small (kda_kv4_attention_workspace_bytes)");
+    if (r.bytes && (st = check_ptr(workspace, "workspace"))) return st;
+    a.part = static_cast<float *>(workspace);
+    if ((st = bind_stream_device(stream))) return st;
+    if (!(a.err = device_error_word())) return fail(KDA_ERR_CUDA, "device error word unavailable");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == KDA_F32) return D == 128 ? kv4::attn_few<128, float, 1>(a, s) : kv4::attn_few<64, float, 1>(a, s);
-    if (!cu_seqlens) {  // one new token each: the rows are known
-        if (a.group > kv4::FEW_ROWS) return kv4::attn_many(a, D, s);
-        if (a.group <= 8)
-            return D == 128 ? kv4::attn_few<128, __nv_bfloat16, 1>(a, s) : kv4::attn_few<64, __nv_bfloat16, 1>(a, s);
-    } else if (T > B || a.group > kv4::FEW_ROWS) {
-        // each kernel takes the sequences that suit it; the second waits for the first, so they share the workspace
-        a.least_rows = kv4::FEW_ROWS + 1;
-        if ((st = kv4::attn_many(a, D, s)) || a.group > kv4::FEW_ROWS) return st;
+    if (r.many) {
+        if (r.few) a.least_rows = kv4::FEW_ROWS + 1;
+        if ((st = kv4::attn_many(a, D, s)) || !r.few) return st;
         a.least_rows = 0;
         a.most_rows = kv4::FEW_ROWS;
     }
+    if (r.row_tiles == 1)
+        return D == 128 ? kv4::attn_few<128, __nv_bfloat16, 1>(a, s) : kv4::attn_few<64, __nv_bfloat16, 1>(a, s);
     return D == 128 ? kv4::attn_few<128, __nv_bfloat16, 2>(a, s) : kv4::attn_few<64, __nv_bfloat16, 2>(a, s);
 }

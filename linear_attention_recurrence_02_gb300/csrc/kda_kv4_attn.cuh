@@ -152,6 +152,33 @@ template <int R, int TILE> __device__ __forceinline__ Walk walk_at(const AttnArg
     return w;
 }
 
+// All 32 lanes: the beginning of item `at`, left = 0; false where there are not so many.
+template <int R, int TILE> __device__ __forceinline__ bool item_at(const AttnArgs &a, int64_t at, int lane, Walk &w) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += 32) {
+        int64_t mine = 0;
+        if (b0 + lane < a.c.B) mine = (int64_t)seq_at<R, TILE>(a, b0 + lane, at == 0).blocks * a.c.Hk;
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > at);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            w.b = b0 + l;
+            w.item = (int)(at - before - __shfl_sync(0xffffffffu, upto - mine, l));
+            w.s = seq_at<R, TILE>(a, w.b, false);
+            w.t = 0;
+            w.left = 0;
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
 // What a run has of one item.
 struct Segment {
     int64_t t0;         // the sequence's first new token

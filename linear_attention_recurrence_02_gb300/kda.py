@@ -101,7 +101,7 @@ _SIGNATURES = {
     "kda_kv4_read": ([_vp] * 6 + [_ci, _i64, _ci, _ci, _ci, _i64, _ci, _i64, _i64, _i64, _ci, _vp], _ci),
     "kda_kv4_attention": ([_vp] * 7 + [_ci, _i64, _ci, _ci, _ci, _ci, _i64, _ci, _i64, _i64, _i64, _cf, _ci, _i64, _ci,
                                        _vp, _sz, _vp], _ci),
-    "kda_kv4_attention_workspace_bytes": ([_ci, _i64, _ci, _ci, _ci, _ci], _sz),
+    "kda_kv4_attention_workspace_bytes": ([_ci, _i64, _ci, _ci, _ci, _ci, _ci, _ci, _i64, _ci], _sz),
     "kda_sync_status": ([_vp], _ci),
     "kda_selftest_bounded_wait": ([ctypes.c_longlong, _vp], _ci),
 }
@@ -701,18 +701,20 @@ def kda_kv4_attention(q, cache, block_table, lens, out, cu_seqlens=None, scale=N
         with _current(q.device):
             return kda_kv4_attention(*args[:6], scale=scale, causal=causal, window=window, lse=lse, workspace=workspace,
                                      stream=stream)
-    if status < -1:
+    if status < -1:  # the workspace that these sizes need
         workspace, _ = _scratch(None, -status, q.device, stream)
         status = fn(*args, workspace, stream)
     if status:
         _check(status)
 
 
-def kda_kv4_attention_workspace_bytes(B, T, Hq, Hk, D, dtype) -> int:
-    """Workspace of kda_kv4_attention for B sequences and T new tokens; dtype torch.bfloat16 or torch.float32."""
+def kda_kv4_attention_workspace_bytes(B, T, Hq, Hk, D, page_size, table_cols, with_cu_seqlens, dtype, window=0) -> int:
+    """Workspace of a kda_kv4_attention of these sizes on the current device (0: none); dtype torch.bfloat16 or
+    torch.float32."""
     import torch
     code = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}[dtype]
-    return int(lib().kda_kv4_attention_workspace_bytes(B, T, Hq, Hk, D, code))
+    return int(lib().kda_kv4_attention_workspace_bytes(B, T, Hq, Hk, D, page_size, table_cols, int(with_cu_seqlens), window,
+                                                       code))
 
 
 def kda_selftest_bounded_wait(limit_cycles=2_000_000, stream=None, device=None):

@@ -351,6 +351,28 @@ def test_attention(env, lens, new, Hq, Hk, D, page, dt, causal, window):
     assert torch.equal(again[:T - extra], out[:T - extra])  # the same bits, without lse too
 
 
+@pytest.mark.parametrize("lens,Hq,Hk,dt,window,cols", [
+    ([3000, 1, 0, 77], 8, 2, "bfloat16", 0, 400),   # a table with room for more than a cluster takes at once
+    ([3000, 1, 0, 77], 12, 1, "bfloat16", 200, 400),
+    ([2500, 640], 4, 4, "float32", 0, 300),
+    ([1030, 5, 0, 65, 64], 8, 8, "bfloat16", 0, 20),
+    ([1030, 5, 0, 65, 64], 32, 2, "float32", 300, 20),
+])
+def test_attention_of_one_token_however_the_work_is_cut(env, lens, Hq, Hk, dt, window, cols):
+    """Lines of tiles cut into runs, and items shared by the CTAs of a cluster: the block table's width decides."""
+    torch, kda = env
+    dt = getattr(torch, dt)
+    rng = np.random.default_rng(cols + Hq)
+    cache, tb, lt, table = _filled(torch, kda, rng, lens, 64, Hk, 128, cols=cols)
+    B = len(lens)
+    q = _dev(torch, 2 * rng.normal(size=(B, Hq, 128))).to(dt)
+    for width in (cols, max(-(-n // 64) for n in lens)):
+        out, lse = torch.full_like(q, 7.0), torch.full((B, Hq), 7.0, device="cuda")
+        kda.kda_kv4_attention(q, cache, tb[:, :width], lt, out, window=window, lse=lse)
+        kda.kda_sync_status()
+        _check(torch, out, lse, q, cache, table, lens, [1] * B, 128 ** -0.5, True, window)
+
+
 @pytest.mark.parametrize("Hq,Hk,new,dt", [(8, 2, None, "bfloat16"), (12, 1, None, "bfloat16"), (4, 2, 5, "float32"),
                                           (8, 2, 40, "bfloat16"), (40, 1, None, "bfloat16")])
 def test_attention_many_sequences(env, Hq, Hk, new, dt):
@@ -601,9 +623,10 @@ def test_calls_side_by_side(env):
     torch, kda = env
     rng = np.random.default_rng(31)
     lens, Hq, Hk, D = [2000, 900], 16, 2, 128
-    cache, tb, lt, table = _filled(torch, kda, rng, lens, 64, Hk, D)
+    cache, tb, lt, table = _filled(torch, kda, rng, lens, 64, Hk, D, cols=200)
     qs = [_dev(torch, rng.normal(size=(2, Hq, D))).to(torch.bfloat16) for _ in range(2)]
-    size = kda.kda_kv4_attention_workspace_bytes(2, 2, Hq, Hk, D, torch.bfloat16)
+    size = kda.kda_kv4_attention_workspace_bytes(2, 2, Hq, Hk, D, 64, tb.shape[1], False, torch.bfloat16)
+    assert size > 0
     spaces = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
     streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.empty_like(q) for q in qs]
     lses = [torch.empty((2, Hq), device="cuda") for _ in qs]

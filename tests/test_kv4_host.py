@@ -122,8 +122,11 @@ def test_sizes(kda):
     assert np.prod(kda.kda_kv4_cache_shape(10, 8, 64, 128)) == kda.kda_kv4_cache_bytes(10, 8, 64, 128)
     assert kda.kda_kv4_cache_bytes(10, 8, 40, 128) == 0 and kda.kda_kv4_cache_bytes(-1, 8, 64, 128) == 0
     size = kda.kda_kv4_attention_workspace_bytes
-    assert size(1, 1, 8, 8, 128, BF) > 0 and size(1, 1, 8, 8, 64, F32) > 0
-    assert size(0, 1, 8, 8, 128, BF) == 0 and size(1, 1, 8, 3, 128, BF) == 0 and size(1, 1, 8, 8, 32, BF) == 0
+    assert size(64, 64, 96, 8, 128, 64, 128, False, BF) > 0 and size(64, 64, 8, 8, 64, 64, 1000, False, F32) > 0
+    assert size(1, 1, 32, 8, 128, 64, 64, False, BF) == 0  # short enough for one item a cluster
+    assert size(1, 4000, 32, 8, 128, 64, 64, True, BF) > size(64, 64, 96, 8, 128, 64, 128, False, BF)
+    assert size(0, 1, 8, 8, 128, 64, 9, False, BF) == 0 and size(1, 1, 8, 3, 128, 64, 9, False, BF) == 0
+    assert size(1, 1, 8, 8, 32, 64, 9, False, BF) == 0 and size(1, 1, 8, 8, 64, 48, 9, False, BF) == 0
 
 
 # ---------------------------------------------------------------- the binding
