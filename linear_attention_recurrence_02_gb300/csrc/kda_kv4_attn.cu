@@ -626,58 +626,85 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
     }
 }
 
-// One row of the item that goes on behind run blockIdx.x: its pieces, in the runs' order within each of four
-// warps and then the warps'.
+// Up to eight rows of the item that goes on behind run blockIdx.x, a warp each; where the item has many pieces the
+// eight warps share a row's after another. Either way in an order that the sizes alone decide.
 template <int D, typename T, int R>
-__global__ void __launch_bounds__(128) kv4_attn_join_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int V = D / 32;
-    __shared__ float sum[4][D], ls[4];
+__global__ void __launch_bounds__(256) kv4_attn_join_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int V = D / 32, MANY = 12;
+    __shared__ float sum[8][D], ls[8];
     dependent_launch();
     const Joint x = a.joint[blockIdx.x];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
-    const int rr = x.block * R + row, i = a.by_group(rr);
-    if (x.pieces == 0 || i >= x.n) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = 8 * blockIdx.y;
+    const int rows = x.n * a.group - x.block * R - row0;  // from row0 on
+    if (x.pieces == 0 || rows <= 0) return;
     // the first piece is its run's second, all others their run's first
-    auto at = [&](int p) { return ((int64_t)(blockIdx.x + p) * 2 + (p == 0)) * R + row; };
-    float m = -INFINITY;
-    for (int p = lane; p < x.pieces; p += 32) m = fmaxf(m, a.ml[at(p)].x);
+    auto at = [&](int p, int row) { return ((int64_t)(blockIdx.x + p) * 2 + (p == 0)) * R + row; };
+    auto pieces_of = [&](int row, int first, int step, float &m, float &l, float (&v)[V]) {
+        m = -INFINITY;
+        for (int p = lane; p < x.pieces; p += 32) m = fmaxf(m, a.ml[at(p, row)].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, v[V];
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        l = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = 0.f;
+        for (int e = 0; e < V; ++e) v[e] = 0.f;
 #pragma unroll 4
-    for (int p = warp; p < x.pieces; p += 4) {
-        const float2 y = a.ml[at(p)];
-        const float f = y.x == -INFINITY ? 0.f : exp2_fast(y.x - m);
-        l = fmaf(y.y, f, l);
-        float w[V];
-        const float *from = a.part + at(p) * D + V * lane;
-        if constexpr (V == 4) {
-            const float4 z = *reinterpret_cast<const float4 *>(from);
-            w[0] = z.x; w[1] = z.y; w[2] = z.z; w[3] = z.w;
-        } else {
-            const float2 z = *reinterpret_cast<const float2 *>(from);
-            w[0] = z.x; w[1] = z.y;
+        for (int p = first; p < x.pieces; p += step) {
+            const float2 y = a.ml[at(p, row)];
+            const float f = y.x == -INFINITY ? 0.f : exp2_fast(y.x - m);
+            l = fmaf(y.y, f, l);
+            const float *from = a.part + at(p, row) * D + V * lane;
+            float w[V];
+            if constexpr (V == 4) {
+                const float4 z = *reinterpret_cast<const float4 *>(from);
+                w[0] = z.x; w[1] = z.y; w[2] = z.z; w[3] = z.w;
+            } else {
+                const float2 z = *reinterpret_cast<const float2 *>(from);
+                w[0] = z.x; w[1] = z.y;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = fmaf(w[e], f, v[e]);
         }
+    };
+    auto put = [&](int row, float m, float l, const float (&v)[V]) {  // channels V lane ..
+        const int rr = x.block * R + row, i = a.by_group(rr), head = x.h * a.group + rr - i * a.group;
+        const int64_t t = x.t0 + i;
+        T *to = static_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D + V * lane;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = fmaf(w[e], f, v[e]);
+        for (int e = 0; e < V; ++e) Elem<T>::store(to + e, v[e] * inv);
+        if (lane == 0 && a.lse) a.lse[t * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+    };
+    float m, l, v[V];
+    if (x.pieces <= MANY) {
+        if (warp >= rows || row0 + warp >= R) return;
+        pieces_of(row0 + warp, 0, 1, m, l, v);
+        put(row0 + warp, m, l, v);
+        return;
     }
+    for (int r = 0; r < min(min(rows, 8), R - row0); ++r) {
+        pieces_of(row0 + r, warp, 8, m, l, v);
 #pragma unroll
-    for (int e = 0; e < V; ++e) sum[warp][V * lane + e] = v[e];
-    if (lane == 0) ls[warp] = l;
-    __syncthreads();
-    l = ls[0] + ls[1] + ls[2] + ls[3];
-    const int head = x.h * a.group + rr - i * a.group;
-    const int64_t t = x.t0 + i;
-    if (threadIdx.x < D)
-        Elem<T>::store(static_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D + threadIdx.x,
-                       l == 0.f ? 0.f : (sum[0][threadIdx.x] + sum[1][threadIdx.x] + sum[2][threadIdx.x] + sum[3][threadIdx.x]) / l);
-    if (threadIdx.x == 0 && a.lse) a.lse[t * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+        for (int e = 0; e < V; ++e) sum[warp][V * lane + e] = v[e];
+        if (lane == 0) ls[warp] = l;
+        __syncthreads();
+        if (warp == 0) {
+            l = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                l += ls[w];
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] += sum[w][V * lane + e];
+            }
+            put(row0 + r, m, l, v);
+        }
+        __syncthreads();
+    }
 }
 
 template <int D, typename T, int R> kda_status launch_join(const AttnArgs &a, cudaStream_t s) {
-    launch_dependent(kv4_attn_join_kernel<D, T, R>, dim3(a.ctas - 1, R), dim3(128), 0, s, a);
+    launch_dependent(kv4_attn_join_kernel<D, T, R>, dim3(a.ctas - 1, (R + 7) / 8), dim3(256), 0, s, a);
     return check_launch("kv4_attn_join_kernel");
 }
 

@@ -12,7 +12,8 @@
 //   group 2      codes from global memory through registers, expanded to bf16 (exact), into the 128-byte
 //                swizzled tiles that the tensor cores read: keys K-major, values as they come (MN-major)
 //   group 3      a warp issues S_i = Q_i K^T and O_i += P_i V for the two row tiles in turn: while one
-//                tile's softmax runs, the tensor cores have the other's products
+//                tile's softmax runs, the tensor cores have the other's products. Where a block has one row
+//                tile only, the two groups take its even and odd tiles of cached tokens and join their outputs
 //
 // TMEM: S_0, S_1 (128 columns each, P_i in the first 64 of S_i), O_0, O_1 (D columns each).
 #include <algorithm>
@@ -52,12 +53,13 @@ template <int D> struct Smem {
     static constexpr int HALF = 128 * 128;             // 128 rows x 64 channels
     static constexpr int TILE_BYTES = 128 * D * 2;
     static constexpr int Q = 0, K = 2 * TILE_BYTES, V = K + 2 * TILE_BYTES, BAR = V + 2 * TILE_BYTES;
-    static constexpr int PLACES = BAR + 256, PARTS = PLACES + 16 * 64, BYTES = PARTS + 16 * 128 + 1024;
+    static constexpr int OTHER = BAR + 256, PLACES = OTHER + 1024, PARTS = PLACES + 16 * 64, BYTES = PARTS + 16 * 128 + 1024;
 };
 static_assert(sizeof(Place) <= 64 && sizeof(Part) <= 64, "room for a place");
 
 struct Bars {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2], other_done,
+        other_read;
     uint32_t taddr;
 };
 
@@ -146,6 +148,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // working ones (a clock read and compared each time made a third of all instructions). NS > 0: nanoseconds
 // between the tries of a warp that is not in a hurry.
 template <int NS> __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+    uint32_t there;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(there)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (there) return true;
     for (uint32_t n = NS > 0 ? WAIT_TRIES / 8 : WAIT_TRIES; n > 0; --n) {
         if (tc::mbar_try_wait(bar, parity)) return true;
         if constexpr (NS > 0) __nanosleep(NS);
@@ -239,6 +250,8 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
     Bars *bar = reinterpret_cast<Bars *>(sm + Sm::BAR);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        mbar_init(&bar->other_done, 4);
+        mbar_init(&bar->other_read, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar->k_full + i, 4);
             mbar_init(bar->v_full + i, 4);
@@ -364,23 +377,23 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
         const int i = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tbase + lanes + 128 * i, to = tbase + lanes + 256 + D * i;
-        int done = 0;  // tiles of this row tile so far
+        int done = 0;    // tiles of this stream so far
+        int joined = 0;  // items whose streams were joined so far
         const float slack = SLACK / a.scale_log2;
         const Part *at_hand = nullptr;
         if (work) at_hand = advance();
         while (at_hand && at_hand->there) {
             const Part &g = *at_hand;
             const Part *next = advance();
-            const bool mine = g.n * a.group - g.block * R > 128 * i;
-            const int rr = g.block * R + 128 * i + row, ti = a.by_group(rr), pos = g.len - g.n + ti;
+            const bool alone = g.n * a.group - g.block * R <= 128;  // one row tile: the streams share its cached tokens
+            const int rr = g.block * R + (alone ? 0 : 128 * i) + row, ti = a.by_group(rr), pos = g.len - g.n + ti;
             const int hi = a.causal ? min(pos + 1, g.len) : g.len, lo = a.window > 0 ? pos - a.window + 1 : 0;
             const int i0 = a.by_group(g.block * R), i1 = a.by_group(min(g.n * a.group - 1, g.block * R + R - 1));
             const int whole_hi = a.causal ? min(g.len - g.n + i0 + 1, g.len) : g.len;
             const int whole_lo = a.window > 0 ? g.len - g.n + i1 - a.window + 1 : 0;
-            const int first = g.first;
+            const int first = g.first + (alone ? i : 0), step = alone ? 2 : 1;
             float neg = 0.f, top = -INFINITY, l = 0.f;
-            if (mine)
-                for (int tile = g.first, last = g.last; tile < last; ++tile) {
+            for (int tile = first, last = g.last; tile < last; tile += step) {
                     wait(bar->s_full + i, done & 1);
                     tc_fence_after();
                     const int tok0 = tile * TILE;
@@ -472,15 +485,35 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                     l += sum.x + sum.y;
                     ++done;
                 }
-            if (mine) {
-                if (l != l && top == -INFINITY) top = 0.f;  // scores that are all NaN leave no maximum
-                const float mx = top == -INFINITY ? -INFINITY : -neg;
-                const bool any = g.first < g.last;
-                if (any) {
-                    wait(bar->pv_done + i, (done - 1) & 1);
+            if (l != l && top == -INFINITY) top = 0.f;  // scores that are all NaN leave no maximum
+            float mx = top == -INFINITY ? -INFINITY : -neg;
+            const bool any = first < g.last;
+            if (any) {
+                wait(bar->pv_done + i, (done - 1) & 1);
+                tc_fence_after();
+            }
+            float2 *other = reinterpret_cast<float2 *>(sm + Sm::OTHER);
+            if (alone && i == 1) {  // the first group joins both streams
+                other[row] = make_float2(mx, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->other_done);
+                wait(&bar->other_read, joined++ & 1);
+            } else {
+                bool both = false;
+                float f0 = 1.f, f1 = 0.f;
+                if (alone) {
+                    wait(&bar->other_done, joined++ & 1);
                     tc_fence_after();
+                    both = g.first + 1 < g.last;
+                    const float2 x = other[row];
+                    const float m = fmaxf(mx, x.x);
+                    f0 = mx == -INFINITY ? 0.f : exp2_fast(mx - m);
+                    f1 = x.x == -INFINITY ? 0.f : exp2_fast(x.x - m);
+                    l = l * f0 + x.y * f1;
+                    mx = m;
                 }
-                const int64_t at = ((int64_t)blockIdx.x * 2 + g.piece) * R + 128 * i + row;
+                const int64_t at = ((int64_t)blockIdx.x * 2 + g.piece) * R + (alone ? 0 : 128 * i) + row;
                 const int head = g.h * a.group + rr - ti * a.group;
                 const bool live = ti < g.n;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -494,6 +527,14 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0;
+                    }
+                    if (both) {
+                        uint32_t o1[32];
+                        tmem_ld32(to + D + 32 * c, o1);
+                        landed(o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
                     }
                     if (live && g.piece >= 0) {
                         float4 *p = reinterpret_cast<float4 *>(a.part + at * D + 32 * c);
@@ -516,6 +557,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                 }
                 __syncwarp();
                 tc_fence_before();
+                if (alone && lane == 0) mbar_arrive(&bar->other_read);
                 if (live) {
                     if (g.piece >= 0) a.ml[at] = make_float2(mx, l);
                     else if (a.lse) a.lse[(g.t0 + ti) * a.Hq + head] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.69314718f;
@@ -547,11 +589,11 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             }
         };
         settle();
+        // Blocks w and w + 4 of a tile. One behind the sequence's end, whose page need not exist, is read from the
+        // tile's first page; a page outside the cache is read as page 0 and flagged. Three tiles are under way ahead of
+        // the one that is expanded: one whose codes are on their way to registers, one on its way to L2, one whose
+        // pages are looked up.
         bool bad = false;
-        const uint8_t *base[2];
-        int tok[2], len = 0;      // of the tile whose codes are in registers
-        // Blocks w and w + 4 of the next tile. One behind the sequence's end, whose page need not exist, is read
-        // from the tile's first page; a page outside the cache is read as page 0 and flagged.
         int page[2] = {0, 0};
         auto look = [&]() {
 #pragma unroll
@@ -560,46 +602,55 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                 page[x] = row[(t < seq_len ? t : at * TILE) >> a.c.page_shift];
             }
         };
-        auto take = [&]() {  // that tile's addresses; on to the one after it
+        struct Tile {
+            const uint8_t *base[2];
+            int tok, len;  // the first block's first token, the sequence's length
+            bool there;
+        };
+        auto aim = [&]() {  // the tile whose pages were looked up; on to the one behind it
+            Tile t;
+            t.there = there;
+            t.tok = at * TILE + 16 * w;
+            t.len = seq_len;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                tok[x] = at * TILE + 16 * (w + 4 * x);
                 const bool out = (uint32_t)page[x] >= (uint32_t)a.c.pages;
-                bad |= out;
-                const int block = (tok[x] & ((1 << a.c.page_shift) - 1)) >> 4;
-                base[x] = a.c.data + ((((int64_t)(out ? 0 : page[x]) * a.c.Hk + h) << (a.c.page_shift - 4)) + block) * FB;
+                bad |= out && there;
+                const int block = ((t.tok + 64 * x) & ((1 << a.c.page_shift) - 1)) >> 4;
+                t.base[x] = a.c.data + ((((int64_t)(out ? 0 : page[x]) * a.c.Hk + h) << (a.c.page_shift - 4)) + block) * FB;
             }
-            len = seq_len;
-            ++at;
-            settle();
-            if (there) look();
+            if (there) {
+                if (lane < 2) prefetch_l2_bulk(lane ? t.base[1] : t.base[0], FB);
+                ++at;
+                settle();
+                if (there) look();
+            }
+            return t;
         };
+        if (there) look();
+        Tile load = aim(), next = aim();
         Raw<D> raw[2];
         auto load_keys = [&](int x) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                ldg<G>(raw[x].k[y], base[x] + (r0 + 8 * y) * (D / 2) + j * (D / 8));
-                ldg<G / 2>(raw[x].ks[y], base[x] + Format<D>::KS + (r0 + 8 * y) * (D / 16));
+                ldg<G>(raw[x].k[y], load.base[x] + (r0 + 8 * y) * (D / 2) + j * (D / 8));
+                ldg<G / 2>(raw[x].ks[y], load.base[x] + Format<D>::KS + (r0 + 8 * y) * (D / 16));
             }
         };
         auto load_values = [&](int x) {
-            const uint8_t *p = base[x] + Format<D>::V + pr * D + ((2 * j + 2 * pr) & 7) * (D / 8);
+            const uint8_t *p = load.base[x] + Format<D>::V + pr * D + ((2 * j + 2 * pr) & 7) * (D / 8);
             ldg<G>(raw[x].v[0], p);
             ldg<G>(raw[x].v[1], p + D / 8);
-            ldg<G>(raw[x].vs, base[x] + Format<D>::VS + pr * (D / 8));
+            ldg<G>(raw[x].vs, load.base[x] + Format<D>::VS + pr * (D / 8));
         };
-        bool have = there;
-        if (have) {
-            look();
-            take();
+        if (load.there)
             for (int x = 0; x < 2; ++x) {
                 load_keys(x);
                 load_values(x);
             }
-        }
-        for (int c = 0; have; ++c) {
+        for (int c = 0; load.there; ++c) {
             const int st = c & 1, ph = (c >> 1) & 1;
-            const int tok_v[2] = {tok[0], tok[1]}, len_v = len;
+            const int tok_v = load.tok, len_v = load.len;
             wait(bar->k_empty + st, ph ^ 1);
             uint8_t *kt = sm + Sm::K + st * Sm::TILE_BYTES, *vt = sm + Sm::V + st * Sm::TILE_BYTES;
 #pragma unroll
@@ -631,11 +682,11 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar->k_full + st);
-            have = there;
-            if (have) {
-                take();
+            load = next;
+            if (load.there) {
                 load_keys(0);
                 load_keys(1);
+                next = aim();
             }
             wait(bar->v_empty + st, ph ^ 1);
 #pragma unroll
@@ -643,7 +694,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = 16 * (w + 4 * x) + 2 * pr + e;
-                    const bool past = tok_v[x] + 2 * pr + e >= len_v;
+                    const bool past = tok_v + 64 * x + 2 * pr + e >= len_v;
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
                         uint32_t s2 = prmt(raw[x].vs[gr], 0, e ? 0x3232 : 0x1010), f[4];
@@ -657,7 +708,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar->v_full + st);
-            if (have) {
+            if (load.there) {
                 load_values(0);
                 load_values(1);
             }
@@ -670,11 +721,11 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             int c = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // tiles, row tiles loaded, factors taken
             const uint64_t q0 = sdesc_sw128(sbase + Sm::Q, 16, 1024), k0 = sdesc_sw128(sbase + Sm::K, 16, 1024),
                            v0 = sdesc_sw128(sbase + Sm::V, Sm::HALF, 1024);
-            auto scores = [&](int i, int st) {
+            auto scores = [&](int i, int rows, int st) {  // of row tile `rows`
                 if (!ok) return;
 #pragma unroll
                 for (int half = 0; half < D / 64; ++half)
-                    mma4_ss(tbase + 128 * i, q0 + (i * Sm::TILE_BYTES + half * Sm::HALF) / 16,
+                    mma4_ss(tbase + 128 * i, q0 + (rows * Sm::TILE_BYTES + half * Sm::HALF) / 16,
                             k0 + (st * Sm::TILE_BYTES + half * Sm::HALF) / 16, ID_S, half > 0);
                 commit(bar->s_full + i);
             };
@@ -691,34 +742,61 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                 const int nt = g->last - g->first, rows = g->n * a.group - g->block * R;
                 after = advance();
                 if (nt <= 0) continue;
-                const int tiles = rows > 128 ? 2 : 1;
+                if (rows <= 128) {
+                    // One row tile: its even and odd tiles of cached tokens are two streams with an output each, so that
+                    // here too one's products run while the other's factors are formed.
+                    wait(bar->q_full, nq[0]++ & 1);
+                    for (int n = 0; n < min(nt, 2); ++n) {
+                        const int st = (c + n) & 1;
+                        wait(bar->k_full + st, ((c + n) >> 1) & 1);
+                        scores(n, 0, st);
+                        release(bar->k_empty + st);
+                    }
+                    if (nt <= 2) release(bar->q_empty);
+                    for (int n = 0; n < nt; ++n, ++c) {
+                        const int st = c & 1, i = n & 1, turn = i ? np[1]++ : np[0]++;
+                        wait(bar->v_full + st, (c >> 1) & 1);
+                        wait(bar->p_half + i, turn & 1);
+                        tc_fence_after();
+                        outputs(i, st, 0, n > 1);
+                        wait(bar->p_full + i, turn & 1);
+                        tc_fence_after();
+                        outputs(i, st, 1, true);
+                        release(bar->v_empty + st);
+                        if (n + 2 < nt) {
+                            wait(bar->k_full + st, ((c + 2) >> 1) & 1);
+                            scores(i, 0, st);
+                            release(bar->k_empty + st);
+                            if (n + 3 == nt) release(bar->q_empty);
+                        }
+                    }
+                    continue;
+                }
                 wait(bar->k_full + (c & 1), (c >> 1) & 1);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (i < tiles) {
-                        wait(bar->q_full + i, nq[i]++ & 1);
-                        scores(i, c & 1);
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    wait(bar->q_full + i, nq[i]++ & 1);
+                    scores(i, i, c & 1);
+                }
                 release(bar->k_empty + (c & 1));
                 if (nt == 1)
-                    for (int i = 0; i < tiles; ++i) release(bar->q_empty + i);
+                    for (int i = 0; i < 2; ++i) release(bar->q_empty + i);
                 for (int n = 0; n < nt; ++n, ++c) {
                     const int st = c & 1, s1 = (c + 1) & 1;
                     const bool next = n + 1 < nt;
                     wait(bar->v_full + st, (c >> 1) & 1);
                     if (next) wait(bar->k_full + s1, ((c + 1) >> 1) & 1);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (i < tiles) {
-                            wait(bar->p_half + i, np[i] & 1);
-                            tc_fence_after();
-                            outputs(i, st, 0, n > 0);
-                            wait(bar->p_full + i, np[i]++ & 1);
-                            tc_fence_after();
-                            outputs(i, st, 1, true);
-                            if (next) scores(i, s1);
-                            if (n + 2 == nt) release(bar->q_empty + i);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        wait(bar->p_half + i, np[i] & 1);
+                        tc_fence_after();
+                        outputs(i, st, 0, n > 0);
+                        wait(bar->p_full + i, np[i]++ & 1);
+                        tc_fence_after();
+                        outputs(i, st, 1, true);
+                        if (next) scores(i, i, s1);
+                        if (n + 2 == nt) release(bar->q_empty + i);
+                    }
                     release(bar->v_empty + st);
                     if (next) release(bar->k_empty + s1);
                 }
