@@ -610,8 +610,8 @@ kda_status kda_chunk_prefill_noalloc(const void *q, const void *k, const void *v
  *   positions int64 [T], inv_freq fp64 [R/2] radians a position; unused with R = 0.
  *            The product is formed modulo a full turn in integers: an angle is as
  *            exact at position 2^31 as at 1. Frequencies are finite.
- * Requires T >= 0, D in {16,32,64,128}, R a multiple of 16 up to D; strides
- * multiples of 16 bytes. A row whose mean square plus eps is zero normalises to
+ * Requires T in 0 .. 2^31 - 1, at most 32768 heads of either kind, D in
+ * {16,32,64,128}, R a multiple of 16 up to D; strides multiples of 16 bytes. A row whose mean square plus eps is zero normalises to
  * zero. A programmatic dependent launch that waits for the kernel before it.
  */
 kda_status kda_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const float *q_weight,
@@ -647,7 +647,8 @@ kda_status kda_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_o
  *               are left as they are. NULL: one new token each, T = B
  * A sequence of length 0 is padding: nothing is written for it, and its rows of
  * kda_kv4_attention's out are zero. Lengths and offsets may pass 32 bits where
- * the products of sizes do; table_cols * page_size is below 2^31.
+ * the products of sizes do; table_cols * page_size is at most 2^31 - 256, B at most
+ * 2^30, T at most 2^31 - 1 (for attention T * Hq at most 2^31 - 256) and Hk at most 32768.
  * A page or length outside the cache and cu_seqlens out of order are found on
  * the device: nothing outside the tensors is touched, the rows concerned are
  * skipped or meaningless, and kda_sync_status reports KDA_ERR_DEVICE_CHECK.

@@ -12,16 +12,16 @@
 // a scale lie in 16 neighbouring lanes and the block's maximum is four
 // shuffles; the row never leaves the registers between its sum of squares
 // and its codes.
+//
+// Both are programmatic dependent launches that wait for the kernel before
+// them first thing, then let the kernel behind them start: a kda_fp8_linear
+// that reads their output sets itself up and prefetches its weights meanwhile.
 #include <string>
 
 #include "kda_fp8.cuh"
 #include "kda_prefill.cuh"
 
 namespace kda {
-
-// Both are programmatic dependent launches that wait for the kernel before
-// them first thing, then let the kernel behind them start: a kda_fp8_linear
-// that reads their output sets itself up and prefetches its weights meanwhile.
 
 // ---------------------------------------------------------------- residual add + RMSNorm
 // A row of N channels is held by blockDim.x threads, VPT vectors of 8

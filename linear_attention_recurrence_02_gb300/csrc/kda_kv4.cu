@@ -134,9 +134,9 @@ __global__ void __launch_bounds__(NT) kv4_read_kernel(Cache c, T *k, T *v, int64
 kda_status check_cache(const void *cache, const int32_t *table, const int64_t *lens, const int64_t *cu, int B,
                        int64_t T, int Hk, int D, int page_size, int64_t pages, int cols, int64_t table_stride,
                        kda_dtype dtype, Cache &c) {
-    if (B < 0) return invalid("B must be >= 0");
-    if (T < 0) return invalid("T must be >= 0");
-    if (Hk < 1) return invalid("Hk must be >= 1");
+    if (B < 0 || B > 1 << 30) return invalid("B must be in 0 .. 2^30");
+    if (T < 0 || T > 0x7fffffffLL) return invalid("T must be in 0 .. 2^31 - 1");
+    if (Hk < 1 || Hk > 32768) return invalid("Hk must be in 1 .. 32768");
     if (D != 64 && D != 128) return invalid("D must be 64 or 128");
     if (dtype != KDA_F32 && dtype != KDA_BF16) return invalid("dtype must be KDA_F32 or KDA_BF16");
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)

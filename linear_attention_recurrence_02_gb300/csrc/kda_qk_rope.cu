@@ -136,7 +136,10 @@ __device__ __forceinline__ void norm_and_turn(float2 (&x)[4], const float *w, co
 // rows (queries' heads, then keys') (blockIdx.y * UP + u) * slots + its slot. ONE: a single token, with no division before
 // the loads. 8192 tokens, 64 + 8 heads of 128 in bf16: 59 us, 5.1 TB/s (with the division 71; with 40 registers 67,
 // with 59 as the compiler likes it 61, and 54 instead of 45 for 4096 tokens of 96 + 8 heads; tokens streamed through
-// shared memory by persistent CTAs 71: the rows' arithmetic needs more warps than that leaves).
+// shared memory by persistent CTAs 71: the rows' arithmetic needs more warps than that leaves; several tokens one after
+// another in a CTA, the next one's rows loaded ahead, 62; lanes of two 16-byte vectors, half as many, 65). What bounds it
+// is a CTA's chain of loads, angles, barrier and stores with the warps that registers allow: fp32 rows, twice the bytes
+// behind each angle, move at 6.5 TB/s.
 template <int D, typename T, bool INTER, int UP, bool ONE>
 __global__ void __maxnreg__(sizeof(T) == 2 ? 48 : 64) qk_norm_rope_kernel(const RopeArgs a, int64_t T_, int many, int slots) {
     constexpr int LPR = D / 8;

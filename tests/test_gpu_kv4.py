@@ -393,6 +393,54 @@ def test_attention_many_sequences(env, Hq, Hk, new, dt):
     _check(torch, out, lse, q, cache, table, lens, counts, D ** -0.5, True, 0)
 
 
+@pytest.mark.parametrize("lens,new,Hq,D,window", [
+    ([6000], [1], 20, 128, 0),           # one row tile, its tokens shared by as many CTAs as there are
+    ([6000, 0, 9], [1, 0, 1], 32, 64, 1500),
+    ([5000], [9], 24, 128, 0),           # two row tiles
+    ([4000, 77], [3, 2], 48, 64, 0),
+])
+def test_attention_of_many_pieces(env, lens, new, Hq, D, window):
+    """Few blocks of many rows over long sequences: an item in more pieces than a warp joins by itself."""
+    torch, kda = env
+    rng = np.random.default_rng(Hq + D)
+    cache, tb, lt, table = _filled(torch, kda, rng, lens, 128, 1, D)
+    q = _dev(torch, 2 * rng.normal(size=(sum(new), Hq, D))).to(torch.bfloat16)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    cu = _dev(torch, np.concatenate([[0], np.cumsum(new)]))
+    kda.kda_kv4_attention(q, cache, tb, lt, out, cu_seqlens=cu, window=window, lse=lse)
+    kda.kda_sync_status()
+    _check(torch, out, lse, q, cache, table, lens, new, D ** -0.5, True, window)
+
+
+def test_two_graphs_share_a_workspace(env):
+    """Captured calls of different sizes that use one workspace in turn, its bytes arbitrary before."""
+    torch, kda = env
+    rng = np.random.default_rng(51)
+    size, calls = 0, []
+    for lens, new, Hq, Hk in (([3000, 40], [1, 1], 8, 1), ([700, 1500], [100, 3], 16, 2), ([2600], [1], 40, 1)):
+        cache, tb, lt, table = _filled(torch, kda, rng, lens, 64, Hk, 128, cols=200)
+        q = _dev(torch, 2 * rng.normal(size=(sum(new), Hq, 128))).to(torch.bfloat16)
+        cu = None if new == [1] * len(lens) else _dev(torch, np.concatenate([[0], np.cumsum(new)]))
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        calls.append((q, cache, tb, lt, out, cu, lse, table, lens, new))
+        size = max(size, kda.kda_kv4_attention_workspace_bytes(len(lens), sum(new), Hq, Hk, 128, 64, tb.shape[1],
+                                                               cu is not None, torch.bfloat16))
+    ws, graphs = torch.full((size,), 255, dtype=torch.uint8, device="cuda"), []
+    for q, cache, tb, lt, out, cu, lse, *_ in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        kda.kda_kv4_attention(q, cache, tb, lt, out, cu_seqlens=cu, lse=lse, workspace=ws)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graphs[-1]):
+            kda.kda_kv4_attention(q, cache, tb, lt, out, cu_seqlens=cu, lse=lse, workspace=ws)
+    for c in calls:
+        c[4].fill_(7.0)
+    for g in graphs + graphs[::-1]:
+        g.replay()
+    kda.kda_sync_status()
+    for q, cache, tb, lt, out, cu, lse, table, lens, new in calls:
+        _check(torch, out, lse, q, cache, table, lens, new, 128 ** -0.5, True, 0)
+
+
 @pytest.mark.parametrize("Hq,new,dt", [(2, 1, "bfloat16"), (4, 40, "bfloat16"), (2, 3, "float32")])
 def test_attention_strides_and_scale(env, Hq, new, dt):
     torch, kda = env

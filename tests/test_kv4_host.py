@@ -80,6 +80,7 @@ _SHARED = [
     (dict(cols=(1 << 31) // 64), "columns"), (dict(ts=3), "table_stride"), (dict(cu=None), "one token for each"),
     (dict(B=0), "without a sequence"), (dict(cache=None), "cache is NULL"), (dict(cache=0x100008), "cache is not 16"),
     (dict(table=None), "block_table is NULL"), (dict(lens=0x300008), "lens is not 16"), (dict(cu=0x400004), "cu_seqlens"),
+    (dict(T=1 << 31), "T must be"), (dict(B=(1 << 30) + 1), "B must be"), (dict(Hk=32769, Hq=32769), "Hk must be"),
 ]
 
 
