@@ -1,7 +1,8 @@
 """Run one workload of the library a fixed number of times, for profiler captures.
 
     python -m linear_attention_recurrence_02_gb300.profile_cases CASE [--B 64] [--T 4096] [--H 96]
-        [--gate channel|head|none] [--dtype bf16|f32] [--N 4096] [--K 4096] [--warmup 3] [--reps 2]
+        [--gate channel|head|none] [--dtype bf16|f32] [--N 4096] [--K 4096] [--Hk 8] [--L 8192]
+        [--warmup 3] [--reps 2]
 
 Every call goes through the C ABI exactly as a user's does. Inputs are drawn
 on the device by a seeded torch generator with the workloads' distributions
@@ -20,6 +21,11 @@ each (the prefill adds no other launch for one sequence). Cases:
   epilogue_fp8    the same with its output in 8 bits (kda_gated_rmsnorm_fp8)
   add_norm_fp8    residual addition + RMSNorm in 8 bits over T tokens of K channels (kda_add_rmsnorm_fp8)
   linear_fp8      the 8-bit product of T tokens of K channels with N features (kda_fp8_linear)
+  qk_norm_rope    norms and rotation of T tokens' H query and Hk key heads (kda_qk_norm_rope)
+  kv4_append      T tokens of Hk heads quantised into the 4-bit cache (kda_kv4_append)
+  kv4_read        the same tokens read back (kda_kv4_read)
+  kv4_attn_step   attention of one new token each of B sequences of L cached tokens, H over Hk heads (kda_kv4_attention)
+  kv4_attn_prompt the same for the last T tokens of one sequence of L
 """
 from __future__ import annotations
 
@@ -34,7 +40,8 @@ from linear_attention_recurrence_02_gb300 import kda
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["decode", "decode_epi", "decode_unfused", "shortconv_step", "prefill",
-                                     "shortconv_prefill", "epilogue", "epilogue_fp8", "add_norm_fp8", "linear_fp8"])
+                                     "shortconv_prefill", "epilogue", "epilogue_fp8", "add_norm_fp8", "linear_fp8",
+                                     "qk_norm_rope", "kv4_append", "kv4_read", "kv4_attn_step", "kv4_attn_prompt"])
     ap.add_argument("--B", type=int, default=64)
     ap.add_argument("--T", type=int, default=4096)
     ap.add_argument("--H", type=int, default=96)
@@ -43,6 +50,8 @@ def main(argv=None) -> int:
     ap.add_argument("--dtype", default="bf16", choices=["bf16", "f32"])
     ap.add_argument("--N", type=int, default=4096)
     ap.add_argument("--K", type=int, default=4096)
+    ap.add_argument("--Hk", type=int, default=8)
+    ap.add_argument("--L", type=int, default=8192)
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--reps", type=int, default=2)
     a = ap.parse_args(argv)
@@ -114,6 +123,38 @@ def main(argv=None) -> int:
                 kda.kda_add_rmsnorm_fp8(x, nw, codes, scales, residual=r, sum_out=so)
             else:
                 kda.kda_gated_rmsnorm_fp8(x, og, nw, codes.view(T, H, D), scales)
+    elif a.case == "qk_norm_rope":
+        dt = bf if a.dtype == "bf16" else torch.float32
+        q, k = rnd(T, H, D).to(dt), rnd(T, a.Hk, D).to(dt)
+        qo, ko, qw, kw = torch.empty_like(q), torch.empty_like(k), rnd(D).abs(), rnd(D).abs()
+        pos = torch.arange(T, device=dev)
+        freq = 10000.0 ** (-torch.arange(D // 2, dtype=torch.float64, device=dev) / (D // 2))
+
+        def call():
+            kda.kda_qk_norm_rope(q, k, qo, ko, pos, freq, qw, kw)
+    elif a.case in ("kv4_append", "kv4_read", "kv4_attn_step", "kv4_attn_prompt"):
+        # a prompt's tokens are one sequence of L, a step's sequences B of them; pages of 64 tokens in any order
+        dt = bf if a.dtype == "bf16" else torch.float32
+        n, L = (B, a.L) if a.case == "kv4_attn_step" else (1, a.L if a.case == "kv4_attn_prompt" else T)
+        cols = (L + 63) // 64
+        table = torch.randperm(n * cols, generator=gen, device=dev).to(torch.int32).view(n, cols)
+        cache = torch.empty(kda.kda_kv4_cache_shape(n * cols, a.Hk, 64, D), dtype=torch.uint8, device=dev)
+        k, v = rnd(L, a.Hk, D).to(dt), rnd(L, a.Hk, D).to(dt)
+        one, cu = torch.full((1,), L, device=dev), torch.tensor([0, L], device=dev)
+        for b in range(n):
+            kda.kda_kv4_append(k, v, cache, table[b:b + 1].clone(), one, cu_seqlens=cu)
+        lens = torch.full((n,), L, device=dev)
+        new = n if a.case == "kv4_attn_step" else min(T, L)
+        q, out = rnd(new, H, D).to(dt), torch.empty((new, H, D), dtype=dt, device=dev)
+        cq = None if a.case == "kv4_attn_step" else torch.tensor([0, new], device=dev)
+
+        def call():
+            if a.case == "kv4_append":
+                kda.kda_kv4_append(k, v, cache, table, one, cu_seqlens=cu)
+            elif a.case == "kv4_read":
+                kda.kda_kv4_read(cache, table, one, k, v, cu_seqlens=cu)
+            else:
+                kda.kda_kv4_attention(q, cache, table, lens, out, cu_seqlens=cq)
     else:
         dt = bf if a.dtype == "bf16" else torch.float32
         q, k, v = rnd(T, H, D).to(dt), rnd(T, H, D).to(dt), rnd(T, H, D).to(dt)
