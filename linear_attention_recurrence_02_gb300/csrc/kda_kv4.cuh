@@ -101,18 +101,26 @@ __device__ __forceinline__ float group_scale(float m) {
     return fminf(fmaxf(__uint_as_float(b), SCALE_MIN), SCALE_MAX);
 }
 
-// Word of eight channels, as pairs of neighbours. The quotient is rounded as a division would round it: with the
+constexpr uint32_t NAN_CODES = 0x44444444u;  // eight codes of 8, rotated
+// Halves of four codes each (first lowest), the even channels' and the odd ones', as a word.
+__device__ __forceinline__ uint32_t rotated(uint32_t even, uint32_t odd) {
+    const uint32_t w = prmt(even, odd, 0x5410);
+    return ((w << 3) & 0xfff8fff8u) | ((w >> 13) & 0x00070007u);
+}
+__device__ __forceinline__ void clip(float2 &x) {
+    x = make_float2(fminf(fmaxf(x.x, -7.f * SCALE_MAX), 7.f * SCALE_MAX), fminf(fmaxf(x.y, -7.f * SCALE_MAX), 7.f * SCALE_MAX));
+}
+
+// Word of eight fp32 channels, as pairs of neighbours. The quotient is rounded as a division would round it: with the
 // reciprocal correctly rounded, one residual step makes x * inv exact to the last bit (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990); values that lie between two codes
 // are common, since inputs and scales have few bits. Adding 1.5 * 2^23 rounds to a whole number, halves to even;
 // the four codes of a half are joined as whole numbers in fp32 (below 2^16, so exactly), two halves at once.
 __device__ __forceinline__ uint32_t quantise8(float2 (&x)[4], float s) {
-    if (!(s == s)) return 0x44444444u;  // eight codes of 8, rotated
+    if (!(s == s)) return NAN_CODES;
     if (s == SCALE_MAX) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[i] = make_float2(fminf(fmaxf(x[i].x, -7.f * SCALE_MAX), 7.f * SCALE_MAX),
-                               fminf(fmaxf(x[i].y, -7.f * SCALE_MAX), 7.f * SCALE_MAX));
+        for (int i = 0; i < 4; ++i) clip(x[i]);
     }
     const float inv = __frcp_rn(s);
     const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-s, -s);
@@ -127,8 +135,32 @@ __device__ __forceinline__ uint32_t quantise8(float2 (&x)[4], float s) {
     }
     // + 8 for every code, and 2^23 so that the number stands in the lowest bits
     code = __fadd2_rn(code, make_float2(8388608.f + 34952.f, 8388608.f + 34952.f));
-    const uint32_t w = __byte_perm(__float_as_uint(code.x), __float_as_uint(code.y), 0x5410);  // [odd][even]
-    return ((w << 3) & 0xfff8fff8u) | ((w >> 13) & 0x00070007u);
+    return rotated(__float_as_uint(code.x), __float_as_uint(code.y));
+}
+
+// The same for bf16 channels, which need no exact quotient: x has eight significant bits and s five, so that x / s is a
+// code and a half or at least 1/512 away from one (|x - (k + 1/2) s| is a multiple of the smaller of x's last place and
+// s / 64). x * inv with an approximate reciprocal, rounded to multiples of 2^-11 by adding 6144, is the half itself in
+// the first case and on the same side of it in the second; the second sum rounds it to 8 + code, halves to even, in the
+// lowest bits of 2^23 + 2^22. The codes are joined there as integers: what the four words have above 16 bits falls off.
+__device__ __forceinline__ uint32_t quantise8_bf16(float2 (&x)[4], float s) {
+    if (!(s == s)) return NAN_CODES;
+    if (s == SCALE_MAX) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) clip(x[i]);
+    }
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float2 inv2 = make_float2(inv, inv), fine = make_float2(6144.f, 6144.f);
+    const float2 whole = make_float2(12582920.f - 6144.f, 12582920.f - 6144.f);
+    uint32_t even = 0, odd = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+        const float2 c = __fadd2_rn(__ffma2_rn(x[i], inv2, fine), whole);
+        even = even * 16 + __float_as_uint(c.x);
+        odd = odd * 16 + __float_as_uint(c.y);
+    }
+    return rotated(even, odd);
 }
 
 // ---------------------------------------------------------------- places

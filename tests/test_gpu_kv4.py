@@ -280,6 +280,38 @@ def test_quantising_edges(env):
     assert np.array_equal(np64(vo), ref.held(-x.astype(np.float64)), equal_nan=True)
 
 
+def test_quantising_every_bf16_quotient(env):
+    """Every bf16 significand against every scale of five bits, of both signs, at the sizes where codes differ, with
+    scales near both ends of their range too."""
+    torch, kda = env
+    D = 128
+    rows = []
+    for S in range(16, 32):
+        for up in (0, -90, 110):
+            x = np.array([X * 2.0 ** a for a in range(-7, 1) for X in range(128, 256) if X * 2.0 ** a <= 7 * S])
+            x = np.concatenate([x, -x]) * 2.0 ** (up - 6)
+            x = np.pad(x, (0, -len(x) % 31)).reshape(-1, 31)
+            rows.append(np.concatenate([np.full((len(x), 1), 7 * S * 2.0 ** (up - 6)), x], 1))
+    x = np.concatenate(rows)
+    x = np.concatenate([x, np.zeros((-len(x) % 4, 32))]).reshape(-1, 1, D)
+    k = _dev(torch, x).to(torch.bfloat16)
+    assert np.array_equal(np64(k), x)
+    big = torch.full_like(k[:3], torch.finfo(torch.bfloat16).max)
+    big[1] = 2.0 ** -133
+    big[2, 0, 5], big[2, 0, 40] = float("nan"), float("inf")
+    k = torch.cat([k, big])
+    n = k.shape[0]
+    table, pages = _layout(torch, np.random.default_rng(2), [n], 64)
+    cache = torch.zeros((pages, 1, 4, 18 * D), dtype=torch.uint8, device="cuda")
+    tb, lens, cu = _dev(torch, table), torch.tensor([n], device="cuda"), torch.tensor([0, n], device="cuda")
+    kda.kda_kv4_append(k, -k, cache, tb, lens, cu_seqlens=cu)
+    ko, vo = torch.empty_like(k), torch.empty_like(k)
+    kda.kda_kv4_read(cache, tb, lens, ko, vo, cu_seqlens=cu)
+    kda.kda_sync_status()
+    assert np.array_equal(np64(ko), ref.held(np64(k)), equal_nan=True)
+    assert np.array_equal(np64(vo), ref.held(-np64(k)), equal_nan=True)
+
+
 # ---------------------------------------------------------------- attention
 def _filled(torch, kda, rng, lens, page, Hk, D, cols=None):
     """A cache with random tokens for every sequence; what the pages hold behind a sequence's end has NaN scales."""
