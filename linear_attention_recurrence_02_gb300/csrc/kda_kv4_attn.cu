@@ -183,6 +183,11 @@ __device__ __forceinline__ float peer_float(uint32_t at, uint32_t rank) {
 template <int D, typename T, int NTL, bool GROUP>
 __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int G = D / 32, QS = sizeof(T) == 4 ? 3 : 1, BYTES = Format<D>::BYTES;
+    // Terms of bf16 that a factor is taken as. With bf16 queries one costs as much accuracy as the output's own rounding
+    // (0.0023 against 0.0017 of the output's root mean square, up to half as much again where there are few heads); two
+    // leave only the latter. They cost next to nothing where one short item a cluster waits for latencies (9.2 -> 9.4 us for
+    // 4096 tokens), and are taken there; runs are bound by instructions (64 x 8192 tokens: 127 -> 151 us).
+    constexpr int PT = QS > 1 ? 3 : GROUP ? 2 : 1;
     using Sm = FewSmem<D, NTL, QS>;
     constexpr int R = Sm::R;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -379,7 +384,10 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
 #pragma unroll
                             for (int e = 0; e < 4; ++e) s[blk][nt][e] = fmaf(z[e], sc[e >> 1], s[blk][nt][e]);
                         }
-                    } else {  // fp32 queries: the cached values themselves, with nothing to cancel
+                    } else {  // fp32 queries: the cached values themselves, with nothing to cancel. The matrix
+                              // instruction cuts what does not fit its sum where an addition would round it; in a long
+                              // chain that adds up, so a group's products start from zero and are added in fp32 (with
+                              // the factors' products below: 26 x 5475 tokens 2.2e-6 off -> 0.3e-6; 141 -> 147 us)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const uint32_t s2 = prmt(ksc[x][gr >> 1], 0, gr & 1 ? 0x3232 : 0x1010);
@@ -387,12 +395,17 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
                         }
 #pragma unroll
                         for (int nt = 0; nt < NTL; ++nt)
+                        {
+                            float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                             for (int z = QS - 1; z >= 0; --z) {
                                 const uint4 q = qs[((nt * G + gr) * QS + z) * 32 + lane];
-                                mma16816(s[blk][nt], f[0][0], f[1][0], f[0][1], f[1][1], q.x, q.y);
-                                mma16816(s[blk][nt], f[0][2], f[1][2], f[0][3], f[1][3], q.z, q.w);
+                                mma16816(t, f[0][0], f[1][0], f[0][1], f[1][1], q.x, q.y);
+                                mma16816(t, f[0][2], f[1][2], f[0][3], f[1][3], q.z, q.w);
                             }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[blk][nt][e] += t[e];
+                        }
                     }
                 }
             }
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
             // factors, and their turn into the second product's operand
 #pragma unroll
             for (int blk = 0; blk < BLOCKS; ++blk) {
-                uint32_t p[NTL][2][QS];
+                uint32_t p[NTL][2][PT];
 #pragma unroll
                 for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
@@ -471,10 +484,10 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
                         const float p1 = exp2_fast(fmaf(s[blk][nt][2 * x + 1], a.scale_log2, neg[nt][1]));
                         l[nt][0] += p0;
                         l[nt][1] += p1;
-                        uint32_t sp[QS];
-                        split_bf16<QS>(p0, p1, sp);
+                        uint32_t sp[PT];
+                        split_bf16<PT>(p0, p1, sp);
 #pragma unroll
-                        for (int z = 0; z < QS; ++z) p[nt][x][z] = transpose8x8(sp[z]);
+                        for (int z = 0; z < PT; ++z) p[nt][x][z] = transpose8x8(sp[z]);
                     }
                 const uint8_t *vb = buf + blk * BYTES;
                 uint32_t vw[2][G], vsc[2][G];  // pairs j and j + 4
@@ -508,11 +521,17 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                        for (int nt = 0; nt < NTL; ++nt)
+                        for (int nt = 0; nt < NTL; ++nt) {
+                            float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int z = QS - 1; z >= 0; --z)
-                                mma16816(o[gr][mt][nt], f[0][2 * mt], f[0][2 * mt + 1], f[1][2 * mt], f[1][2 * mt + 1],
-                                         p[nt][0][z], p[nt][1][z]);
+                            for (int z = PT - 1; z >= 0; --z)
+                                mma16816(QS > 1 ? t : o[gr][mt][nt], f[0][2 * mt], f[0][2 * mt + 1], f[1][2 * mt],
+                                         f[1][2 * mt + 1], p[nt][0][z], p[nt][1][z]);
+                            if constexpr (QS > 1) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[gr][mt][nt][e] += t[e];
+                            }
+                        }
                 }
             }
             __syncwarp();  // every lane has read the stage

@@ -444,6 +444,48 @@ def test_attention_of_many_pieces(env, lens, new, Hq, D, window):
     _check(torch, out, lse, q, cache, table, lens, new, D ** -0.5, True, window)
 
 
+def _against_64_bits(torch, kda, B, L, Hq, Hk, D, dt, cols, seed):
+    """Relative root-mean-square error of one new token's attention for each of B sequences of about L, positive values."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    lens = [L - 37 * b for b in range(B)]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), device="cuda")
+    table, pages = _layout(torch, np.random.default_rng(seed), lens, 64, cols=cols)
+    cache, tb, lt = (torch.zeros((pages, Hk, 4, 18 * D), dtype=torch.uint8, device="cuda"), _dev(torch, table),
+                     torch.tensor(lens, device="cuda"))
+    k, v = (torch.randn((sum(lens), Hk, D), generator=gen, device="cuda") for _ in range(2))
+    kda.kda_kv4_append(k, v.abs(), cache, tb, lt, cu_seqlens=cu)
+    kda.kda_kv4_read(cache, tb, lt, k, v, cu_seqlens=cu)
+    q = torch.randn((B, Hq, D), generator=gen, device="cuda").to(dt)
+    out = torch.empty_like(q)
+    kda.kda_kv4_attention(q, cache, tb, lt, out)
+    kda.kda_sync_status()
+    far = size = 0.0
+    for b in range(B):
+        kb, vb = (x[cu[b]:cu[b + 1]].double().repeat_interleave(Hq // Hk, 1).transpose(0, 1) for x in (k, v))
+        p = torch.softmax(torch.einsum("hd,hjd->hj", q[b].double(), kb) * D ** -0.5, -1)
+        want = torch.einsum("hj,hjd->hd", p, vb)
+        far += float((out[b].double() - want).pow(2).sum())
+        size += float(want.pow(2).sum())
+    return (far / size) ** 0.5
+
+
+@pytest.mark.parametrize("B,L,cols", [(26, 5475, 200), (2, 1000, 20)])
+def test_long_fp32_sums_do_not_drift(env, B, L, cols):
+    """Values of one sign, over which the cutting of a chain of matrix products would add up. Scores of up to 8 are off by
+    some 2^-24 of themselves a step of a short chain, the exponential by 2^-22, and sums that round walk at random: 2^-21 in
+    all, twice that allowed."""
+    torch, kda = env
+    assert _against_64_bits(torch, kda, B, L, 7, 7, 128, torch.float32, cols, 61) <= 2.0 ** -20
+
+
+def test_short_bf16_items_lose_the_outputs_rounding_only(env):
+    """Factors in two terms are off by 2^-16 at most, the output by its rounding: 2^-8 / sqrt(3) of the lower end of an
+    octave, at most."""
+    torch, kda = env
+    for seed in range(4):
+        assert _against_64_bits(torch, kda, 1, 4000, 20, 5, 64, torch.bfloat16, 63, seed) <= 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -14
+
+
 def test_two_graphs_share_a_workspace(env):
     """Captured calls of different sizes that use one workspace in turn, its bytes arbitrary before."""
     torch, kda = env
