@@ -15,9 +15,14 @@
 //
 // Each warp is on its own: it takes every fourth tile of 64 tokens of the CTA's run, brings its tiles in
 // through a ring of two (by 16-byte asynchronous copies of all lanes: a bulk copy's issue by one lane, its
-// barrier and the wait on it took as many issue slots as a third of the tile's arithmetic), and keeps a running maximum and sum (moved only when a score passes the
-// maximum by 2^8: the factors stay in range and most tiles rescale nothing). At an item's end the four
-// warps' results are joined through shared memory.
+// barrier and the wait on it took as many issue slots as a third of the tile's arithmetic), and keeps a running
+// maximum and sum (moved only when a score passes the maximum by 2^8: the factors stay in range and most
+// tiles rescale nothing). At an item's end the four warps' results are joined through shared memory.
+//
+// 64 sequences of up to 8192 tokens, 96 over 8 heads of 128 in bf16: 127 us, 3.5 TB/s; one query head a
+// cached one: 99 us. By then instructions bound it and their latencies, with eight warps an SM (255 registers each):
+// tiles of 32 tokens with three CTAs an SM take 136 us, with deeper rings 134 to 141, the tile's body as a
+// loop over halves or quarters 136 or 139. One sequence of 4096 tokens takes 9 us, a single tile 6.
 #include <algorithm>
 #include <string>
 
@@ -646,7 +651,8 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
 }
 
 // Up to eight rows of the item that goes on behind run blockIdx.x, a warp each; where the item has many pieces the
-// eight warps share a row's after another. Either way in an order that the sizes alone decide.
+// eight warps share a row's after another. Either way in an order that the sizes alone decide. (A CTA a row: 4096 queries
+// over 8192 tokens 406 us instead of 384, in blocks of 256 rows of which few have pieces.)
 template <int D, typename T, int R>
 __global__ void __launch_bounds__(256) kv4_attn_join_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int V = D / 32, MANY = 12;
