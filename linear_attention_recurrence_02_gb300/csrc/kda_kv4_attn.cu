@@ -749,9 +749,12 @@ struct FewPlan {
     int64_t blocks, tiles;
     int group;
 };
-static FewPlan plan_few(const AttnArgs &a, int R, int cap) {
+// one_block: only sequences of at most R rows are this kernel's (the others went to the one for many rows). A ragged batch
+// is then three launches instead of four as a rule, and no empty clusters (3 prompts of up to 598 tokens, 84 over 7 heads:
+// 83 -> 70 us).
+static FewPlan plan_few(const AttnArgs &a, int R, int cap, bool one_block) {
     FewPlan p;
-    p.blocks = a.c.cu ? a.c.T * a.group / R + a.c.B : (int64_t)a.c.B * ((a.group + R - 1) / R);
+    p.blocks = one_block ? std::min<int64_t>(a.c.B, a.c.T) : a.c.cu ? a.c.T * a.group / R + a.c.B : (int64_t)a.c.B * ((a.group + R - 1) / R);
     p.tiles = ((int64_t)a.c.cols << a.c.page_shift) / TILE + 1;
     if (a.window > 0) p.tiles = std::min(p.tiles, ((int64_t)a.window + (a.c.cu ? a.c.T : 1)) / TILE + 2);
     p.group = MOST_GROUP;
@@ -763,7 +766,7 @@ static FewPlan plan_few(const AttnArgs &a, int R, int cap) {
 template <int D, typename T, int NTL> static kda_status attn_few(AttnArgs a, cudaStream_t s) {
     using Sm = FewSmem<D, NTL, sizeof(T) == 4 ? 3 : 1>;
     const int cap = few_ctas(few_per_sm(D));
-    const FewPlan plan = plan_few(a, Sm::R, cap);
+    const FewPlan plan = plan_few(a, Sm::R, cap, a.most_rows <= Sm::R);
     if (plan.group > 0) {
         constexpr auto kern = kv4_attn_few_kernel<D, T, NTL, true>;
         if (smem_attr_once<kern>(Sm::BYTES) != cudaSuccess) return check_launch("kv4_attn_few_kernel: shared memory");
@@ -816,7 +819,7 @@ static Route route(const AttnArgs &a, int D, kda_dtype dtype) {
         r.row_tiles = !a.c.cu && a.group <= 8 ? 1 : 2;
     }
     const int cap = few_ctas(few_per_sm(D));
-    if (r.few && plan_few(a, 8 * r.row_tiles, cap).group == 0) r.bytes = pieces_bytes(cap, 8 * r.row_tiles, D);
+    if (r.few && plan_few(a, 8 * r.row_tiles, cap, r.many).group == 0) r.bytes = pieces_bytes(cap, 8 * r.row_tiles, D);
     if (r.many) r.bytes = std::max(r.bytes, many_bytes(D));
     return r;
 }
