@@ -682,9 +682,9 @@ kda_status kda_kv4_read(const void *cache, const int32_t *block_table, const int
  *          (the states of an encoder, say)
  *   window > 0: only the tokens less than `window` before its position; 0: all
  * A query that sees nothing gets zeros and lse = -infinity. Scores, maxima, sums and
- * the output's sums are fp32. With dtype bf16 the softmax factors are rounded
- * for the second product, to bf16 or, where the block table is short and the rows few, to
- * two bf16 terms; with fp32 both products take all 24 bits.
+ * the output's sums are fp32. With dtype bf16 the softmax factors enter the second
+ * product as two bf16 terms (off by 2^-16 at most), so that the output's own rounding is what is
+ * left; with fp32 both products take all 24 bits.
  * A token whose keys are not finite makes the queries that see it NaN, one
  * whose values are not finite those of its channels at least; queries that do
  * not see it are not touched.

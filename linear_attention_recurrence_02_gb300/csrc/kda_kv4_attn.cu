@@ -19,10 +19,10 @@
 // maximum and sum (moved only when a score passes the maximum by 2^8: the factors stay in range and most
 // tiles rescale nothing). At an item's end the four warps' results are joined through shared memory.
 //
-// 64 sequences of up to 8192 tokens, 96 over 8 heads of 128 in bf16: 127 us, 3.5 TB/s; one query head a
-// cached one: 99 us. By then instructions bound it and their latencies, with eight warps an SM (255 registers each):
-// tiles of 32 tokens with three CTAs an SM take 136 us, with deeper rings 134 to 141, the tile's body as a
-// loop over halves or quarters 136 or 139. One sequence of 4096 tokens takes 9 us, a single tile 6.
+// 64 sequences of up to 8192 tokens, 96 over 8 heads of 128 in bf16: 152 us, 3.0 TB/s; one query head a
+// cached one: 108 us. By then instructions bound it and their latencies, with eight warps an SM (255 registers each).
+// While factors were one bf16 term, and it took 127 us, tiles of 32 tokens with three CTAs an SM took 136, with deeper rings
+// 134 to 141, the tile's body as a loop over halves or quarters 136 or 139. One sequence of 4096 tokens takes 9 us, a single tile 6.
 #include <algorithm>
 #include <string>
 
@@ -66,20 +66,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// x as a sum of bf16 numbers, as many as QS: one rounds, three hold all 24 bits of an fp32.
-template <int QS> __device__ __forceinline__ void split_bf16(float lo, float hi, uint32_t (&p)[QS]) {
-#pragma unroll
-    for (int i = 0; i < QS; ++i) {
-        p[i] = pack_bf16(lo, hi);
-        lo -= __uint_as_float(p[i] << 16);
-        hi -= __uint_as_float(p[i] & 0xffff0000u);
-    }
 }
 
 // N words of shared memory.
@@ -190,9 +176,9 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
     constexpr int G = D / 32, QS = sizeof(T) == 4 ? 3 : 1, BYTES = Format<D>::BYTES;
     // Terms of bf16 that a factor is taken as. With bf16 queries one costs as much accuracy as the output's own rounding
     // (0.0023 against 0.0017 of the output's root mean square, up to half as much again where there are few heads); two
-    // leave only the latter. They cost next to nothing where one short item a cluster waits for latencies (9.2 -> 9.4 us for
-    // 4096 tokens), and are taken there; runs are bound by instructions (64 x 8192 tokens: 127 -> 151 us).
-    constexpr int PT = QS > 1 ? 3 : GROUP ? 2 : 1;
+    // leave only the latter, whatever the form that a call's sizes choose. One sequence of 4096 tokens 9.2 -> 9.4 us; 64 x
+    // 8192 tokens 128 -> 152 with 96 query heads over 8, 99 -> 108 with 8 over 8.
+    constexpr int PT = QS > 1 ? 3 : 2;
     using Sm = FewSmem<D, NTL, QS>;
     constexpr int R = Sm::R;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -282,10 +268,10 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
                 const float4 *p = reinterpret_cast<const float4 *>(smem + Sm::Q + turn * Sm::RAW) + x * 64 + lane;
                 const float4 u = p[0], v = p[32];
                 uint32_t f[4][QS];
-                split_bf16<QS>(u.x, u.y, f[0]);
-                split_bf16<QS>(u.z, u.w, f[1]);
-                split_bf16<QS>(v.x, v.y, f[2]);
-                split_bf16<QS>(v.z, v.w, f[3]);
+                split_bf16<QS>(make_float2(u.x, u.y), f[0]);
+                split_bf16<QS>(make_float2(u.z, u.w), f[1]);
+                split_bf16<QS>(make_float2(v.x, v.y), f[2]);
+                split_bf16<QS>(make_float2(v.z, v.w), f[3]);
 #pragma unroll
                 for (int k = 0; k < QS; ++k)
                     reinterpret_cast<uint4 *>(smem + Sm::SPLIT)[(x * QS + k) * 32 + lane] =
@@ -490,7 +476,7 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
                         l[nt][0] += p0;
                         l[nt][1] += p1;
                         uint32_t sp[PT];
-                        split_bf16<PT>(p0, p1, sp);
+                        split_bf16<PT>(make_float2(p0, p1), sp);
 #pragma unroll
                         for (int z = 0; z < PT; ++z) p[nt][x][z] = transpose8x8(sp[z]);
                     }
@@ -523,20 +509,29 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
                         expand(prmt(ev, od, gr & 1 ? 0x7632 : 0x5410), prmt(ev, od, gr & 1 ? 0x6723 : 0x4501), vsc[x][gr],
                                minus24(vsc[x][gr]), f[x]);
                     }
+                    if constexpr (QS == 1) {  // an accumulator's products apart from one another
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
+                        for (int z = PT - 1; z >= 0; --z)
 #pragma unroll
-                        for (int nt = 0; nt < NTL; ++nt) {
-                            float t[4] = {0.f, 0.f, 0.f, 0.f};
+                            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                            for (int z = PT - 1; z >= 0; --z)
-                                mma16816(QS > 1 ? t : o[gr][mt][nt], f[0][2 * mt], f[0][2 * mt + 1], f[1][2 * mt],
-                                         f[1][2 * mt + 1], p[nt][0][z], p[nt][1][z]);
-                            if constexpr (QS > 1) {
+                                for (int nt = 0; nt < NTL; ++nt)
+                                    mma16816(o[gr][mt][nt], f[0][2 * mt], f[0][2 * mt + 1], f[1][2 * mt], f[1][2 * mt + 1],
+                                             p[nt][0][z], p[nt][1][z]);
+                    } else {
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int nt = 0; nt < NTL; ++nt) {
+                                float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int z = PT - 1; z >= 0; --z)
+                                    mma16816(t, f[0][2 * mt], f[0][2 * mt + 1], f[1][2 * mt], f[1][2 * mt + 1], p[nt][0][z],
+                                             p[nt][1][z]);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) o[gr][mt][nt][e] += t[e];
                             }
-                        }
+                    }
                 }
             }
             __syncwarp();  // every lane has read the stage

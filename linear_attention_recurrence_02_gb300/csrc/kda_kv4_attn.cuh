@@ -227,6 +227,22 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Pairs of fp32 as sums of bf16 pairs, as many as QS: one rounds (2^-8), two leave 2^-16, three hold all 24 bits.
+template <int QS> __device__ __forceinline__ void split_bf16(float2 x, uint32_t (&p)[QS]) {
+#pragma unroll
+    for (int i = 0; i < QS; ++i) {
+        p[i] = pack_bf16(x.x, x.y);
+        if (i + 1 < QS)
+            x = __ffma2_rn(make_float2(__uint_as_float(p[i] << 16), __uint_as_float(p[i] & 0xffff0000u)),
+                           make_float2(-1.f, -1.f), x);
+    }
+}
+
 // Bytes of the pieces of `ctas` runs of blocks of R rows, and where they stand in a workspace.
 inline size_t pieces_bytes(int ctas, int R, int D) {
     return (size_t)ctas * (2 * (size_t)R * (D + 2) * sizeof(float) + sizeof(Joint));

@@ -7,21 +7,27 @@
 // tiles share. One CTA an SM, roles by warp group:
 //
 //   groups 0, 1  softmax of row tile 0, 1: a thread owns a row, reads its 128 scores from TMEM, writes the
-//                factors back over them in bf16 (the second product's A operand), rescales its row of the
-//                output in TMEM in the rare case that the running maximum moves
+//                factors back over them in two bf16 terms (the second product's A operand), rescales its row of
+//                the output in TMEM in the rare case that the running maximum moves
 //   group 2      codes from global memory through registers, expanded to bf16 (exact), into the 128-byte
 //                swizzled tiles that the tensor cores read: keys K-major, values as they come (MN-major)
 //   group 3      a warp issues S_i = Q_i K^T and O_i += P_i V for the two row tiles in turn: while one
 //                tile's softmax runs, the tensor cores have the other's products. Where a block has one row
 //                tile only, the two groups take its even and odd tiles of cached tokens and join their outputs
 //
-// TMEM: S_0, S_1 (128 columns each, P_i in the first 64 of S_i), O_0, O_1 (D columns each).
+// TMEM: S_0, S_1 (128 columns each, P_i over S_i), O_0, O_1 (D columns each).
 //
-// 4096 queries of 32 heads over 8192 cached tokens of 8 heads of 128: 365 us, 1.12 PFLOP/s; a pair of tiles takes about
-// 3850 cycles, of which the tensor cores need 2150, and the products of Q and K read shared memory at its full rate.
-// Measured and not taken: half the codes to expand (as two CTAs would share them) 347 us; scores read from TMEM once,
-// the maximum kept per 64 tokens, 369; 64 tokens' scores computed under the other 64's softmax 420, because a product
-// that narrow reads more of shared memory than the tensor cores can wait for.
+// A factor is two bf16 terms, off by 2^-16 at most: with one, its rounding (2^-8) costs an output as much as the output's
+// own (0.0023 of its root mean square against 0.0017), and the same query over the same cache would be less exact here than
+// in the kernel for few rows. The second term is half as many products again.
+//
+// 4096 queries of 32 heads over 8192 cached tokens of 8 heads of 128: 442 us (0.93 PFLOP/s; with one term 364). A pair of
+// tiles takes about 4700 cycles, of which the tensor cores need 3200, and the products of Q and K read shared memory at
+// its full rate. Measured with one term and not taken: half the codes to expand (as two CTAs would share them) 347 us;
+// scores read from TMEM once, the maximum kept per 64 tokens, 369; 64 tokens' scores computed under the other 64's
+// softmax 420, because a product that narrow reads more of shared memory than the tensor cores can wait for. fp16 factors and
+// values in tiles whose scales fit fp16, two bf16 terms in the others: 426 us, and a row's last bits would then depend on
+// tokens that it does not see.
 #include <algorithm>
 #include <string>
 
@@ -148,12 +154,6 @@ __device__ __forceinline__ void next_part(const AttnArgs &a, Place &w, Part &g) 
     }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // A bounded wait of few instructions: the waiting warps' polls take issue slots and integer units from the
 // working ones (a clock read and compared each time made a third of all instructions). NS > 0: nanoseconds
 // between the tries of a warp that is not in a hurry.
@@ -192,18 +192,24 @@ __device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// A in TMEM (8 columns a step), B MN-major in shared memory (2048 bytes a step).
-__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// A in TMEM, for 64 tokens: the first terms of 32 in 16 columns, their second terms in the next 16; then the other 32
+// tokens'. B MN-major in shared memory (2048 bytes a step of 16 tokens).
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t.reg .b64 b1, b2, b3;\n\t"
         "setp.ne.u32 q, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
         "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.u32 a4, %1, 32;\n\tadd.u32 a5, %1, 40;\n\tadd.u32 a6, %1, 48;\n\tadd.u32 a7, %1, 56;\n\t"
         "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
         "elect.sync _|p, 0xffffffff;\n\t"
         "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
         "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}\n" ::"r"(d),
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], %2, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b1, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b2, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b3, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b2, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b3, %3, t;\n\t}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -460,37 +466,34 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                             }
                         }
                     }
-                    // The factors, 64 scores at a time, in the columns of scores that are read: the product starts on the
-                    // first half of them.
+                    // The factors, 32 at a time, in the columns of the scores that they come from: 16 columns of first terms, 16
+                    // of second ones. The product starts on the first half of them. (64 at a time: 470 us instead of 442.)
                     float2 sum = make_float2(0.f, 0.f);
                     const float2 sc = make_float2(a.scale_log2, a.scale_log2), ng = make_float2(neg, neg);
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t x[32], y[32], p[32];
-                        tmem_ld32(ts + 64 * c, x);
-                        tmem_ld32(ts + 64 * c + 32, y);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32], p[32];
+                        tmem_ld32(ts + 32 * c, x);
                         landed(x);
-                        landed(y);
                         float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float2 u = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc, ng);
-                            float2 v = __ffma2_rn(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), sc, ng);
                             u.x = exp2_fast(u.x);
                             u.y = exp2_fast(u.y);
-                            v.x = exp2_fast(v.x);
-                            v.y = exp2_fast(v.y);
-                            sum = __fadd2_rn(sum, u);
-                            s2 = __fadd2_rn(s2, v);
-                            p[e] = pack_bf16(u.x, u.y);
-                            p[16 + e] = pack_bf16(v.x, v.y);
+                            s2 = __fadd2_rn(s2, u);
+                            uint32_t t[2];
+                            split_bf16<2>(u, t);
+                            p[e] = t[0];
+                            p[16 + e] = t[1];
                         }
                         sum = __fadd2_rn(sum, s2);
                         tmem_st32(ts + 32 * c, p);
+                        if (c % 2 == 0) continue;
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive((c == 0 ? bar->p_half : bar->p_full) + i);
+                        if (lane == 0) mbar_arrive((c == 1 ? bar->p_half : bar->p_full) + i);
                     }
                     l += sum.x + sum.y;
                     ++done;
@@ -753,8 +756,8 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             };
             auto outputs = [&](int i, int st, int half, bool more) {  // the first or second 64 tokens
                 if (!ok) return;
-                mma4_ts(tbase + 256 + D * i, tbase + 128 * i + 32 * half, v0 + st * (Sm::TILE_BYTES / 16) + 512 * half, ID_O,
-                        more || half);
+                mma8_ts(tbase + 256 + D * i, tbase + 128 * i + 64 * half, v0 + st * (Sm::TILE_BYTES / 16) + 512 * half,
+                        ID_O, more || half);
                 if (half) commit(bar->pv_done + i);
             };
             auto release = [&](uint64_t *b) {

@@ -1,0 +1,69 @@
+"""GPU tests of the 4-bit cache's calls at what their first tests did not reach: how exact the softmax factors are in
+every form of the attention, bad lengths and offsets wherever they stand, and long lines of work.
+
+Tolerances as in test_gpu_kv4, but a softmax factor is off by at most 2^-16 of itself, what two bf16 terms leave,
+whatever the form that a call takes (2^-8 there, half a step of bf16).
+"""
+import numpy as np
+import pytest
+
+from tests import _kv4 as ref
+from tests.test_gpu_kv4 import _dev, _filled, env, half_step, np64  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _check_tightly(torch, got, q, cache, table, lens, new, scale):
+    host, t, D = cache.cpu().numpy(), 0, q.shape[-1]
+    for b, (n, m) in enumerate(zip(lens, new)):
+        k, v = ref.tokens(host, table, b, n)
+        out, _, terms, size = ref.attention(np64(q[t:t + m]), k, v, [n - m + i for i in range(m)], scale, True, 0)
+        ds = (D + 8) * 2.0 ** -23 * size + 2.0 ** -20
+        rest = (2 * ds + (n + 64) * 2.0 ** -23)[..., None]
+        tol = 2.0 ** -16 * terms + half_step(torch, q.dtype) * np.abs(out) + rest * 1.1 * terms + 1e-30
+        assert np.all(np.abs(np64(got[t:t + m]) - out) <= tol), (b, n, m)
+        t += m
+
+
+_FORMS = [
+    ([20, 33, 9], None, 8, 2, 128, 4),             # an item a cluster
+    ([20, 130, 9], None, 8, 2, 128, 1000),         # runs, eight rows a block
+    ([20, 130, 9], None, 24, 2, 64, 1000),         # sixteen
+    ([70, 33, 9], None, 24, 2, 128, 1000),
+    ([40, 21, 80], [3, 1, 2], 8, 2, 128, 1000),    # runs behind the kernel for many rows
+    ([40, 21, 30], [9, 1, 20], 8, 2, 128, 1000),   # up to 128 rows: one row tile
+    ([24, 140], None, 40, 1, 64, 4),
+    ([60, 150], [50, 40], 8, 2, 128, 4),           # two row tiles
+    ([45, 300], [33, 70], 12, 2, 64, 1000),
+]
+
+
+def _sized(torch, kda, rng, lens, page, Hk, D, cols, size):
+    """As _filled, with token t's values size[t] as large; a size of 0 leaves it zeros."""
+    cache, tb, lt, table = _filled(torch, kda, rng, lens, page, Hk, D, cols=cols)
+    k, v = (rng.normal(size=(sum(lens), Hk, D)) for _ in range(2))
+    kda.kda_kv4_append(_dev(torch, k).float(), _dev(torch, v * size[:, None, None]).float(), cache, tb, lt,
+                       cu_seqlens=_dev(torch, np.concatenate([[0], np.cumsum(lens)])))
+    return cache, tb, lt, table
+
+
+_SIZES = {"even": lambda rng, n: np.ones(n),
+          "uneven": lambda rng, n: np.where(rng.random(n) < 0.02, rng.choice([0.0, 1e-9, 300.0, 1e30], n), 1.0)}
+
+
+@pytest.mark.parametrize("size", list(_SIZES))
+@pytest.mark.parametrize("lens,new,Hq,Hk,D,cols", _FORMS)
+def test_factors_are_as_exact_in_every_form(env, lens, new, Hq, Hk, D, cols, size):  # noqa: F811
+    """Few tokens of near-equal weight and values of both signs: an output far below its terms shows what the factors
+    lost, which the output's own rounding hides elsewhere."""
+    torch, kda = env
+    rng = np.random.default_rng(Hq + D + cols)
+    cache, tb, lt, table = _sized(torch, kda, rng, lens, 16, Hk, D, max(cols, -(-max(lens) // 16)),
+                                  _SIZES[size](rng, sum(lens)))
+    counts = [1] * len(lens) if new is None else new
+    q = _dev(torch, 0.5 * rng.normal(size=(sum(counts), Hq, D))).to(torch.bfloat16)
+    out = torch.empty_like(q)
+    cu = None if new is None else _dev(torch, np.concatenate([[0], np.cumsum(counts)]))
+    kda.kda_kv4_attention(q, cache, tb, lt, out, cu_seqlens=cu)
+    kda.kda_sync_status()
+    _check_tightly(torch, out, q, cache, table, lens, counts, D ** -0.5)
