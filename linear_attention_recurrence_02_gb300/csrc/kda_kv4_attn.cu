@@ -783,7 +783,7 @@ template <int D, typename T, int NTL> static kda_status attn_few(AttnArgs a, cud
     }
     constexpr auto kern = kv4_attn_few_kernel<D, T, NTL, false>;
     if (smem_attr_once<kern>(Sm::BYTES) != cudaSuccess) return check_launch("kv4_attn_few_kernel: shared memory");
-    a.ctas = (int)std::min<int64_t>(cap, (plan.blocks * a.c.Hk * plan.tiles + WARPS - 1) / WARPS);
+    a.ctas = ctas_for(plan.blocks, a.c.Hk, plan.tiles, WARPS, cap);
     place_pieces(a, a.part, Sm::R, D);
     launch_dependent(kern, dim3(a.ctas), dim3(32 * WARPS), Sm::BYTES, s, a);
     kda_status st = check_launch("kv4_attn_few_kernel");

@@ -179,6 +179,31 @@ template <int R, int TILE> __device__ __forceinline__ bool item_at(const AttnArg
     return false;
 }
 
+// Tiles of a block of rows where each block is cut by what its own rows see.
+template <int R, int TILE>
+__device__ __forceinline__ void block_tiles(const AttnArgs &a, int n, int len, int block, int &first, int &tiles) {
+    const int i0 = a.by_group(block * R), i1 = a.by_group(min(n * a.group - 1, block * R + R - 1));
+    const int hi = a.causal ? max(len - n + i1 + 1, 0) : len;
+    const int lo = a.window > 0 ? max(len - n + i0 - a.window + 1, 0) : 0;
+    first = lo / TILE;
+    tiles = max((hi + TILE - 1) / TILE - first, 1);
+}
+// All lanes: the tiles of sequence b's items, each with COST more. A prompt of a million and a half tokens with 64 query
+// heads on one key/value head has more than 2^31.
+template <int R, int TILE, int COST>
+__device__ __forceinline__ int64_t sequence_tiles(const AttnArgs &a, int b, int lane, bool flag) {
+    const Seq s = seq_at<R, TILE>(a, b, flag);
+    int64_t sum = 0;
+    for (int k = lane; k < s.blocks; k += 32) {
+        int first, tiles;
+        block_tiles<R, TILE>(a, s.n, s.len, k, first, tiles);
+        sum += tiles + COST;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum * a.c.Hk;
+}
+
 // What a run has of one item.
 struct Segment {
     int64_t t0;         // the sequence's first new token
@@ -241,6 +266,13 @@ template <int QS> __device__ __forceinline__ void split_bf16(float2 x, uint32_t 
             x = __ffma2_rn(make_float2(__uint_as_float(p[i] << 16), __uint_as_float(p[i] & 0xffff0000u)),
                            make_float2(-1.f, -1.f), x);
     }
+}
+
+// CTAs for `blocks` blocks of rows over Hk heads of at most `tiles` tiles: one for every `least` of them, at most `cap`.
+inline int ctas_for(int64_t blocks, int Hk, int64_t tiles, int least, int cap) {
+    const int64_t some = blocks < 1 << 20 ? blocks : 1 << 20;  // so that the product keeps within 64 bits
+    const int64_t n = (some * Hk * tiles + least - 1) / least;
+    return n < cap ? (int)n : cap;
 }
 
 // Bytes of the pieces of `ctas` runs of blocks of R rows, and where they stand in a workspace.

@@ -28,7 +28,6 @@
 // softmax 420, because a product that narrow reads more of shared memory than the tensor cores can wait for. fp16 factors and
 // values in tiles whose scales fit fp16, two bf16 terms in the others: 426 us, and a row's last bits would then depend on
 // tokens that it does not see.
-#include <algorithm>
 #include <string>
 
 #include "kda_kv4_attn.cuh"
@@ -79,31 +78,8 @@ struct Bars {
     uint32_t taddr;
 };
 
-// Tiles of a block of rows.
-__device__ __forceinline__ void block_tiles(const AttnArgs &a, int n, int len, int block, int &first, int &tiles) {
-    const int i0 = a.by_group(block * R), i1 = a.by_group(min(n * a.group - 1, block * R + R - 1));
-    const int hi = a.causal ? max(len - n + i1 + 1, 0) : len;
-    const int lo = a.window > 0 ? max(len - n + i0 - a.window + 1, 0) : 0;
-    first = lo / TILE;
-    tiles = max((hi + TILE - 1) / TILE - first, 1);
-}
-
-// All lanes: the tiles of sequence b's items.
-__device__ __forceinline__ int64_t sequence_tiles(const AttnArgs &a, int b, int lane, bool flag) {
-    const Seq s = seq_at<R, TILE>(a, b, flag);
-    int sum = 0;
-    for (int k = lane; k < s.blocks; k += 32) {
-        int first, tiles;
-        block_tiles(a, s.n, s.len, k, first, tiles);
-        sum += tiles + ITEM_COST;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return (int64_t)sum * a.c.Hk;
-}
-
 __device__ __forceinline__ void enter_block(const AttnArgs &a, Place &w) {
-    block_tiles(a, w.n, w.len, w.block, w.first, w.tiles);
+    block_tiles<R, TILE>(a, w.n, w.len, w.block, w.first, w.tiles);
     w.h = w.t = 0;
 }
 __device__ __forceinline__ void enter_sequence(const AttnArgs &a, Place &w) {
@@ -293,7 +269,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
     const int per = (a.c.B + SUMS - 1) / SUMS, entries = (a.c.B + per - 1) / per;
     for (int e = warp; e < entries; e += NT / 32) {
         int64_t s = 0;
-        for (int b = e * per; b < min((e + 1) * per, a.c.B); ++b) s += sequence_tiles(a, b, lane, blockIdx.x == 0);
+        for (int b = e * per; b < min((e + 1) * per, a.c.B); ++b) s += sequence_tiles<R, TILE, ITEM_COST>(a, b, lane, blockIdx.x == 0);
         if (lane == 0) sums[e] = s;
     }
     if (threadIdx.x == 0) a.joint[blockIdx.x].pieces = 0;
@@ -332,14 +308,14 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
         Place w;
         w.b = e * per;
         for (;; ++w.b) {  // the sequence
-            const int64_t s = sequence_tiles(a, w.b, lane, false);
+            const int64_t s = sequence_tiles<R, TILE, ITEM_COST>(a, w.b, lane, false);
             if (before + s > start) break;
             before += s;
         }
         enter_sequence(a, w);
         for (int k = 0;; k += 32) {  // the block of rows
             int first = 0, tiles = 0;
-            if (k + lane < w.blocks) block_tiles(a, w.n, w.len, k + lane, first, tiles);
+            if (k + lane < w.blocks) block_tiles<R, TILE>(a, w.n, w.len, k + lane, first, tiles);
             const int64_t mine = k + lane < w.blocks ? (int64_t)(tiles + ITEM_COST) * a.c.Hk : 0;
             int64_t upto = mine;
 #pragma unroll
@@ -883,7 +859,7 @@ template <int D> static kda_status run_many(AttnArgs a, cudaStream_t s) {
     constexpr auto kern = many::kv4_attn_many_kernel<D>;
     if (smem_attr_once<kern>(Sm::BYTES) != cudaSuccess) return check_launch("kv4_attn_many_kernel: shared memory");
     const int64_t blocks = a.c.T * a.group / many::R + a.c.B, tiles = ((int64_t)a.c.cols << a.c.page_shift) / many::TILE + 1;
-    a.ctas = (int)std::min<int64_t>(many_ctas(), blocks * a.c.Hk * tiles);
+    a.ctas = ctas_for(blocks, a.c.Hk, tiles, 1, many_ctas());
     place_pieces(a, a.part, many::R, D);
     launch_dependent(kern, dim3(a.ctas), dim3(many::NT), Sm::BYTES, s, a);
     const kda_status st = check_launch("kv4_attn_many_kernel");

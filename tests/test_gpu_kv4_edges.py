@@ -4,6 +4,9 @@ every form of the attention, bad lengths and offsets wherever they stand, and lo
 Tolerances as in test_gpu_kv4, but a softmax factor is off by at most 2^-16 of itself, what two bf16 terms leave,
 whatever the form that a call takes (2^-8 there, half a step of bf16).
 """
+import ctypes
+import subprocess
+
 import numpy as np
 import pytest
 
@@ -67,3 +70,54 @@ def test_factors_are_as_exact_in_every_form(env, lens, new, Hq, Hk, D, cols, siz
     kda.kda_kv4_attention(q, cache, tb, lt, out, cu_seqlens=cu)
     kda.kda_sync_status()
     _check_tightly(torch, out, q, cache, table, lens, counts, D ** -0.5)
+
+
+_LINE = """
+#include "kda_kv4_attn.cuh"
+using namespace kda::kv4;
+__global__ void line(AttnArgs a, int64_t *out) {
+    const int64_t many = sequence_tiles<256, 128, 3>(a, 0, threadIdx.x, false), few = line_tiles<16, 64>(a, threadIdx.x);
+    if (threadIdx.x == 0) out[0] = many, out[1] = few;
+}
+extern "C" int tiles_of(const int64_t *lens, const int64_t *cu, int64_t T, int group, int Hk, int cols, int causal,
+                        int window, int64_t *out) {
+    AttnArgs a = {};
+    a.c.lens = lens, a.c.cu = cu, a.c.T = T, a.c.B = 1, a.c.Hk = Hk, a.c.cols = cols, a.c.page_shift = 8;
+    a.group = group, a.by_group = Div(group), a.causal = causal, a.window = window, a.most_rows = 0x7fffffff;
+    line<<<1, 32>>>(a, out);
+    return (int)cudaDeviceSynchronize();
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def tiles_of(env, tmp_path_factory):  # noqa: F811
+    from linear_attention_recurrence_02_gb300 import build
+    d = tmp_path_factory.mktemp("line")
+    (d / "line.cu").write_text(_LINE)
+    subprocess.run([build._nvcc(), "-O2", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", *build.ARCH, "-I",
+                    build.INCLUDE, "-I", build.CSRC, "-shared", "-o", str(d / "line.so"), str(d / "line.cu")], check=True)
+    fn = ctypes.CDLL(str(d / "line.so")).tiles_of
+    p, i = ctypes.c_void_p, ctypes.c_int
+    fn.argtypes, fn.restype = [p, p, ctypes.c_int64, i, i, i, i, i, p], i
+    return fn
+
+
+@pytest.mark.parametrize("n,length,group,Hk,causal,window", [
+    (1000, 3000, 4, 2, True, 0), (77, 5000, 16, 3, False, 0), (3000, 3000, 8, 1, True, 700),
+    (1_500_000, 1_500_000, 64, 1, True, 0),     # 2.2e9 tiles
+    (1 << 20, 1 << 20, 128, 1, False, 0), (4_200_000, 4_200_000, 8, 1, True, 0), (1_500_000, 8_000_000, 64, 4, True, 5000),
+])
+def test_long_lines_of_work_are_counted(env, tiles_of, n, length, group, Hk, causal, window):  # noqa: F811
+    """The tiles that the kernels cut into runs, at sizes whose product passes 32 bits (and would take minutes to run)."""
+    torch, _ = env
+    lens, cu, out = torch.tensor([length], device="cuda"), torch.tensor([0, n], device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda")
+    torch.cuda.synchronize()
+    assert tiles_of(lens.data_ptr(), cu.data_ptr(), n, group, Hk, -(-length // 256), causal, window, out.data_ptr()) == 0
+    row = np.arange(0, n * group, 256)
+    hi = length - n + np.minimum(row + 255, n * group - 1) // group + 1 if causal else np.full(len(row), length)
+    lo = np.maximum(length - n + row // group - window + 1, 0) if window else np.zeros(len(row), int)
+    many = int((np.maximum(-(-hi // 128) - lo // 128, 1) + 3).sum()) * Hk
+    first = max(length - n - window + 1, 0) // 64 if window else 0
+    few = -(-n * group // 16) * Hk * (-(-length // 64) - first)
+    assert out.tolist() == [many, few]
