@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(32 * WARPS, few_per_sm(D)) kv4_attn_few_kernel
     bool shared_out = false;  // GROUP: more than one CTA has tiles of the item
     if constexpr (GROUP) {
         const int size = cluster_size(), rank = cluster_rank();
-        if (!item_at<R, TILE>(a, blockIdx.x / size, lane, w)) return;  // the whole cluster
+        if (!item_at<R, TILE>(a, blockIdx.x / size, lane, blockIdx.x >= gridDim.x - size, w)) return;  // the whole cluster
         const int per = (w.s.tiles + size - 1) / size;
         w.t = min(rank * per, w.s.tiles);
         w.left = min(per, w.s.tiles - w.t);

@@ -152,12 +152,14 @@ template <int R, int TILE> __device__ __forceinline__ Walk walk_at(const AttnArg
     return w;
 }
 
-// All 32 lanes: the beginning of item `at`, left = 0; false where there are not so many.
-template <int R, int TILE> __device__ __forceinline__ bool item_at(const AttnArgs &a, int64_t at, int lane, Walk &w) {
+// All 32 lanes: the beginning of item `at`, left = 0; false where there are not so many. Reports the bad sequences on its
+// way, and with `last` those behind it too, which may have no item.
+template <int R, int TILE>
+__device__ __forceinline__ bool item_at(const AttnArgs &a, int64_t at, int lane, bool last, Walk &w) {
     int64_t before = 0;
     for (int b0 = 0; b0 < a.c.B; b0 += 32) {
         int64_t mine = 0;
-        if (b0 + lane < a.c.B) mine = (int64_t)seq_at<R, TILE>(a, b0 + lane, at == 0).blocks * a.c.Hk;
+        if (b0 + lane < a.c.B) mine = (int64_t)seq_at<R, TILE>(a, b0 + lane, true).blocks * a.c.Hk;
         int64_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -172,6 +174,8 @@ template <int R, int TILE> __device__ __forceinline__ bool item_at(const AttnArg
             w.s = seq_at<R, TILE>(a, w.b, false);
             w.t = 0;
             w.left = 0;
+            if (last)
+                for (int b = b0 + 32 + lane; b < a.c.B; b += 32) seq_at<R, TILE>(a, b, true);
             return true;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);

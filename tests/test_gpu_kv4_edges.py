@@ -121,3 +121,86 @@ def test_long_lines_of_work_are_counted(env, tiles_of, n, length, group, Hk, cau
     first = max(length - n - window + 1, 0) // 64 if window else 0
     few = -(-n * group // 16) * Hk * (-(-length // 64) - first)
     assert out.tolist() == [many, few]
+
+
+def _reported(kda):
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_sync_status()
+    assert e.value.status == kda.KDA_ERR_DEVICE_CHECK
+    kda.kda_sync_status()  # and cleared
+
+
+@pytest.mark.parametrize("where", [40, 63])
+@pytest.mark.parametrize("cols,Hq,dt", [(4, 4, "bfloat16"), (4, 2, "float32"), (1000, 4, "bfloat16"), (4, 40, "bfloat16")])
+@pytest.mark.parametrize("what", ["long", "negative", "offsets", "past"])
+def test_bad_lengths_far_down_the_batch_are_reported(env, where, cols, Hq, dt, what):  # noqa: F811
+    """More sequences than a warp has lanes, a bad one behind the first 32: in the cluster form, in runs, in the
+    kernel for many rows."""
+    torch, kda = env
+    B, Hk, D = 64, 2, 64
+    rng = np.random.default_rng(where + cols)
+    lens = [int(x) for x in rng.integers(1, 60, B)]
+    cache, tb, lt, _ = _filled(torch, kda, rng, lens, 16, Hk, D, cols=cols)
+    q = _dev(torch, rng.normal(size=(B, Hq, D))).to(getattr(torch, dt))
+    good, out = torch.empty_like(q), torch.full_like(q, 7.0)
+    cu = torch.arange(B + 1, device="cuda") if what in ("offsets", "past") else None
+    kda.kda_kv4_attention(q, cache, tb, lt, good, cu_seqlens=cu)
+    kda.kda_sync_status()
+    bad = lt.clone()
+    clean = [b for b in range(B) if b != where]
+    if what == "long":
+        bad[where] = 16 * cols + 1
+    elif what == "negative":
+        bad[where] = -1
+    elif what == "past":  # ends behind the call's rows (the last one); starts before them (another)
+        if where == B - 1:
+            cu[B] = B + 1
+        else:
+            cu[where] = -3
+            clean.remove(where - 1)
+    else:
+        cu[where] = where - 4  # the sequence before ends before it starts, this one overlaps those before it
+        clean = [b for b in range(B) if not where - 4 <= b <= where]
+    kda.kda_kv4_attention(q, cache, tb, bad if cu is None else lt, out, cu_seqlens=cu)
+    _reported(kda)
+    assert torch.equal(out[clean], good[clean])
+
+
+def test_empty_sequences_with_bad_lengths_are_reported(env):  # noqa: F811
+    """Sequences without new tokens that no block of rows belongs to, the last ones of the batch."""
+    torch, kda = env
+    rng = np.random.default_rng(3)
+    B, D = 70, 64
+    lens = [int(x) for x in rng.integers(1, 60, B)]
+    for new, Hq in ((1, 2), (30, 2), (1, 40)):
+        cache, tb, lt, _ = _filled(torch, kda, rng, lens, 16, 1, D, cols=4)
+        q = _dev(torch, rng.normal(size=(new, Hq, D))).to(torch.bfloat16)
+        good, out = torch.empty_like(q), torch.empty_like(q)
+        cu = torch.full((B + 1,), new, device="cuda")
+        cu[0] = 0
+        kda.kda_kv4_attention(q, cache, tb, lt, good, cu_seqlens=cu)
+        kda.kda_sync_status()
+        lt[B - 1] = -1
+        kda.kda_kv4_attention(q, cache, tb, lt, out, cu_seqlens=cu)
+        _reported(kda)
+        assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("Hq,new", [(4, 1), (4, 40), (40, 1), (6, 3)])
+def test_pages_outside_the_cache_are_reported_in_every_form(env, Hq, new):  # noqa: F811
+    torch, kda = env
+    rng = np.random.default_rng(Hq + new)
+    lens, D, Hk = [50, 200, 90], 128, 2
+    cache, tb, lt, _ = _filled(torch, kda, rng, lens, 32, Hk, D)
+    q = _dev(torch, rng.normal(size=(3 * new, Hq, D))).to(torch.bfloat16)
+    cu = torch.arange(0, 3 * new + 1, new, device="cuda")
+    good, out, before = torch.empty_like(q), torch.empty_like(q), cache.clone()
+    kda.kda_kv4_attention(q, cache, tb, lt, good, cu_seqlens=cu)
+    kda.kda_sync_status()
+    for page in (cache.shape[0], -1, 1 << 30):
+        bad = tb.clone()
+        bad[1, 3] = page
+        kda.kda_kv4_attention(q, cache, bad, lt, out, cu_seqlens=cu)
+        _reported(kda)
+        assert torch.equal(out[:new], good[:new]) and torch.equal(out[2 * new:], good[2 * new:])
+    assert torch.equal(cache, before)
