@@ -649,9 +649,13 @@ kda_status kda_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_o
  * kda_kv4_attention's out are zero. Lengths and offsets may pass 32 bits where
  * the products of sizes do; table_cols * page_size is at most 2^31 - 256, B at most
  * 2^30, T at most 2^31 - 1 (for attention T * Hq at most 2^31 - 256) and Hk at most 32768.
+ * A sequence that counts fewer tokens than are new has none before its beginning:
+ * they are not written or read, and see nothing where causal is 1.
  * A page or length outside the cache and cu_seqlens out of order are found on
- * the device: nothing outside the tensors is touched, the rows concerned are
- * skipped or meaningless, and kda_sync_status reports KDA_ERR_DEVICE_CHECK.
+ * the device, for sequences without new tokens too: nothing outside the tensors is
+ * touched, nothing is written or read for a sequence whose offsets or length are
+ * wrong, its rows of kda_kv4_attention's out are skipped or meaningless, and
+ * kda_sync_status reports KDA_ERR_DEVICE_CHECK.
  * Programmatic dependent launches that wait for the kernel before them.
  */
 size_t kda_kv4_cache_bytes(int64_t pages, int Hk, int page_size, int D);

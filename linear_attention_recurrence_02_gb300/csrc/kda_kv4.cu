@@ -42,16 +42,26 @@ template <typename T> __device__ __forceinline__ uint32_t codes_of(const Raw8<T>
     else return quantise8(x, s);
 }
 
+// A launch's first CTAs look at every sequence, for a wrong one may have no token: at CHECKED each. (The others' threads
+// asked for one sequence each, 81393 tokens read in 82 us instead of 72.)
+constexpr int CHECKED = 16 * NT;
+__device__ __forceinline__ void check_sequences(const Cache &c, unsigned *err) {
+    unsigned bad = 0;
+    for (int b = blockIdx.x * CHECKED + threadIdx.x; b < c.B && b < (int)(blockIdx.x + 1) * CHECKED; b += NT) bad |= range_of(c, b).bad;
+    if (bad) atomicOr(err, bad);
+}
+
 // HU heads a thread, a token's lookup (sequence, length, page) shared by them.
 template <int D, typename T, int HU>
 __global__ void __launch_bounds__(NT) kv4_append_kernel(const T *k, const T *v, Cache c, int64_t k_stride,
-                                                        int64_t v_stride, unsigned *err) {
+                                                        int64_t v_stride, int checks, unsigned *err) {
     constexpr int LPR = D / 8;  // lanes of a row
     const int hc = (c.Hk + HU - 1) / HU;
-    const int64_t unit = ((int64_t)blockIdx.x * NT + threadIdx.x) / LPR;
+    const int64_t unit = ((int64_t)((int)blockIdx.x - checks) * NT + threadIdx.x) / LPR;
     const int64_t t = unit / hc;
     const int h0 = (int)(unit - t * hc) * HU, w = threadIdx.x % LPR, g = w >> 2, j = w & 3;
     dependent_launch();
+    if ((int)blockIdx.x < checks) return check_sequences(c, err);
     Raw8<T> rk[HU] = {}, rv[HU] = {};
 #pragma unroll
     for (int u = 0; u < HU; ++u)
@@ -105,13 +115,14 @@ template <> __device__ __forceinline__ void store_values(float *p, const uint32_
 
 template <int D, typename T, int HU>
 __global__ void __launch_bounds__(NT) kv4_read_kernel(Cache c, T *k, T *v, int64_t k_stride, int64_t v_stride,
-                                                      unsigned *err) {
+                                                      int checks, unsigned *err) {
     constexpr int LPR = D / 8;
     const int hc = (c.Hk + HU - 1) / HU;
-    const int64_t unit = ((int64_t)blockIdx.x * NT + threadIdx.x) / LPR;
+    const int64_t unit = ((int64_t)((int)blockIdx.x - checks) * NT + threadIdx.x) / LPR;
     const int64_t t = unit / hc;
     const int h0 = (int)(unit - t * hc) * HU, w = threadIdx.x % LPR, g = w >> 2, j = w & 3;
     dependent_launch();
+    if ((int)blockIdx.x < checks) return check_sequences(c, err);
     int b = 0, page = -1;
     int64_t pos = 0;
     if (t < c.T && token_place(c, t, b, pos)) page = page_of(c, b, pos, err);
@@ -192,27 +203,28 @@ static kda_status check_rows(const void *k, const void *v, int64_t k_stride, int
 constexpr int APPEND_HEADS = 4, READ_HEADS = 2;
 template <typename F> static kda_status launch_rows(const Cache &c, int D, int most, F &&go) {
     const int hu = c.T * c.Hk * (D / 8) >= (int64_t)current_sms() * 2048 * 4 && c.Hk >= most ? most : 1;
-    const int64_t blocks = (c.T * ((c.Hk + hu - 1) / hu) * (D / 8) + NT - 1) / NT;
+    const int checks = (int)(((int64_t)c.B + CHECKED - 1) / CHECKED);
+    const int64_t blocks = (c.T * ((c.Hk + hu - 1) / hu) * (D / 8) + NT - 1) / NT + checks;
     if (blocks > 0x7fffffffLL) return invalid("T*Hk*D too large for one launch");
-    go((unsigned)blocks, hu > 1);
+    go((unsigned)blocks, checks, hu > 1);
     return KDA_OK;
 }
 
 template <int D, typename T>
 static kda_status append(const void *k, const void *v, const Cache &c, int64_t ks, int64_t vs, unsigned *err,
                          cudaStream_t s) {
-    const kda_status st = launch_rows(c, D, APPEND_HEADS, [&](unsigned blocks, bool several) {
+    const kda_status st = launch_rows(c, D, APPEND_HEADS, [&](unsigned blocks, int checks, bool several) {
         auto kern = several ? kv4_append_kernel<D, T, APPEND_HEADS> : kv4_append_kernel<D, T, 1>;
         launch_dependent(kern, dim3(blocks), dim3(NT), 0, s, static_cast<const T *>(k), static_cast<const T *>(v), c, ks,
-                         vs, err);
+                         vs, checks, err);
     });
     return st ? st : check_launch("kv4_append_kernel");
 }
 template <int D, typename T>
 static kda_status read(const Cache &c, void *k, void *v, int64_t ks, int64_t vs, unsigned *err, cudaStream_t s) {
-    const kda_status st = launch_rows(c, D, READ_HEADS, [&](unsigned blocks, bool several) {
+    const kda_status st = launch_rows(c, D, READ_HEADS, [&](unsigned blocks, int checks, bool several) {
         auto kern = several ? kv4_read_kernel<D, T, READ_HEADS> : kv4_read_kernel<D, T, 1>;
-        launch_dependent(kern, dim3(blocks), dim3(NT), 0, s, c, static_cast<T *>(k), static_cast<T *>(v), ks, vs, err);
+        launch_dependent(kern, dim3(blocks), dim3(NT), 0, s, c, static_cast<T *>(k), static_cast<T *>(v), ks, vs, checks, err);
     });
     return st ? st : check_launch("kv4_read_kernel");
 }

@@ -187,13 +187,27 @@ struct Cache {
     int B, Hk, pages, cols, page_shift;
 };
 
+// A sequence's new tokens [t0, t1) and its length, and what is wrong with them: bits of the device error word.
+struct Range {
+    int64_t t0, t1, len;
+    unsigned bad;
+};
+__device__ __forceinline__ Range range_of(const Cache &c, int b) {
+    Range r = {b, (int64_t)b + 1, c.lens[b], 0};
+    if (c.cu) {
+        r.t0 = c.cu[b];
+        r.t1 = c.cu[b + 1];
+        if (r.t0 < 0 || r.t1 < r.t0 || r.t1 > c.T) r.bad |= DEVERR_SEQLENS;
+    }
+    if (r.len < 0 || r.len > (int64_t)c.cols << c.page_shift) r.bad |= DEVERR_PAGES;
+    return r;
+}
+
 // Of new token t: its sequence and its position there; false where it has none (rows behind the last
-// sequence, a sequence of length zero) or where the cache has no place for it, which is flagged.
+// sequence, before the beginning of one that counts fewer tokens than are new, of one that is wrong).
 __device__ __forceinline__ bool token_place(const Cache &c, int64_t t, int &b, int64_t &pos) {
-    int64_t left = 1;  // new tokens of the sequence from this one on
-    if (c.cu == nullptr) {
-        b = (int)t;
-    } else {
+    b = (int)t;
+    if (c.cu) {
         int lo = 0, hi = c.B;  // the last b with cu[b] <= t
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -201,11 +215,10 @@ __device__ __forceinline__ bool token_place(const Cache &c, int64_t t, int &b, i
             else hi = mid;
         }
         b = lo;
-        left = c.cu[b + 1] - t;
-        if (left <= 0 || c.cu[b] > t) return false;
     }
-    pos = c.lens[b] - left;
-    return pos >= 0;
+    const Range r = range_of(c, b);
+    pos = r.len - (r.t1 - t);
+    return r.bad == 0 && r.t0 <= t && t < r.t1 && pos >= 0;
 }
 // The page of position pos of sequence b, or -1 with the error word set.
 __device__ __forceinline__ int page_of(const Cache &c, int b, int64_t pos, unsigned *err) {

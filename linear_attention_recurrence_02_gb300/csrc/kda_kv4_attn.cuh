@@ -64,24 +64,12 @@ struct Seq {
 
 template <int R, int TILE> __device__ __forceinline__ Seq seq_at(const AttnArgs &a, int b, bool flag) {
     Seq s;
-    int64_t t0 = b, t1 = b + 1, len = a.c.lens[b];
-    unsigned bad = 0;
-    if (a.c.cu) {
-        t0 = a.c.cu[b];
-        t1 = a.c.cu[b + 1];
-        if (t0 < 0 || t1 < t0 || t1 > a.c.T) {
-            bad |= DEVERR_SEQLENS;
-            t1 = t0 = 0;
-        }
-    }
-    const int64_t most = (int64_t)a.c.cols << a.c.page_shift;
-    if (len < 0 || len > most) {
-        bad |= DEVERR_PAGES;
-        len = len < 0 ? 0 : most;
-    }
-    if (bad && flag) atomicOr(a.err, bad);
-    s.t0 = t0;
-    s.n = (int)(t1 - t0);
+    const Range r = range_of(a.c, b);
+    if (r.bad && flag) atomicOr(a.err, r.bad);
+    const bool none = r.bad & DEVERR_SEQLENS;
+    const int64_t len = max((int64_t)0, min(r.len, (int64_t)a.c.cols << a.c.page_shift));
+    s.t0 = r.t0;
+    s.n = none ? 0 : (int)(r.t1 - r.t0);
     s.len = (int)len;
     const int rows = s.n * a.group;
     if (rows > a.most_rows || rows < a.least_rows) s.n = 0;

@@ -204,3 +204,65 @@ def test_pages_outside_the_cache_are_reported_in_every_form(env, Hq, new):  # no
         _reported(kda)
         assert torch.equal(out[:new], good[:new]) and torch.equal(out[2 * new:], good[2 * new:])
     assert torch.equal(cache, before)
+
+
+_BAD_SEQUENCES = {  # lens, cu_seqlens (None: one new token each), tokens of the call; which of its tokens may be written
+    "past the rows": ([9], [0, 3], 2, []),
+    "before the rows": ([9, 9], [-2, 1, 3], 3, [1, 2]),
+    "falling": ([9, 9, 9], [0, 2, 1, 3], 3, [0, 1, 2]),
+    "falling behind all rows": ([9, 9, 9], [0, 3, 5, 2], 3, [0, 1, 2]),
+    "empty, past the rows": ([9, 9, 9], [0, 1, 3, 4], 3, [0, 1, 2]),
+    "negative length": ([9, -4, 9], None, 3, [0, 2]),
+    "long": ([9, 49, 9], None, 3, [0, 2]),
+    "long, several": ([9, 50, 9], [0, 1, 3, 5], 5, [0, 3, 4]),
+    "far": ([9, 1 << 40, 9], [0, 1, 3, 5], 5, [0, 3, 4]),
+    "lowest": ([9, -(1 << 63), 9], [0, 1, 3, 5], 5, [0, 3, 4]),
+    "negative length of an empty one": ([9, -1, 9], [0, 1, 1, 3], 3, [0, 1, 2]),
+    "long one of an empty one": ([9, 4000, 9], [0, 1, 1, 3], 3, [0, 1, 2]),
+    "far down": ([9] * 600 + [-1], None, 601, list(range(600))),
+    "far down, empty": ([9] * 600 + [-1], [0, 3] + [3] * 600, 3, [0, 1, 2]),
+}
+
+
+@pytest.mark.parametrize("name", list(_BAD_SEQUENCES))
+@pytest.mark.parametrize("Hk", [2, 70])
+def test_append_and_read_report_bad_sequences(env, name, Hk):  # noqa: F811
+    """Nothing is written or read for a sequence whose offsets or length cannot be, and the status says so, whether or
+    not one of the call's tokens is its."""
+    torch, kda = env
+    lens, cu, T, may = _BAD_SEQUENCES[name]
+    B, D, page, cols = len(lens), 64, 16, 3
+    table = _dev(torch, np.arange(B * cols, dtype=np.int32).reshape(B, cols))
+    before = torch.randint(0, 256, (B * cols, Hk, 1, 18 * D), dtype=torch.uint8, device="cuda",
+                           generator=torch.Generator(device="cuda").manual_seed(1))
+    cache, lt = before.clone(), torch.tensor(lens, device="cuda")
+    ct = None if cu is None else torch.tensor(cu, device="cuda")
+    k = torch.randn((T, Hk, D), device="cuda")
+    kda.kda_kv4_append(k, k, cache, table, lt, cu_seqlens=ct)
+    _reported(kda)
+    ok = set()  # the pages that a token which may be written can go to
+    seq = range(B) if cu is None else [max((b for b in range(B) if cu[b] <= t), default=0) for t in range(T)]
+    for t in may:
+        ok.update(range(cols * seq[t], cols * seq[t] + cols))
+    for p in (cache != before).flatten(1).any(1).nonzero().flatten().tolist():
+        assert p in ok, (p, name)
+    ko, vo = torch.full_like(k, 7.0), torch.full_like(k, 7.0)
+    kda.kda_kv4_read(cache, table, lt, ko, vo, cu_seqlens=ct)
+    _reported(kda)
+    for t in range(T):
+        if t not in may:
+            assert bool((ko[t] == 7).all()) and bool((vo[t] == 7).all()), t
+
+
+def test_append_and_read_leave_padding_alone(env):  # noqa: F811
+    """Sequences of length 0, empty ones and more new tokens than a sequence counts are not errors."""
+    torch, kda = env
+    table = torch.arange(6, dtype=torch.int32, device="cuda").view(3, 2)
+    cache = torch.zeros((6, 1, 1, 18 * 64), dtype=torch.uint8, device="cuda")
+    k = torch.randn((9, 1, 64), device="cuda")
+    for lens, cu in (([0, 0, 32], [0, 3, 3, 5]), ([2, 0, 1], [0, 4, 4, 9]), ([5, 32, 0], [0, 0, 0, 0])):
+        lt, ct = torch.tensor(lens, device="cuda"), torch.tensor(cu, device="cuda")
+        kda.kda_kv4_append(k, k, cache, table, lt, cu_seqlens=ct)
+        kda.kda_kv4_read(cache, table, lt, k.clone(), k.clone(), cu_seqlens=ct)
+    kda.kda_kv4_append(k[:3], k[:3], cache, table, torch.tensor([0, 32, 0], device="cuda"))
+    kda.kda_sync_status()
