@@ -694,8 +694,8 @@ kda_status kda_kv4_read(const void *cache, const int32_t *block_table, const int
  * not see it are not touched.
  * Cached tokens are cut into equal runs for the SMs whatever the lengths, and the
  * pieces joined in a fixed order: the same call gives the same bits.
- *   workspace: kda_kv4_attention_workspace_bytes bytes (of the current device, for the
- *   call's sizes; it does not depend on lengths, and may be 0: then NULL will do), 16-byte
+ *   workspace: kda_kv4_attention_workspace_bytes bytes (on the stream's device made current, for
+ *   the call's sizes; it does not depend on lengths, and may be 0: then NULL will do), 16-byte
  *   aligned; scratch, needs no clearing, not shared by calls that may overlap.
  */
 kda_status kda_kv4_attention(const void *q, const void *cache, const int32_t *block_table, const int64_t *lens,

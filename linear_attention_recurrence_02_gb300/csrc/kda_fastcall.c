@@ -465,7 +465,11 @@ static PyObject *kv4_attention(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (a[10] == Py_None) {
         const size_t need = S.kv4_space((int)c.B, c.T, (int)Hq, (int)c.Hk, (int)c.D, c.page, (int)c.cols,
                                         a[5] != Py_None, window, q.dt);
-        if (need > 0) return PyLong_FromLongLong(-(long long)need);
+        if (need > 0) {  /* of the current device, which has to be the tensors' */
+            long long cur;
+            if (!long_of(PyObject_CallNoArgs(S.get_device), &cur)) return NULL;
+            return PyLong_FromLongLong(cur == q.dev ? -(long long)need : -1);
+        }
         size = 0;
     }
     for (int i = 0; a[10] != Py_None && i < ws.nd; ++i) size *= (size_t)ws.dim[i];

@@ -731,11 +731,6 @@ template <int D, typename T, int R> kda_status launch_join(const AttnArgs &a, cu
 template kda_status launch_join<128, __nv_bfloat16, 256>(const AttnArgs &a, cudaStream_t s);
 template kda_status launch_join<64, __nv_bfloat16, 256>(const AttnArgs &a, cudaStream_t s);
 
-static int few_ctas(int per_sm) {
-    const int sms = current_sms();
-    return per_sm * (sms > 0 ? sms : 152);
-}
-
 // Blocks of R rows and tiles of an item that these sizes allow, and the CTAs of a cluster where a cluster has one item
 // (0: the CTAs have runs). One item a cluster, of as many CTAs as fit the card at once, saves the second kernel (5 us
 // a call where launches follow one another) but leaves the SMs as unequal work as the lengths are: taken where even
@@ -760,7 +755,7 @@ static FewPlan plan_few(const AttnArgs &a, int R, int cap, bool one_block) {
 
 template <int D, typename T, int NTL> static kda_status attn_few(AttnArgs a, cudaStream_t s) {
     using Sm = FewSmem<D, NTL, sizeof(T) == 4 ? 3 : 1>;
-    const int cap = few_ctas(few_per_sm(D));
+    const int cap = a.sms * few_per_sm(D);
     const FewPlan plan = plan_few(a, Sm::R, cap, a.most_rows <= Sm::R);
     if (plan.group > 0) {
         constexpr auto kern = kv4_attn_few_kernel<D, T, NTL, true>;
@@ -804,6 +799,10 @@ struct Route {
     int row_tiles;   // of 8 rows, of the kernel for few rows
     size_t bytes;
 };
+static int sms_here() {
+    const int sms = current_sms();
+    return sms > 0 ? sms : 152;
+}
 static Route route(const AttnArgs &a, int D, kda_dtype dtype) {
     Route r = {false, true, 1, 0};
     if (dtype == KDA_BF16) {
@@ -813,9 +812,9 @@ static Route route(const AttnArgs &a, int D, kda_dtype dtype) {
         r.few = a.group <= FEW_ROWS;
         r.row_tiles = !a.c.cu && a.group <= 8 ? 1 : 2;
     }
-    const int cap = few_ctas(few_per_sm(D));
+    const int cap = a.sms * few_per_sm(D);
     if (r.few && plan_few(a, 8 * r.row_tiles, cap, r.many).group == 0) r.bytes = pieces_bytes(cap, 8 * r.row_tiles, D);
-    if (r.many) r.bytes = std::max(r.bytes, many_bytes(D));
+    if (r.many) r.bytes = std::max(r.bytes, many_bytes(a.sms, D));
     return r;
 }
 }  // namespace kv4
@@ -837,6 +836,7 @@ extern "C" size_t kda_kv4_attention_workspace_bytes(int B, int64_t T, int Hq, in
     while ((1 << a.c.page_shift) < page_size) ++a.c.page_shift;
     a.group = Hq / Hk;
     a.window = window > 0x7fffff00LL ? 0 : (int)window;
+    a.sms = kv4::sms_here();
     return kv4::route(a, D, dtype).bytes;
 }
 
@@ -878,11 +878,13 @@ extern "C" kda_status kda_kv4_attention(const void *q, const void *cache, const 
     a.scale_log2 = scale * 1.44269504f;
     a.most_rows = 0x7fffffff;
     a.least_rows = 0;
+    // the pieces' room and the launches go by one device, the stream's, whichever was current
+    if ((st = bind_stream_device(stream))) return st;
+    a.sms = kv4::sms_here();
     const kv4::Route r = kv4::route(a, D, dtype);
     if (workspace_bytes < r.bytes) return invalid("workspace too small (kda_kv4_attention_workspace_bytes)");
     if (r.bytes && (st = check_ptr(workspace, "workspace"))) return st;
     a.part = static_cast<float *>(workspace);
-    if ((st = bind_stream_device(stream))) return st;
     if (!(a.err = device_error_word())) return fail(KDA_ERR_CUDA, "device error word unavailable");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == KDA_F32) return D == 128 ? kv4::attn_few<128, float, 1>(a, s) : kv4::attn_few<64, float, 1>(a, s);

@@ -49,6 +49,7 @@ struct AttnArgs {
     Div by_group, by_hk;
     int causal, window;
     float scale_log2;  // scale * log2(e)
+    int sms;          // of the stream's device
     int ctas;         // CTAs that cut the line
     int most_rows;    // sequences with more rows a key/value head are another kernel's
     int least_rows;   // and those with fewer
@@ -277,9 +278,9 @@ inline void place_pieces(AttnArgs &a, void *workspace, int R, int D) {
     a.joint = reinterpret_cast<Joint *>(a.ml + (size_t)a.ctas * 2 * R);
 }
 
-// The kernel for many rows (bf16): blocks of 256 rows, tcgen05. Uses many_bytes(D) of a.part.
+// The kernel for many rows (bf16): blocks of 256 rows, tcgen05. Uses many_bytes(a.sms, D) of a.part.
 kda_status attn_many(const AttnArgs &a, int D, cudaStream_t s);
-size_t many_bytes(int D);
+inline size_t many_bytes(int sms, int D) { return pieces_bytes(sms, 256, D); }
 
 // Launches the kernel that joins the pieces of items of R rows.
 template <int D, typename T, int R> kda_status launch_join(const AttnArgs &a, cudaStream_t s);

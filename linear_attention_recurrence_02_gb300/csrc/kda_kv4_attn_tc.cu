@@ -848,18 +848,12 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
 
 }  // namespace many
 
-int many_ctas() {
-    const int sms = current_sms();
-    return sms > 0 ? sms : 152;
-}
-size_t many_bytes(int D) { return pieces_bytes(many_ctas(), many::R, D); }
-
 template <int D> static kda_status run_many(AttnArgs a, cudaStream_t s) {
     using Sm = many::Smem<D>;
     constexpr auto kern = many::kv4_attn_many_kernel<D>;
     if (smem_attr_once<kern>(Sm::BYTES) != cudaSuccess) return check_launch("kv4_attn_many_kernel: shared memory");
     const int64_t blocks = a.c.T * a.group / many::R + a.c.B, tiles = ((int64_t)a.c.cols << a.c.page_shift) / many::TILE + 1;
-    a.ctas = ctas_for(blocks, a.c.Hk, tiles, 1, many_ctas());
+    a.ctas = ctas_for(blocks, a.c.Hk, tiles, 1, a.sms);
     place_pieces(a, a.part, many::R, D);
     launch_dependent(kern, dim3(a.ctas), dim3(many::NT), Sm::BYTES, s, a);
     const kda_status st = check_launch("kv4_attn_many_kernel");
