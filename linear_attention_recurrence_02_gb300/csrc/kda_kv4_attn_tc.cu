@@ -21,7 +21,7 @@
 // own (0.0023 of its root mean square against 0.0017), and the same query over the same cache would be less exact here than
 // in the kernel for few rows. The second term is half as many products again.
 //
-// 4096 queries of 32 heads over 8192 cached tokens of 8 heads of 128: 442 us (0.93 PFLOP/s; with one term 364). A pair of
+// 4096 queries of 32 heads over 8192 cached tokens of 8 heads of 128: 440 us (0.94 PFLOP/s; with one term 364). A pair of
 // tiles takes about 4700 cycles, of which the tensor cores need 3200, and the products of Q and K read shared memory at
 // its full rate. Measured with one term and not taken: half the codes to expand (as two CTAs would share them) 347 us;
 // scores read from TMEM once, the maximum kept per 64 tokens, 369; 64 tokens' scores computed under the other 64's
@@ -39,7 +39,8 @@ namespace kv4 {
 namespace many {
 
 constexpr int R = 256, TILE = 128, NT = 512;
-constexpr uint32_t WAIT_TRIES = 1u << 25;        // of a wait before it gives up (about 1 s)
+constexpr long long WAIT_LIMIT = 2000000000LL;  // clock cycles of a wait before it gives up (about 1 s)
+constexpr long long TILE_LIMIT = 100000;        // and for every tile that it is behind (one takes some 2500)
 constexpr float SLACK = 8.f;                    // log2 of how far scores may pass the reference maximum
 // What starting and finishing an item costs, in tiles: a run of many short items has as much less to compute (8192 queries
 // of a prompt, 32 over 8 heads: 489 us; counted as two tiles 546, as one 664).
@@ -128,26 +129,6 @@ __device__ __forceinline__ void next_part(const AttnArgs &a, Place &w, Part &g) 
         g.there = true;
         return;
     }
-}
-
-// A bounded wait of few instructions: the waiting warps' polls take issue slots and integer units from the
-// working ones (a clock read and compared each time made a third of all instructions). NS > 0: nanoseconds
-// between the tries of a warp that is not in a hurry.
-template <int NS> __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
-    uint32_t there;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(there)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (there) return true;
-    for (uint32_t n = NS > 0 ? WAIT_TRIES / 8 : WAIT_TRIES; n > 0; --n) {
-        if (tc::mbar_try_wait(bar, parity)) return true;
-        if constexpr (NS > 0) __nanosleep(NS);
-    }
-    return false;
 }
 
 // ---------------------------------------------------------------- issuing
@@ -347,10 +328,10 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
         if (lane == 0) atomicOr(a.err, DEVERR_TIMEOUT);
     };
     auto wait = [&](uint64_t *b, int parity) {  // all lanes
-        if (ok && !__all_sync(0xffffffffu, wait_for<0>(b, parity))) gave_up();
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_lean<0>(b, parity, WAIT_LIMIT))) gave_up();
     };
-    auto wait_idly = [&](uint64_t *b, int parity) {
-        if (ok && !__all_sync(0xffffffffu, wait_for<100>(b, parity))) gave_up();
+    auto wait_idly = [&](uint64_t *b, int parity, int tiles) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_lean<100>(b, parity, WAIT_LIMIT + TILE_LIMIT * tiles))) gave_up();
     };
     // All lanes: the run's next part, in the one of the warp's two places that the current part does not have. Parts
     // stay in shared memory: they are looked at once per item, and registers are short.
@@ -814,14 +795,14 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
         if (warp > 12 && work) {
             // ------------------------------------------------ an item's rows of q, 16 bytes a lane
             const int c = lane & (D / 8 - 1);  // of a row's chunks
-            int n[2] = {0, 0};
+            int n[2] = {0, 0}, behind = 0;  // behind: tiles of the item whose rows are there
             for (const Part *g = advance(); g->there; g = advance()) {
                 if (g->first >= g->last) continue;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int r0 = g->block * R + 128 * i, rows = g->n * a.group - r0;
                     if (rows <= 0) break;
-                    wait_idly(bar->q_empty + i, (n[i]++ & 1) ^ 1);
+                    wait_idly(bar->q_empty + i, (n[i]++ & 1) ^ 1, behind);
                     for (int row = (warp - 13) * (256 / D) + lane / (D / 8); row < 128; row += 3 * (256 / D)) {
                         const int ti = a.by_group(r0 + row);
                         const bool live = row < rows;
@@ -838,6 +819,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar->q_full + i);
                 }
+                behind = g->last - g->first;
             }
         }
     }

@@ -90,14 +90,19 @@ extern "C" int tiles_of(const int64_t *lens, const int64_t *cu, int64_t T, int g
 """
 
 
+def _compiled(where, name, source):
+    """A small library of kernels that include the library's own headers."""
+    from linear_attention_recurrence_02_gb300 import build
+    (where / (name + ".cu")).write_text(source)
+    subprocess.run([build._nvcc(), "-O2", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", *build.ARCH, "-I",
+                    build.INCLUDE, "-I", build.CSRC, "-shared", "-o", str(where / (name + ".so")),
+                    str(where / (name + ".cu"))], check=True)
+    return ctypes.CDLL(str(where / (name + ".so")))
+
+
 @pytest.fixture(scope="module")
 def tiles_of(env, tmp_path_factory):  # noqa: F811
-    from linear_attention_recurrence_02_gb300 import build
-    d = tmp_path_factory.mktemp("line")
-    (d / "line.cu").write_text(_LINE)
-    subprocess.run([build._nvcc(), "-O2", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", *build.ARCH, "-I",
-                    build.INCLUDE, "-I", build.CSRC, "-shared", "-o", str(d / "line.so"), str(d / "line.cu")], check=True)
-    fn = ctypes.CDLL(str(d / "line.so")).tiles_of
+    fn = _compiled(tmp_path_factory.mktemp("line"), "line", _LINE).tiles_of
     p, i = ctypes.c_void_p, ctypes.c_int
     fn.argtypes, fn.restype = [p, p, ctypes.c_int64, i, i, i, i, i, p], i
     return fn
@@ -266,3 +271,45 @@ def test_append_and_read_leave_padding_alone(env):  # noqa: F811
         kda.kda_kv4_read(cache, table, lt, k.clone(), k.clone(), cu_seqlens=ct)
     kda.kda_kv4_append(k[:3], k[:3], cache, table, torch.tensor([0, 32, 0], device="cuda"))
     kda.kda_sync_status()
+
+
+_WAIT = """
+#include "kda_common.cuh"
+#include "kda_tc.cuh"
+using namespace kda::tc;
+template <int NS> __device__ void one(uint64_t *bar, long long limit, long long *out) {
+    const long long t0 = clock64();
+    out[0] = mbar_wait_lean<NS>(bar, 0, limit);
+    out[1] = clock64() - t0;
+    mbar_arrive(bar);
+    out[2] = mbar_wait_lean<NS>(bar, 0, limit);
+}
+__global__ void wait_twice(long long limit, long long *out) {
+    __shared__ uint64_t bar[2];
+    if (threadIdx.x == 0) {
+        mbar_init(bar, 1);
+        mbar_init(bar + 1, 1);
+        fence_mbar_init();
+        one<0>(bar, limit, out);
+        one<100>(bar + 1, limit, out + 3);
+    }
+}
+extern "C" int waits(long long limit, long long *out) {
+    wait_twice<<<1, 32>>>(limit, out);
+    return (int)cudaDeviceSynchronize();
+}
+"""
+
+
+def test_a_wait_that_nothing_ends_gives_up_by_the_clock(env, tmp_path):  # noqa: F811
+    """After its limit in clock cycles and at most 64 tries more, however long the hardware suspends a try; one whose
+    barrier has completed does not wait."""
+    torch, _ = env
+    fn = _compiled(tmp_path, "wait", _WAIT).waits
+    fn.argtypes, fn.restype = [ctypes.c_longlong, ctypes.c_void_p], ctypes.c_int
+    out = torch.zeros(6, dtype=torch.int64, device="cuda")
+    torch.cuda.synchronize()
+    for limit in (1_000_000, 20_000_000):
+        assert fn(limit, out.data_ptr()) == 0
+        for gave, cycles, ended in (out[:3].tolist(), out[3:].tolist()):
+            assert gave == 0 and ended == 1 and limit <= cycles < 2 * limit + 20_000_000
