@@ -734,7 +734,10 @@ template kda_status launch_join<64, __nv_bfloat16, 256>(const AttnArgs &a, cudaS
 // Blocks of R rows and tiles of an item that these sizes allow, and the CTAs of a cluster where a cluster has one item
 // (0: the CTAs have runs). One item a cluster, of as many CTAs as fit the card at once, saves the second kernel (5 us
 // a call where launches follow one another) but leaves the SMs as unequal work as the lengths are: taken where even
-// the longest item that the block table has room for gives a warp four tiles at most (8 us).
+// the longest item that the block table has room for gives a warp four tiles at most (8 us), and where the clusters come in
+// three turns at most: each of them looks for its item among all sequences, so that many more take longer than runs do (8
+// key/value heads of 128, 250 tokens a sequence, clusters and runs: 64 sequences 14.4 and 19.4 us, 96 21.2 and 25.0, 128
+// 28.2 and 26.1, 256 53.8 and 48.6, 512 125 and 88; 900 tokens: 96 42.8 and 44.5, 192 80.7 and 74.3).
 struct FewPlan {
     int64_t blocks, tiles;
     int group;
@@ -749,7 +752,7 @@ static FewPlan plan_few(const AttnArgs &a, int R, int cap, bool one_block) {
     if (a.window > 0) p.tiles = std::min(p.tiles, ((int64_t)a.window + (a.c.cu ? a.c.T : 1)) / TILE + 2);
     p.group = MOST_GROUP;
     while (p.group > 1 && (p.blocks * a.c.Hk * p.group > cap || p.group / 2 * WARPS >= p.tiles)) p.group /= 2;
-    if (p.tiles > 4 * WARPS * p.group || p.blocks * a.c.Hk * p.group > 0x7fffffffLL) p.group = 0;
+    if (p.tiles > 4 * WARPS * p.group || p.blocks * a.c.Hk * p.group > 3 * (int64_t)cap) p.group = 0;
     return p;
 }
 

@@ -11,7 +11,7 @@ import numpy as np
 import pytest
 
 from tests import _kv4 as ref
-from tests.test_gpu_kv4 import _dev, _filled, env, half_step, np64  # noqa: F401
+from tests.test_gpu_kv4 import _check, _dev, _filled, env, half_step, np64  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -313,3 +313,18 @@ def test_a_wait_that_nothing_ends_gives_up_by_the_clock(env, tmp_path):  # noqa:
         assert fn(limit, out.data_ptr()) == 0
         for gave, cycles, ended in (out[:3].tolist(), out[3:].tolist()):
             assert gave == 0 and ended == 1 and limit <= cycles < 2 * limit + 20_000_000
+
+
+def test_a_large_batch_of_short_sequences(env):  # noqa: F811
+    """More items than clusters take in a few turns: runs over a narrow block table."""
+    torch, kda = env
+    B, Hq, Hk, D, rng = 260, 8, 4, 64, np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    cache, tb, lt, table = _filled(torch, kda, rng, lens, 16, Hk, D, cols=3)
+    assert kda.kda_kv4_attention_workspace_bytes(2 * B, 2 * B, Hq, Hk, D, 16, 3, False, torch.bfloat16) > 0
+    for dt in (torch.bfloat16, torch.float32):
+        q = _dev(torch, rng.normal(size=(2 * B, Hq, D))).to(dt)
+        out, lse = torch.empty_like(q), torch.empty((2 * B, Hq), device="cuda")
+        kda.kda_kv4_attention(q, cache, tb.repeat(2, 1), lt.repeat(2), out, lse=lse)
+        kda.kda_sync_status()
+        _check(torch, out, lse, q, cache, np.tile(table, (2, 1)), lens + lens, [1] * (2 * B), D ** -0.5, True, 0)

@@ -32,3 +32,11 @@ def test_a_workspace_is_sized_on_the_tensors_device(kda, on_device_0):  # noqa: 
     need = kda.kda_kv4_attention_workspace_bytes(64, 64, 96, 8, 128, 64, 128, False, BF)
     assert need > 1 and call(0) == -need
     assert call(1) == -1
+
+
+def test_many_short_sequences_are_cut_into_runs(kda):  # noqa: F811
+    """Clusters, which need no workspace, as long as they come in a few turns; runs, which do, for more sequences."""
+    size = kda.kda_kv4_attention_workspace_bytes
+    for dt in (BF, torch.float32):
+        assert size(1, 1, 32, 8, 128, 64, 4, False, dt) == 0 and size(64, 64, 32, 8, 128, 64, 4, False, dt) == 0
+        assert size(512, 512, 32, 8, 128, 64, 4, False, dt) > 0 and size(512, 512, 32, 1, 128, 64, 4, True, dt) > 0
