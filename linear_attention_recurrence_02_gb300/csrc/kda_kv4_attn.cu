@@ -36,7 +36,13 @@ namespace kv4 {
 
 constexpr int WARPS = 4, STAGES = 2, TILE = 64, BLOCKS = TILE / BLOCK;
 constexpr int MOST_GROUP = 8;  // CTAs of a cluster
-constexpr int FEW_ROWS = 16;  // rows a key/value head up to which this kernel takes bf16 queries
+// Rows a key/value head up to which this kernel takes bf16 queries, in blocks of 16 that each go over the tokens once more;
+// the kernel for many rows expands them once and works on 128 rows whatever it has. One token of 32 sequences of 8192, 8
+// heads of 128, in us, this kernel and that one: 17 rows 184 and 203, 32 185 and 205, 48 270 and 206; heads of 64: 104 and
+// 169, 105 and 170, 153 and 171; one key/value head: 37 and 41, 37 and 41, 47 and 41; 16 sequences of 1000: 28 and 32, 28
+// and 32, 40 and 33. (Drafts of four tokens, which launch both: 20 rows 201 and 211, of heads of 64 116 and 176; one sequence 41
+// and 36.)
+constexpr int FEW_ROWS = 32;
 constexpr float SLACK = 8.f;  // log2 of how far scores may pass the running maximum before it moves
 
 // Where the run's computing (one for the CTA) and its copies (one a warp) stand. In shared memory, because
@@ -742,12 +748,13 @@ struct FewPlan {
     int64_t blocks, tiles;
     int group;
 };
-// one_block: only sequences of at most R rows are this kernel's (the others went to the one for many rows). A ragged batch
-// is then three launches instead of four as a rule, and no empty clusters (3 prompts of up to 598 tokens, 84 over 7 heads:
-// 83 -> 70 us).
-static FewPlan plan_few(const AttnArgs &a, int R, int cap, bool one_block) {
+// few_rows: only sequences of at most FEW_ROWS rows are this kernel's (the others went to the one for many rows). A ragged
+// batch is then three launches instead of four as a rule, and few empty clusters (3 prompts of up to 598 tokens, 84 over 7
+// heads: 83 -> 70 us).
+static FewPlan plan_few(const AttnArgs &a, int R, int cap, bool few_rows) {
     FewPlan p;
-    p.blocks = one_block ? std::min<int64_t>(a.c.B, a.c.T) : a.c.cu ? a.c.T * a.group / R + a.c.B : (int64_t)a.c.B * ((a.group + R - 1) / R);
+    p.blocks = a.c.cu ? a.c.T * a.group / R + a.c.B : (int64_t)a.c.B * ((a.group + R - 1) / R);
+    if (few_rows) p.blocks = std::min(p.blocks, std::min<int64_t>(a.c.B, a.c.T) * ((FEW_ROWS + R - 1) / R));
     p.tiles = ((int64_t)a.c.cols << a.c.page_shift) / TILE + 1;
     if (a.window > 0) p.tiles = std::min(p.tiles, ((int64_t)a.window + (a.c.cu ? a.c.T : 1)) / TILE + 2);
     p.group = MOST_GROUP;
@@ -759,7 +766,7 @@ static FewPlan plan_few(const AttnArgs &a, int R, int cap, bool one_block) {
 template <int D, typename T, int NTL> static kda_status attn_few(AttnArgs a, cudaStream_t s) {
     using Sm = FewSmem<D, NTL, sizeof(T) == 4 ? 3 : 1>;
     const int cap = a.sms * few_per_sm(D);
-    const FewPlan plan = plan_few(a, Sm::R, cap, a.most_rows <= Sm::R);
+    const FewPlan plan = plan_few(a, Sm::R, cap, a.most_rows <= FEW_ROWS);
     if (plan.group > 0) {
         constexpr auto kern = kv4_attn_few_kernel<D, T, NTL, true>;
         if (smem_attr_once<kern>(Sm::BYTES) != cudaSuccess) return check_launch("kv4_attn_few_kernel: shared memory");

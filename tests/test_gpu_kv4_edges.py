@@ -36,6 +36,10 @@ _FORMS = [
     ([40, 21, 80], [3, 1, 2], 8, 2, 128, 1000),    # runs behind the kernel for many rows
     ([40, 21, 30], [9, 1, 20], 8, 2, 128, 1000),   # up to 128 rows: one row tile
     ([24, 140], None, 40, 1, 64, 4),
+    ([20, 130], None, 40, 2, 128, 1000),           # two blocks of sixteen
+    ([70, 33, 9], None, 34, 2, 64, 4),
+    ([40, 21, 80], [8, 1, 5], 8, 2, 128, 4),
+    ([90, 70, 12], [2, 3, 9], 20, 2, 64, 1000),    # 20, 30 and 90 rows
     ([60, 150], [50, 40], 8, 2, 128, 4),           # two row tiles
     ([45, 300], [33, 70], 12, 2, 64, 1000),
 ]
