@@ -98,6 +98,21 @@ __device__ __forceinline__ int64_t run_length(int64_t total, int ctas, int least
     return c < least ? least : c;
 }
 
+// All 32 lanes: the first lane up to whose end `at` is passed, counting from `before`, each lane with `mine`; `before` is then
+// what stands ahead of it. Without such a lane -1, and `before` is what stands ahead of the next 32.
+__device__ __forceinline__ int lane_past(int64_t mine, int64_t at, int lane, int64_t &before) {
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > at);
+    const int l = past ? __ffs(past) - 1 : -1;
+    before += __shfl_sync(0xffffffffu, past ? upto - mine : upto, past ? l : 31);
+    return l;
+}
+
 // A place in the line.
 struct Walk {
     int64_t left;      // tiles left in the run
@@ -115,24 +130,15 @@ template <int R, int TILE> __device__ __forceinline__ Walk walk_at(const AttnArg
             const Seq s = seq_at<R, TILE>(a, b0 + lane, false);
             mine = (int64_t)s.blocks * a.c.Hk * s.tiles;
         }
-        int64_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + upto > at);
-        if (past) {
-            const int l = __ffs(past) - 1;
+        const int l = lane_past(mine, at, lane, before);
+        if (l >= 0) {
             w.b = b0 + l;
-            const int64_t rest = at - before - __shfl_sync(0xffffffffu, upto - mine, l);
             w.s = seq_at<R, TILE>(a, w.b, false);
-            w.item = (int)div64(rest, w.s.tiles);
-            w.t = (int)(rest - (int64_t)w.item * w.s.tiles);
+            w.item = (int)div64(at - before, w.s.tiles);
+            w.t = (int)(at - before - (int64_t)w.item * w.s.tiles);
             w.left = 0;
             return w;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
     }
     w.b = a.c.B;  // not reached
     w.item = w.t = 0;
@@ -149,17 +155,10 @@ __device__ __forceinline__ bool item_at(const AttnArgs &a, int64_t at, int lane,
     for (int b0 = 0; b0 < a.c.B; b0 += 32) {
         int64_t mine = 0;
         if (b0 + lane < a.c.B) mine = (int64_t)seq_at<R, TILE>(a, b0 + lane, true).blocks * a.c.Hk;
-        int64_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + upto > at);
-        if (past) {
-            const int l = __ffs(past) - 1;
+        const int l = lane_past(mine, at, lane, before);
+        if (l >= 0) {
             w.b = b0 + l;
-            w.item = (int)(at - before - __shfl_sync(0xffffffffu, upto - mine, l));
+            w.item = (int)(at - before);
             w.s = seq_at<R, TILE>(a, w.b, false);
             w.t = 0;
             w.left = 0;
@@ -167,7 +166,6 @@ __device__ __forceinline__ bool item_at(const AttnArgs &a, int64_t at, int lane,
                 for (int b = b0 + 32 + lane; b < a.c.B; b += 32) seq_at<R, TILE>(a, b, true);
             return true;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
     }
     return false;
 }

@@ -271,20 +271,11 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
         int e = 0;
         for (;; e += 32) {  // the entry, 32 at a time
             const int64_t mine = e + lane < entries ? sums[e + lane] : 0;
-            int64_t upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, before + upto > start);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                before += __shfl_sync(0xffffffffu, upto - mine, l);
+            const int l = lane_past(mine, start, lane, before);
+            if (l >= 0) {
                 e += l;
                 break;
             }
-            before += __shfl_sync(0xffffffffu, upto, 31);
         }
         Place w;
         w.b = e * per;
@@ -298,20 +289,11 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             int first = 0, tiles = 0;
             if (k + lane < w.blocks) block_tiles<R, TILE>(a, w.n, w.len, k + lane, first, tiles);
             const int64_t mine = k + lane < w.blocks ? (int64_t)(tiles + ITEM_COST) * a.c.Hk : 0;
-            int64_t upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, before + upto > start);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                before += __shfl_sync(0xffffffffu, upto - mine, l);
+            const int l = lane_past(mine, start, lane, before);
+            if (l >= 0) {
                 w.block = k + l;
                 break;
             }
-            before += __shfl_sync(0xffffffffu, upto, 31);
         }
         enter_block(a, w);
         w.h = (int)div64(start - before, w.tiles + ITEM_COST);
