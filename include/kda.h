@@ -658,6 +658,7 @@ kda_status kda_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_o
  * kda_sync_status reports KDA_ERR_DEVICE_CHECK.
  * Programmatic dependent launches that wait for the kernel before them.
  */
+/* 0 for sizes that the calls below refuse. */
 size_t kda_kv4_cache_bytes(int64_t pages, int Hk, int page_size, int D);
 
 /* New keys and values k, v [T,Hk,D] dtype (tokens at strides in elements that

@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(NT) kv4_read_kernel(Cache c, T *k, T *v, int64
     }
 }
 
+static bool valid_page(int size) { return size >= BLOCK && size <= 256 && (size & (size - 1)) == 0; }
+
 kda_status check_cache(const void *cache, const int32_t *table, const int64_t *lens, const int64_t *cu, int B,
                        int64_t T, int Hk, int D, int page_size, int64_t pages, int cols, int64_t table_stride,
                        kda_dtype dtype, Cache &c) {
@@ -167,7 +169,7 @@ kda_status check_cache(const void *cache, const int32_t *table, const int64_t *l
     if (Hk < 1 || Hk > 32768) return invalid("Hk must be in 1 .. 32768");
     if (D != 64 && D != 128) return invalid("D must be 64 or 128");
     if (dtype != KDA_F32 && dtype != KDA_BF16) return invalid("dtype must be KDA_F32 or KDA_BF16");
-    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
+    if (!valid_page(page_size))
         return invalid("page_size must be 16, 32, 64, 128 or 256");
     if (pages < 1 || pages > 0x7fffffffLL) return invalid("pages must be in 1 .. 2^31 - 1");
     if (cols < 1 || (int64_t)cols * page_size > 0x7fffff00LL)
@@ -235,7 +237,7 @@ static kda_status read(const Cache &c, void *k, void *v, int64_t ks, int64_t vs,
 using namespace kda;
 
 extern "C" size_t kda_kv4_cache_bytes(int64_t pages, int Hk, int page_size, int D) {
-    if (pages < 0 || Hk < 0 || page_size < 0 || page_size % 16 || D < 0 || D % 32) return 0;
+    if (pages < 0 || pages > 0x7fffffffLL || Hk < 1 || Hk > 32768 || !kv4::valid_page(page_size) || (D != 64 && D != 128)) return 0;
     return (size_t)pages * (size_t)Hk * (size_t)(page_size / 16) * 18u * (size_t)D;
 }
 

@@ -665,6 +665,8 @@ def kda_kv4_cache_bytes(pages, Hk, page_size, D) -> int:
 
 def kda_kv4_cache_shape(pages, Hk, page_size, D):
     """Shape of the uint8 tensor that holds `pages` pages of page_size tokens of Hk key/value heads."""
+    if pages != 0 and kda_kv4_cache_bytes(pages, Hk, page_size, D) == 0:
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256, D 64 or 128, Hk 1 to 32768, pages at most 2^31 - 1")
     return pages, Hk, page_size // 16, 18 * D
 
 

@@ -40,3 +40,17 @@ def test_many_short_sequences_are_cut_into_runs(kda):  # noqa: F811
     for dt in (BF, torch.float32):
         assert size(1, 1, 32, 8, 128, 64, 4, False, dt) == 0 and size(64, 64, 32, 8, 128, 64, 4, False, dt) == 0
         assert size(512, 512, 32, 8, 128, 64, 4, False, dt) > 0 and size(512, 512, 32, 1, 128, 64, 4, True, dt) > 0
+
+
+def test_sizes_of_caches_that_the_calls_would_refuse(kda):  # noqa: F811
+    """No bytes, and no shape: rounded down to whole blocks, a page of 40 tokens would be one of 32 that the caller's
+    block table knows nothing of."""
+    for args in ((10, 8, 40, 128), (10, 8, 8, 128), (10, 8, 512, 128), (10, 8, 48, 64), (10, 8, 64, 32), (10, 8, 64, 96),
+                 (10, 0, 64, 128), (10, 32769, 64, 128), (-1, 8, 64, 128), (1 << 31, 8, 64, 128)):
+        assert kda.kda_kv4_cache_bytes(*args) == 0
+        with pytest.raises(ValueError):
+            kda.kda_kv4_cache_shape(*args)
+    for page in (16, 32, 64, 128, 256):
+        assert kda.kda_kv4_cache_shape(3, 2, page, 64) == (3, 2, page // 16, 18 * 64)
+        assert kda.kda_kv4_cache_bytes(3, 2, page, 64) == 3 * 2 * page // 16 * 18 * 64
+    assert kda.kda_kv4_cache_bytes(0, 8, 64, 128) == 0
