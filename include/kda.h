@@ -592,7 +592,9 @@ kda_status kda_chunk_prefill_noalloc(const void *q, const void *k, const void *v
  * layers ("为什么 Kimi K3 敢把 KV Cache 扔掉？一篇讲透 GPT-2 到 K3 的架构进化", section
  * 7: three KDA layers to one of full attention): norms and rotation of the
  * queries and keys, a paged cache that holds keys and values in 4 bits, and
- * attention over it.
+ * attention over it. For layers with query heads in groups over key/value heads of 64
+ * or 128 channels; the latent form that the same pages have between KDA layers (576
+ * channels shared by all heads) and heads of 192 or 256 are not served.
  *
  * kda_qk_norm_rope: RMSNorm of each (token, head) row of q and k and the
  * rotation by the token's position, in one pass.

@@ -3,15 +3,15 @@
 //
 //   y = x / sqrt(mean x^2 + eps) * w;  then pair i of the first R channels turns by position * freq_i
 //
-// Bound by memory: each element is read and written once. A row (token, head) is D / 8 lanes of eight
-// channels, so the sum of squares is a shuffle reduction and a channel's partner R/2 further on is a
-// lane's shuffle away. A CTA owns one token and some or all of its heads: the R/2 sines and cosines are
-// formed once per CTA, while the rows' loads are in flight.
+// Bound by memory: each element is read and written once (in bf16 the issue slots come close behind). A row (token,
+// head) is D / 8 lanes of eight channels, both channels of a pair in one lane, so the sum of squares is a shuffle
+// reduction and the rotation needs none. A CTA owns one token, or several where they have few rows, and some or all of
+// their heads: the R/2 sines and cosines of each are formed once per CTA, while the rows' loads are in flight.
 //
 // Angles: a position's turn is position * freq / 2 pi modulo 1. freq / 2 pi modulo 1 is formed as a 64-bit
 // fraction (2^-64 turns a unit), so the product with an integer position wraps around exactly: the angle
-// of position 2^31 is as good as that of position 1, and its upper 32 bits (2^-32 turns, 1.5e-9 radians)
-// go to the sine and cosine in half turns.
+// of position 2^31 is as good as that of position 1. Its upper 32 bits go to the sine and cosine as an fp32 number of
+// half turns in [-1, 1], off by at most 2^-25 of one: 9.4e-8 radians.
 #include <algorithm>
 #include <string>
 
@@ -44,7 +44,7 @@ __device__ __forceinline__ float2 turn_of(const RopeArgs &a, int64_t pos, int i)
                   : down < 64 ? (lo >> down) | (hi << (64 - down)) : down < 128 ? hi >> (down - 64) : 0;
     if (bits >> 63) unit = 0 - unit;
     const uint64_t phase = (uint64_t)pos * unit;
-    float x = (float)(int32_t)(phase >> 32) * 0x1p-31f;  // half turns in [-1, 1)
+    float x = (float)(int32_t)(phase >> 32) * 0x1p-31f;  // half turns in [-1, 1]
     if (e == 0x7ff) x = __int_as_float(0x7fc00000);
     float sn, cs;
     sincospif(x, &sn, &cs);
@@ -138,8 +138,8 @@ __device__ __forceinline__ void norm_and_turn(float2 (&x)[4], const float *w, co
 // with 59 as the compiler likes it 61, and 54 instead of 45 for 4096 tokens of 96 + 8 heads; tokens streamed through
 // shared memory by persistent CTAs 71: the rows' arithmetic needs more warps than that leaves; several tokens one after
 // another in a CTA, the next one's rows loaded ahead, 62; lanes of two 16-byte vectors, half as many, 65). What bounds it
-// is a CTA's chain of loads, angles, barrier and stores with the warps that registers allow: fp32 rows, twice the bytes
-// behind each angle, move at 6.5 TB/s.
+// is issue slots (73 % used; ALU 45 %) and a CTA's chain of loads, angles, barrier and stores with the warps that
+// registers allow: fp32 rows, twice the bytes behind each angle, move at 6.5 TB/s.
 template <int D, typename T, bool INTER, int UP, bool ONE>
 __global__ void __maxnreg__(sizeof(T) == 2 ? 48 : 64) qk_norm_rope_kernel(const RopeArgs a, int64_t T_, int many, int slots) {
     constexpr int LPR = D / 8;
