@@ -21,8 +21,8 @@
 // own (0.0023 of its root mean square against 0.0017), and the same query over the same cache would be less exact here than
 // in the kernel for few rows. The second term is half as many products again.
 //
-// 4096 queries of 32 heads over 8192 cached tokens of 8 heads of 128: 440 us (0.94 PFLOP/s; with one term 364). A pair of
-// tiles takes about 4700 cycles, of which the tensor cores need 3200, and the products of Q and K read shared memory at
+// 4096 queries of 32 heads over 8192 cached tokens of 8 heads of 128: 428 us (0.96 PFLOP/s; with one term 364). A pair of
+// tiles takes about 4600 cycles, of which the tensor cores need 3200, and the products of Q and K read shared memory at
 // its full rate. Measured with one term and not taken: half the codes to expand (as two CTAs would share them) 347 us;
 // scores read from TMEM once, the maximum kept per 64 tokens, 369; 64 tokens' scores computed under the other 64's
 // softmax 420, because a product that narrow reads more of shared memory than the tensor cores can wait for. fp16 factors and
@@ -304,16 +304,12 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
     }
     __syncthreads();
 
-    bool ok = true;
-    auto gave_up = [&]() {
-        ok = false;
-        if (lane == 0) atomicOr(a.err, DEVERR_TIMEOUT);
-    };
+    bool ok = true;  // no wait of this warp has given up
     auto wait = [&](uint64_t *b, int parity) {  // all lanes
-        if (ok && !__all_sync(0xffffffffu, mbar_wait_lean<0>(b, parity, WAIT_LIMIT))) gave_up();
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_lean<0>(b, parity, WAIT_LIMIT))) ok = false;
     };
     auto wait_idly = [&](uint64_t *b, int parity, int tiles) {
-        if (ok && !__all_sync(0xffffffffu, mbar_wait_lean<100>(b, parity, WAIT_LIMIT + TILE_LIMIT * tiles))) gave_up();
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_lean<100>(b, parity, WAIT_LIMIT + TILE_LIMIT * tiles))) ok = false;
     };
     // All lanes: the run's next part, in the one of the warp's two places that the current part does not have. Parts
     // stay in shared memory: they are looked at once per item, and registers are short.
@@ -805,6 +801,7 @@ __global__ void __launch_bounds__(NT, 1) kv4_attn_many_kernel(const __grid_const
             }
         }
     }
+    if (!ok && lane == 0) atomicOr(a.err, DEVERR_TIMEOUT);  // said once, not at every wait: 439 -> 428 us
     tc_fence_before();
     __syncthreads();
     if (warp == 12) tmem_dealloc(tbase, 512);
